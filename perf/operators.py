@@ -362,12 +362,13 @@ def _plain_store(s):
     qmax = _QMAX[c["format"]]
     x = s["pool"][s["slots"].long()]
     amax = x.abs().amax(-1, keepdim=True)
+    top = torch.full_like(amax, qmax)        # tensors on both sides: correctly rounded quotients, not products with 1 / x
     zero = amax < _TINY
-    y = torch.where(zero, torch.zeros_like(x), x * (qmax / amax))
+    y = torch.where(zero, torch.zeros_like(x), x * (top / amax))
     y = torch.round(y).clamp(-qmax, qmax).to(torch.int8) if c["format"] == "int8" else y.to(torch.float8_e4m3fn)
     at = s["cache_slots"].long()
     s["codes"].view(torch.int8)[at] = y.view(torch.int8)
-    s["scales"][at] = torch.where(zero, torch.zeros_like(amax), amax / qmax)[..., 0]
+    s["scales"][at] = torch.where(zero, torch.zeros_like(amax), amax / top)[..., 0]
     return s["codes"], s["scales"]
 
 
