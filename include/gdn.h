@@ -428,6 +428,181 @@ gdn_status gdn_bwd_chunk(const void *q, const void *k, const void *v, const floa
                          int B, int T, int Hqk, int Hv, int dk_, int dv_, gdn_dtype dtype,
                          void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Linear attention with a constant decay per head (gdn_decay_*): the recurrence
+ * of the gated delta rule without its delta term, and with one decay constant
+ * per V head instead of a gate per token:
+ *
+ *     S_t = lambda_h S_{t-1} + k_t v_t^T,      o_t = S_t^T q_t.
+ *
+ * Layouts, head map, ownership, streams and errors are those at the top of this
+ * file; instead of alpha and beta there is
+ *   decay     [Hv]     float, lambda_h itself (not its logarithm)
+ * expected in (0, 1]; the kernels clamp log lambda below at -87.  The decay is a
+ * constant of the layer: no gradient with respect to it is computed.
+ * A non-finite q, k or v makes the outputs of its whole chunk of 64 tokens (from
+ * its sequence's start) undefined, and those after it; other sequences and heads
+ * keep their values.
+ */
+
+/*
+ * gdn_decay_fwd -- prefill: T tokens of every (sequence, V head) from S0.
+ *
+ * In:  q, k [B, T, Hqk, dk]; v [B, T, Hv, dv]; decay [Hv]; S0 [B, Hv, dk, dv] or
+ *      NULL (zeros).
+ * Out: o [B, T, Hv, dv]; S_final [B, Hv, dk, dv] or NULL (may be S0).
+ * dtype: GDN_F32 computes in fp32 on CUDA cores; GDN_BF16 on the tensor cores
+ *      with an fp32 state: k's decayed copies enter in three bf16 pieces (the
+ *      24 bits of an fp32), so S_final carries fp32 accuracy; the state that o
+ *      reads enters in two.
+ * With few heads for the device (B * Hv below the number of SMs) each sequence
+ * is cut into up to 16 segments whose states a first launch computes side by
+ * side.  workspace: device scratch of gdn_decay_fwd_workspace(...) bytes for the
+ * current device (0: no segments, may be NULL), 256-byte aligned, owned by the
+ * caller; contents on entry do not matter; calls sharing it must not overlap.
+ * Too small or misaligned: GDN_ERR_INVALID_ARG.
+ * Sizes: as gdn_chunk_fwd (B <= 65535, dk == dv == 128, Hv % Hqk == 0).
+ * Repeated calls return the same bits.
+ */
+size_t gdn_decay_fwd_workspace(int B, int T, int Hv, int dk, int dv, gdn_dtype dtype);
+gdn_status gdn_decay_fwd(const void *q, const void *k, const void *v, const float *decay,
+                         const float *S0, void *o, float *S_final,
+                         int B, int T, int Hqk, int Hv, int dk, int dv,
+                         gdn_dtype dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_decay_fwd_varlen -- gdn_decay_fwd for N sequences packed back to back, with
+ * the table and rules of gdn_chunk_fwd_varlen (cu_seqlens [N + 1] int32 on the
+ * device, offsets clamped into [0, T_total]).  An empty sequence copies its S0
+ * (or zeros) to S_final; token rows that no sequence covers are left as they were.
+ */
+gdn_status gdn_decay_fwd_varlen(const void *q, const void *k, const void *v, const float *decay,
+                                const float *S0, void *o, float *S_final, const int *cu_seqlens,
+                                int N, int T_total, int Hqk, int Hv, int dk, int dv,
+                                gdn_dtype dtype, void *stream);
+
+/*
+ * gdn_decay_decode_step / _slots -- one token for each of B sequences; the
+ * contracts of gdn_decode_step and gdn_decode_step_slots with decay [Hv] in
+ * place of the gates.  S_new may be S; a slot outside [0, n_slots) is a padding
+ * entry (its o row and every state are left as they were); two entries with the
+ * same slot race.
+ */
+gdn_status gdn_decay_decode_step(const void *q, const void *k, const void *v, const float *decay,
+                                 const float *S, void *o, float *S_new,
+                                 int B, int Hqk, int Hv, int dk, int dv,
+                                 gdn_dtype dtype, void *stream);
+gdn_status gdn_decay_decode_step_slots(const void *q, const void *k, const void *v,
+                                       const float *decay, float *state_pool, const int *slots,
+                                       void *o, int B, int n_slots, int Hqk, int Hv, int dk, int dv,
+                                       gdn_dtype dtype, void *stream);
+
+/*
+ * gdn_decay_bwd -- gradients of L = sum_t <dO_t, o_t> + <dS_final, S_T> through
+ * gdn_decay_fwd with respect to q, k, v and S0.  With G_t = dL/dS_t (all of it):
+ *   G_t = q_t dO_t^T + lambda G_{t+1}   (lambda G_{T} read as dS_final),
+ *   dq_t = S_t dO_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,  dS0 = lambda G_0.
+ * dq and dk of a QK head sum over the V heads that read it (in fp32).
+ *
+ * In:  q, k [B, T, Hqk, dk]; v, dO [B, T, Hv, dv], all of dtype; decay [Hv];
+ *      S0, dS_final [B, Hv, dk, dv] fp32 or NULL (zeros).
+ * Out (overwritten): dq, dk [B, T, Hqk, dk] and dv [B, T, Hv, dv] of dtype (the
+ *      inputs' type, rounded once from fp32); dS0 [B, Hv, dk, dv] fp32 or NULL
+ *      (skipped).  Outputs must not overlap inputs or each other, except that
+ *      dS0 may be dS_final.
+ * workspace: gdn_decay_bwd_workspace(...) bytes for the current device, rules as
+ *      for gdn_decay_fwd.  It holds the segments' states and, where QK heads are
+ *      shared, one fp32 row per token and V head.
+ * Sizes, dtypes and errors as gdn_decay_fwd.  No atomics: repeated calls return
+ * the same bits.
+ */
+size_t gdn_decay_bwd_workspace(int B, int T, int Hqk, int Hv, int dk, int dv, gdn_dtype dtype);
+gdn_status gdn_decay_bwd(const void *q, const void *k, const void *v, const float *decay,
+                         const float *S0, const void *dO, const float *dS_final,
+                         void *dq, void *dk, void *dv, float *dS0,
+                         int B, int T, int Hqk, int Hv, int dk_, int dv_,
+                         gdn_dtype dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Verification of a TREE of drafted tokens over a pool of states, and the update
+ * of the states along the accepted path.  gdn_decode_tokens checks a chain of
+ * drafts; a tree checks several continuations in one pass, and reads each state
+ * once without writing any.
+ *
+ * Node i of sequence b continues the state after its parent node, or the cached
+ * state where it has none:
+ *   parents [B, n] int32 (device): parents[b, i] in [0, i) is an earlier node,
+ *           -1 the cached state; any other value makes node i padding, and so
+ *           is every node below a padding node.
+ *   slots   [B] int32 (device): the state of sequence b is state_pool[slots[b]];
+ *           NULL: state_pool[b] (then n_slots >= B).  A slot outside
+ *           [0, n_slots) skips the sequence.
+ * n from 1 to 64 nodes (more: GDN_ERR_UNSUPPORTED).
+ *
+ * gdn_decode_tree / gdn_decay_decode_tree:
+ * In:  q, k [B, n, Hqk, dk]; v [B, n, Hv, dv]; alpha, beta [B, n, Hv] (decay
+ *      rule: decay [Hv]); state_pool [n_slots, Hv, dk, dv], not changed.
+ * Out: o [B, n, Hv, dv], o_i = S_i^T q_i with the state after node i's update.
+ *      Rows of padding nodes and of skipped sequences are left as they were.
+ *      A non-finite input of a node (or a padding node's row) reaches only the
+ *      outputs of that node and the nodes below it, or none.
+ *
+ * gdn_tree_commit / gdn_decay_tree_commit: state_pool[slots[b]] becomes the
+ * state after node accepted[b] ([B] int32, device): the update applied to the
+ * nodes of its path in order.  A value outside [0, n), or a padding node, leaves
+ * the state as it was (nothing accepted).  Two entries with the same slot race.
+ *
+ * Other arguments, alignment and errors as gdn_decode_step_slots.
+ */
+gdn_status gdn_decode_tree(const void *q, const void *k, const void *v,
+                           const float *alpha, const float *beta, const int *parents,
+                           const float *state_pool, const int *slots, void *o,
+                           int B, int n, int n_slots, int Hqk, int Hv, int dk, int dv,
+                           gdn_dtype dtype, void *stream);
+gdn_status gdn_tree_commit(const void *k, const void *v, const float *alpha, const float *beta,
+                           const int *parents, const int *accepted,
+                           float *state_pool, const int *slots,
+                           int B, int n, int n_slots, int Hqk, int Hv, int dk, int dv,
+                           gdn_dtype dtype, void *stream);
+gdn_status gdn_decay_decode_tree(const void *q, const void *k, const void *v, const float *decay,
+                                 const int *parents, const float *state_pool, const int *slots,
+                                 void *o, int B, int n, int n_slots, int Hqk, int Hv, int dk, int dv,
+                                 gdn_dtype dtype, void *stream);
+gdn_status gdn_decay_tree_commit(const void *k, const void *v, const float *decay,
+                                 const int *parents, const int *accepted,
+                                 float *state_pool, const int *slots,
+                                 int B, int n, int n_slots, int Hqk, int Hv, int dk, int dv,
+                                 gdn_dtype dtype, void *stream);
+
+/*
+ * 8-bit state cache: snapshots of states (shared prompt prefixes, swapped-out
+ * sequences) at a quarter of the bytes.  A state row (one key dimension, dv
+ * values) is stored as dv codes and one fp32 scale:
+ *     inv = qmax / amax,  code = round(x * inv),  scale = amax / qmax
+ * with amax the row's largest |x|, qmax 127 (GDN_CODE_INT8) or 448
+ * (GDN_CODE_E4M3), both quotients and the product correctly rounded in fp32 and
+ * codes rounded to the nearest, ties to even.  A row with amax < 1e-30 is stored
+ * as zeros with scale 0; a row with a NaN or an infinity as zero codes with
+ * scale NaN, so that it reads back as NaN.  Reading gives code * scale.
+ *
+ *   codes   [n_cache, Hv, dk, dv] 8-bit;  scales [n_cache, Hv, dk] fp32
+ * Entry i of N moves state_pool[slots[i]] to cache row cache_slots[i]
+ * (gdn_state_store), or back (gdn_state_load); slots and cache_slots are [N]
+ * int32 on the device, and an entry with either index out of range is skipped.
+ * Two entries that write the same row race.  slots, cache_slots 4-byte aligned,
+ * the other pointers 16-byte aligned.
+ */
+typedef enum {
+    GDN_CODE_INT8 = 0,
+    GDN_CODE_E4M3 = 1
+} gdn_code;
+gdn_status gdn_state_store(const float *state_pool, const int *slots, void *codes, float *scales,
+                           const int *cache_slots, int N, int n_slots, int n_cache,
+                           int Hv, int dk, int dv, gdn_code code, void *stream);
+gdn_status gdn_state_load(const void *codes, const float *scales, const int *cache_slots,
+                          float *state_pool, const int *slots, int N, int n_slots, int n_cache,
+                          int Hv, int dk, int dv, gdn_code code, void *stream);
+
 /* Static, NUL-terminated name of a status code. */
 const char *gdn_status_string(gdn_status status);
 

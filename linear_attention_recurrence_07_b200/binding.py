@@ -18,6 +18,7 @@ LIBRARY_PATH = os.path.join(_PKG, "libgdn.so")
 GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA, GDN_ERR_TIMEOUT = 0, 1, 2, 3, 4
 GDN_F32, GDN_BF16 = 0, 1
 _DTYPES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
+_CODES = {torch.int8: 0, torch.float8_e4m3fn: 1}   # gdn_code values
 # gdn_prefill_kernel values
 PREFILL_KERNELS = {"auto": 0, "simt": 1, "tc": 2}
 
@@ -85,6 +86,25 @@ def library():
                                                 I, I, I, I, I, I, I, I,
                                                 ctypes.POINTER(PipelineOptions), vp, ctypes.c_size_t, vp]
         lib.gdn_chunk_fwd_pipelined.restype = I
+        sz = ctypes.c_size_t
+        lib.gdn_decay_fwd_workspace.argtypes = [I, I, I, I, I, I]
+        lib.gdn_decay_fwd_workspace.restype = sz
+        lib.gdn_decay_bwd_workspace.argtypes = [I, I, I, I, I, I, I]
+        lib.gdn_decay_bwd_workspace.restype = sz
+        for name, args in (
+                ("gdn_decay_fwd", [vp] * 7 + [I] * 7 + [vp, sz, vp]),
+                ("gdn_decay_fwd_varlen", [vp] * 8 + [I] * 7 + [vp]),
+                ("gdn_decay_decode_step", [vp] * 7 + [I] * 6 + [vp]),
+                ("gdn_decay_decode_step_slots", [vp] * 7 + [I] * 7 + [vp]),
+                ("gdn_decay_bwd", [vp] * 11 + [I] * 7 + [vp, sz, vp]),
+                ("gdn_decode_tree", [vp] * 9 + [I] * 8 + [vp]),
+                ("gdn_tree_commit", [vp] * 8 + [I] * 8 + [vp]),
+                ("gdn_decay_decode_tree", [vp] * 8 + [I] * 8 + [vp]),
+                ("gdn_decay_tree_commit", [vp] * 7 + [I] * 8 + [vp]),
+                ("gdn_state_store", [vp] * 5 + [I] * 7 + [vp]),
+                ("gdn_state_load", [vp] * 5 + [I] * 7 + [vp])):
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = I
         lib.gdn_device_status.argtypes = [vp]
         lib.gdn_device_status.restype = I
         lib.gdn_status_string.argtypes = [I]
@@ -459,6 +479,274 @@ def gdn_chunk_fwd_pipelined(q, k, v, alpha, beta, S0, o, S_final, chain_ctas=0,
                  _DTYPES[q.dtype], ctypes.byref(opts), _ptr(workspace), workspace.numel(),
                  _stream_handle(stream, dev)),
            "gdn_chunk_fwd_pipelined")
+
+
+def _workspace(workspace, nbytes, dev, stream):
+    """The caller's workspace checked, or one for this call, kept by the allocator until the
+    work on ``stream`` is done."""
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        if stream is not None:
+            workspace.record_stream(stream)
+    elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise GdnError("workspace must be a contiguous uint8 tensor on the inputs' device")
+    return workspace
+
+
+def _shape(t, name, dims):
+    if t is None:
+        raise GdnError(f"{name} is required")
+    if t.dim() != dims:
+        raise GdnError(f"{name}: expected {dims} dimensions, got shape {tuple(t.shape)}")
+    return tuple(t.shape)
+
+
+def decay_fwd_workspace_bytes(B, T, Hv, dtype, dk=128, dv=128):
+    """Device scratch bytes gdn_decay_fwd needs on the current device (C entry point
+    ``gdn_decay_fwd_workspace``); 0 when it cuts no sequence into segments."""
+    return library().gdn_decay_fwd_workspace(B, T, Hv, dk, dv, _DTYPES[dtype])
+
+
+def decay_bwd_workspace_bytes(B, T, Hqk, Hv, dtype, dk=128, dv=128):
+    """Device scratch bytes gdn_decay_bwd needs on the current device (C entry point
+    ``gdn_decay_bwd_workspace``)."""
+    return library().gdn_decay_bwd_workspace(B, T, Hqk, Hv, dk, dv, _DTYPES[dtype])
+
+
+def gdn_decay_fwd(q, k, v, decay, S0, o, S_final, workspace=None, stream=None):
+    """Prefill of linear attention with a constant decay per head (C entry point
+    ``gdn_decay_fwd``); writes o and S_final.
+
+    q, k [B, T, Hqk, dk] and v, o [B, T, Hv, dv] (float32 or bfloat16); decay [Hv]
+    float32; S0, S_final [B, Hv, dk, dv] float32 or None (S_final may be S0).
+    ``workspace``: uint8 CUDA tensor of decay_fwd_workspace_bytes(...) bytes; None
+    allocates one for this call."""
+    B, T, Hqk, dk = _shape(q, "q", 4)
+    _, _, Hv, dv = _shape(v, "v", 4)
+    dev = q.device
+    _expect_cuda(q)
+    for name, t, shape, dt in (("q", q, q.shape, q.dtype), ("k", k, q.shape, q.dtype),
+                               ("v", v, (B, T, Hv, dv), q.dtype), ("o", o, (B, T, Hv, dv), q.dtype),
+                               ("decay", decay, (Hv,), torch.float32)):
+        _expect(t, name, shape, dt, dev)
+    for name, t in (("S0", S0), ("S_final", S_final)):
+        if t is not None:
+            _expect(t, name, (B, Hv, dk, dv), torch.float32, dev)
+    need = _call(dev, library().gdn_decay_fwd_workspace, B, T, Hv, dk, dv, _DTYPES[q.dtype])
+    workspace = _workspace(workspace, need, dev, stream)
+    _check(_call(dev, library().gdn_decay_fwd, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0), _ptr(o),
+                 _ptr(S_final), B, T, Hqk, Hv, dk, dv, _DTYPES[q.dtype], _ptr(workspace),
+                 workspace.numel(), _stream_handle(stream, dev)),
+           "gdn_decay_fwd")
+
+
+def gdn_decay_fwd_varlen(q, k, v, decay, S0, o, S_final, cu_seqlens, stream=None):
+    """gdn_decay_fwd of N packed sequences (C entry point ``gdn_decay_fwd_varlen``).
+    q, k [T_total, Hqk, dk]; v, o [T_total, Hv, dv]; decay [Hv]; cu_seqlens [N + 1]
+    int32; S0, S_final [N, Hv, dk, dv] float32 or None."""
+    T, Hqk, dk = _shape(q, "q", 3)
+    _, Hv, dv = _shape(v, "v", 3)
+    N = _shape(cu_seqlens, "cu_seqlens", 1)[0] - 1
+    if N < 0:
+        raise GdnError("cu_seqlens: at least one entry is required")
+    dev = q.device
+    _expect_cuda(q)
+    for name, t, shape, dt in (("q", q, q.shape, q.dtype), ("k", k, q.shape, q.dtype),
+                               ("v", v, (T, Hv, dv), q.dtype), ("o", o, (T, Hv, dv), q.dtype),
+                               ("decay", decay, (Hv,), torch.float32),
+                               ("cu_seqlens", cu_seqlens, (N + 1,), torch.int32)):
+        _expect(t, name, shape, dt, dev)
+    for name, t in (("S0", S0), ("S_final", S_final)):
+        if t is not None:
+            _expect(t, name, (N, Hv, dk, dv), torch.float32, dev)
+    _check(_call(dev, library().gdn_decay_fwd_varlen, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0),
+                 _ptr(o), _ptr(S_final), _ptr(cu_seqlens), N, T, Hqk, Hv, dk, dv, _DTYPES[q.dtype],
+                 _stream_handle(stream, dev)),
+           "gdn_decay_fwd_varlen")
+
+
+def gdn_decay_decode_step(q, k, v, decay, S, o, S_new, stream=None):
+    """One decode token with a constant decay per head (C entry point
+    ``gdn_decay_decode_step``); writes o and S_new (which may be S).  q, k
+    [B, Hqk, dk]; v, o [B, Hv, dv]; decay [Hv]; S, S_new [B, Hv, dk, dv] float32."""
+    B, Hqk, dk = _shape(q, "q", 3)
+    _, Hv, dv = _shape(v, "v", 3)
+    dev = q.device
+    _expect_cuda(q)
+    for name, t, shape, dt in (("q", q, q.shape, q.dtype), ("k", k, q.shape, q.dtype), ("v", v, (B, Hv, dv), q.dtype),
+                               ("o", o, (B, Hv, dv), q.dtype), ("decay", decay, (Hv,), torch.float32),
+                               ("S", S, (B, Hv, dk, dv), torch.float32),
+                               ("S_new", S_new, (B, Hv, dk, dv), torch.float32)):
+        _expect(t, name, shape, dt, dev)
+    _check(_call(dev, library().gdn_decay_decode_step, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S), _ptr(o),
+                 _ptr(S_new), B, Hqk, Hv, dk, dv, _DTYPES[q.dtype], _stream_handle(stream, dev)),
+           "gdn_decay_decode_step")
+
+
+def gdn_decay_decode_step_slots(q, k, v, decay, state_pool, slots, o, stream=None):
+    """gdn_decay_decode_step with states in a pool, updated in place (C entry point
+    ``gdn_decay_decode_step_slots``): state_pool [n_slots, Hv, dk, dv] float32;
+    slots [B] int32, out of range = padding."""
+    B, Hqk, dk = _shape(q, "q", 3)
+    _, Hv, dv = _shape(v, "v", 3)
+    n_slots = _shape(state_pool, "state_pool", 4)[0]
+    dev = q.device
+    _expect_cuda(q)
+    for name, t, shape, dt in (("q", q, q.shape, q.dtype), ("k", k, q.shape, q.dtype), ("v", v, (B, Hv, dv), q.dtype),
+                               ("o", o, (B, Hv, dv), q.dtype), ("decay", decay, (Hv,), torch.float32),
+                               ("state_pool", state_pool, (n_slots, Hv, dk, dv), torch.float32),
+                               ("slots", slots, (B,), torch.int32)):
+        _expect(t, name, shape, dt, dev)
+    _check(_call(dev, library().gdn_decay_decode_step_slots, _ptr(q), _ptr(k), _ptr(v), _ptr(decay),
+                 _ptr(state_pool), _ptr(slots), _ptr(o), B, n_slots, Hqk, Hv, dk, dv, _DTYPES[q.dtype],
+                 _stream_handle(stream, dev)),
+           "gdn_decay_decode_step_slots")
+
+
+def gdn_decay_bwd(q, k, v, decay, S0, dO, dS_final, dq, dk, dv, dS0, workspace=None, stream=None):
+    """Gradients of sum <dO, o> + <dS_final, S_final> through gdn_decay_fwd (C entry
+    point ``gdn_decay_bwd``).  q, k, v, dO of one dtype (float32 or bfloat16); S0,
+    dS_final float32 or None.  Outputs (overwritten): dq, dk, dv like q, k, v, in their
+    dtype; dS0 [B, Hv, dk, dv] float32 or None.  ``workspace``: uint8 CUDA tensor of
+    decay_bwd_workspace_bytes(...) bytes; None allocates one."""
+    B, T, Hqk, dkk = _shape(q, "q", 4)
+    _, _, Hv, dvv = _shape(v, "v", 4)
+    dev = q.device
+    _expect_cuda(q)
+    for name, t, shape, dt in (("q", q, q.shape, q.dtype), ("k", k, q.shape, q.dtype),
+                               ("v", v, (B, T, Hv, dvv), q.dtype), ("dO", dO, (B, T, Hv, dvv), q.dtype),
+                               ("dq", dq, q.shape, q.dtype), ("dk", dk, q.shape, q.dtype),
+                               ("dv", dv, (B, T, Hv, dvv), q.dtype), ("decay", decay, (Hv,), torch.float32)):
+        _expect(t, name, shape, dt, dev)
+    for name, t in (("S0", S0), ("dS_final", dS_final), ("dS0", dS0)):
+        if t is not None:
+            _expect(t, name, (B, Hv, dkk, dvv), torch.float32, dev)
+    need = _call(dev, library().gdn_decay_bwd_workspace, B, T, Hqk, Hv, dkk, dvv, _DTYPES[q.dtype])
+    workspace = _workspace(workspace, need, dev, stream)
+    _check(_call(dev, library().gdn_decay_bwd, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0), _ptr(dO),
+                 _ptr(dS_final), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dS0), B, T, Hqk, Hv, dkk, dvv,
+                 _DTYPES[q.dtype], _ptr(workspace), workspace.numel(), _stream_handle(stream, dev)),
+           "gdn_decay_bwd")
+
+
+def _tree_sizes(k, v, parents, state_pool, slots, dtype_of):
+    B, n, Hqk, dk = _shape(k, "k", 4)
+    _, _, Hv, dv = _shape(v, "v", 4)
+    n_slots = _shape(state_pool, "state_pool", 4)[0]
+    dev = k.device
+    _expect_cuda(k)
+    for name, t, shape, dt in (("k", k, k.shape, dtype_of), ("v", v, (B, n, Hv, dv), dtype_of),
+                               ("parents", parents, (B, n), torch.int32),
+                               ("state_pool", state_pool, (n_slots, Hv, dk, dv), torch.float32)):
+        _expect(t, name, shape, dt, dev)
+    if slots is not None:
+        _expect(slots, "slots", (B,), torch.int32, dev)
+    return B, n, n_slots, Hqk, Hv, dk, dv
+
+
+def _gates(alpha, beta, B, n, Hv, dev):
+    _expect(alpha, "alpha", (B, n, Hv), torch.float32, dev)
+    _expect(beta, "beta", (B, n, Hv), torch.float32, dev)
+
+
+def gdn_decode_tree(q, k, v, alpha, beta, parents, state_pool, slots, o, stream=None):
+    """Outputs of trees of drafted tokens (C entry point ``gdn_decode_tree``): node i
+    of sequence b continues node parents[b, i] < i, or the state state_pool[slots[b]]
+    where that is -1; any other parent marks padding, whose o rows stay as they were.
+
+    q, k [B, n, Hqk, dk]; v, o [B, n, Hv, dv]; alpha, beta [B, n, Hv] float32;
+    parents [B, n] int32; state_pool [n_slots, Hv, dk, dv] float32 (not changed);
+    slots [B] int32 or None (sequence b uses row b).  n <= 64."""
+    B, n, n_slots, Hqk, Hv, dk, dv = _tree_sizes(k, v, parents, state_pool, slots, q.dtype)
+    dev = k.device
+    _expect(q, "q", k.shape, k.dtype, dev)
+    _expect(o, "o", v.shape, v.dtype, dev)
+    _gates(alpha, beta, B, n, Hv, dev)
+    _check(_call(dev, library().gdn_decode_tree, _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(parents),
+                 _ptr(state_pool), _ptr(slots), _ptr(o), B, n, n_slots, Hqk, Hv, dk, dv, _DTYPES[k.dtype],
+                 _stream_handle(stream, dev)),
+           "gdn_decode_tree")
+
+
+def gdn_tree_commit(k, v, alpha, beta, parents, accepted, state_pool, slots, stream=None):
+    """Moves state_pool[slots[b]] to the state after node accepted[b] of its tree, in
+    place (C entry point ``gdn_tree_commit``); accepted [B] int32, out of range =
+    nothing accepted.  Other arguments as gdn_decode_tree."""
+    B, n, n_slots, Hqk, Hv, dk, dv = _tree_sizes(k, v, parents, state_pool, slots, k.dtype)
+    dev = k.device
+    _gates(alpha, beta, B, n, Hv, dev)
+    _expect(accepted, "accepted", (B,), torch.int32, dev)
+    _check(_call(dev, library().gdn_tree_commit, _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(parents),
+                 _ptr(accepted), _ptr(state_pool), _ptr(slots), B, n, n_slots, Hqk, Hv, dk, dv, _DTYPES[k.dtype],
+                 _stream_handle(stream, dev)),
+           "gdn_tree_commit")
+
+
+def gdn_decay_decode_tree(q, k, v, decay, parents, state_pool, slots, o, stream=None):
+    """gdn_decode_tree for the constant-decay rule (C entry point
+    ``gdn_decay_decode_tree``): decay [Hv] float32 in place of the gates."""
+    B, n, n_slots, Hqk, Hv, dk, dv = _tree_sizes(k, v, parents, state_pool, slots, q.dtype)
+    dev = k.device
+    _expect(q, "q", k.shape, k.dtype, dev)
+    _expect(o, "o", v.shape, v.dtype, dev)
+    _expect(decay, "decay", (Hv,), torch.float32, dev)
+    _check(_call(dev, library().gdn_decay_decode_tree, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(parents),
+                 _ptr(state_pool), _ptr(slots), _ptr(o), B, n, n_slots, Hqk, Hv, dk, dv, _DTYPES[k.dtype],
+                 _stream_handle(stream, dev)),
+           "gdn_decay_decode_tree")
+
+
+def gdn_decay_tree_commit(k, v, decay, parents, accepted, state_pool, slots, stream=None):
+    """gdn_tree_commit for the constant-decay rule (C entry point
+    ``gdn_decay_tree_commit``)."""
+    B, n, n_slots, Hqk, Hv, dk, dv = _tree_sizes(k, v, parents, state_pool, slots, k.dtype)
+    dev = k.device
+    _expect(decay, "decay", (Hv,), torch.float32, dev)
+    _expect(accepted, "accepted", (B,), torch.int32, dev)
+    _check(_call(dev, library().gdn_decay_tree_commit, _ptr(k), _ptr(v), _ptr(decay), _ptr(parents), _ptr(accepted),
+                 _ptr(state_pool), _ptr(slots), B, n, n_slots, Hqk, Hv, dk, dv, _DTYPES[k.dtype],
+                 _stream_handle(stream, dev)),
+           "gdn_decay_tree_commit")
+
+
+def _cache_sizes(state_pool, slots, codes, scales, cache_slots):
+    n_slots, Hv, dk, dv = _shape(state_pool, "state_pool", 4)
+    n_cache = _shape(codes, "codes", 4)[0]
+    N = _shape(slots, "slots", 1)[0]
+    dev = state_pool.device
+    if dev.type != "cuda":
+        raise GdnError(f"tensors must be on a CUDA device, got {dev}")
+    if codes.dtype not in _CODES:
+        raise GdnError(f"codes: expected torch.int8 or torch.float8_e4m3fn, got {codes.dtype}")
+    for name, t, shape, dt in (("state_pool", state_pool, state_pool.shape, torch.float32),
+                               ("codes", codes, (n_cache, Hv, dk, dv), codes.dtype),
+                               ("scales", scales, (n_cache, Hv, dk), torch.float32),
+                               ("slots", slots, (N,), torch.int32), ("cache_slots", cache_slots, (N,), torch.int32)):
+        _expect(t, name, shape, dt, dev)
+    return N, n_slots, n_cache, Hv, dk, dv, _CODES[codes.dtype]
+
+
+def gdn_state_store(state_pool, slots, codes, scales, cache_slots, stream=None):
+    """Snapshots of pool states as 8-bit codes with one scale per key row (C entry
+    point ``gdn_state_store``): row cache_slots[i] of the cache gets
+    state_pool[slots[i]].  state_pool [n_slots, Hv, dk, dv] float32; codes
+    [n_cache, Hv, dk, dv] int8 or float8_e4m3fn; scales [n_cache, Hv, dk] float32;
+    slots, cache_slots [N] int32, out of range = skipped."""
+    sizes = _cache_sizes(state_pool, slots, codes, scales, cache_slots)
+    dev = state_pool.device
+    _check(_call(dev, library().gdn_state_store, _ptr(state_pool), _ptr(slots), _ptr(codes), _ptr(scales),
+                 _ptr(cache_slots), *sizes, _stream_handle(stream, dev)),
+           "gdn_state_store")
+
+
+def gdn_state_load(codes, scales, cache_slots, state_pool, slots, stream=None):
+    """Brings snapshots back (C entry point ``gdn_state_load``): state_pool[slots[i]] =
+    codes * scales of cache row cache_slots[i].  Arguments as gdn_state_store."""
+    sizes = _cache_sizes(state_pool, slots, codes, scales, cache_slots)
+    dev = state_pool.device
+    _check(_call(dev, library().gdn_state_load, _ptr(codes), _ptr(scales), _ptr(cache_slots), _ptr(state_pool),
+                 _ptr(slots), *sizes, _stream_handle(stream, dev)),
+           "gdn_state_load")
 
 
 def device_status(stream=None, device=None):

@@ -1,0 +1,69 @@
+// Shared by the walks of the decay recurrence (CUDA cores and tensor cores): where a
+// CTA's tokens, start state and end state are, and the powers of its head's decay.
+#pragma once
+
+#include "gdn_internal.cuh"
+
+namespace gdn {
+namespace {
+
+// lambda^e for integer e >= 0, with log lambda >= -87; computed in 64 bits, because a
+// power is applied once per chunk and its relative error adds up over the chunks.
+__device__ __forceinline__ double decay_log(float lam) { return fmax(log((double)lam), -87.0); }
+__device__ __forceinline__ double decay_pow(double loglam, double e) { return exp(e * loglam); }
+
+// What one CTA of a walk does.  Chunk c of the walk (c0 <= c < c1) holds token rows
+// tb + 64 m .. of batch row bt, m = c forwards and nchunks - 1 - c backwards.
+struct WalkSpan {
+    int bt, tb, L;         // batch row, first token row, tokens of the sequence
+    int nchunks;           // chunks of the whole sequence
+    int c0, c1;            // this CTA's chunks
+    int b, seg;            // sequence, segment
+    bool copy_init;        // first launch, segment 0: only carry the start state over
+};
+
+__device__ __forceinline__ int chunk_rows(const WalkSpan &s, bool rev, int c, int &t0)
+{
+    const int m = rev ? s.nchunks - 1 - c : c;
+    t0 = s.tb + m * kChunk;
+    return min(kChunk, s.L - m * kChunk);
+}
+
+// y: index over sequences x segments.  state_only: the first launch of a segmented walk.
+__device__ __forceinline__ WalkSpan walk_span(const DecayWalk &w, int y, bool state_only)
+{
+    WalkSpan s;
+    s.copy_init = false;
+    if (w.cu_seqlens) {
+        const int a = min(max(w.cu_seqlens[y], 0), w.T);
+        const int e = min(max(w.cu_seqlens[y + 1], a), w.T);
+        s.b = y; s.seg = 0; s.bt = 0; s.tb = a; s.L = e - a;
+        s.nchunks = (s.L + kChunk - 1) / kChunk;
+        s.c0 = 0; s.c1 = s.nchunks;
+        return s;
+    }
+    s.b = y / w.nseg;
+    s.seg = y - s.b * w.nseg;
+    s.bt = s.b; s.tb = 0; s.L = w.T;
+    s.nchunks = (w.T + kChunk - 1) / kChunk;
+    if (state_only) {
+        s.copy_init = s.seg == 0;
+        s.c0 = (s.seg - 1) * w.seg_chunks;
+        s.c1 = s.copy_init ? s.c0 : s.c0 + w.seg_chunks;
+    } else {
+        s.c0 = s.seg * w.seg_chunks;
+        s.c1 = s.seg == w.nseg - 1 ? s.nchunks : s.c0 + w.seg_chunks;
+    }
+    return s;
+}
+
+// Tokens that the walk has passed before chunk c.
+__device__ __forceinline__ int tokens_before(const WalkSpan &s, bool rev, int c)
+{
+    if (c >= s.nchunks) return s.L;
+    if (!rev) return c * kChunk;
+    return c == 0 ? 0 : s.L - (s.nchunks - c) * kChunk;   // backwards the ragged chunk comes first
+}
+
+}  // namespace
+}  // namespace gdn

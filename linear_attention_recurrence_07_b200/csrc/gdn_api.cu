@@ -86,6 +86,8 @@ gdn_status chunk_fwd_common(const void *q, const void *k, const void *v,
 
 }  // namespace
 
+gdn_status gdn::launch_status(cudaError_t err) { return cuda_status(err); }
+
 extern "C" {
 
 gdn_status gdn_chunk_fwd(const void *q, const void *k, const void *v,

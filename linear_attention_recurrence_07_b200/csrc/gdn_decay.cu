@@ -1,0 +1,272 @@
+// Linear attention with a constant decay per head, chunk by chunk on CUDA cores in
+// fp32 (the path of fp32 inputs; see DecayWalk for the walk that prefill and all
+// gradients share).
+//
+// Per chunk of L <= 64 tokens, with H the state at its start (decayed to its first
+// token), p_i = i forwards and L - 1 - i backwards (tokens since the start):
+//   P_ij = lambda^{|i - j|} x_i . y_j   for j at or before i in the walk, else 0
+//   o_i  = lambda^{p_i} H^T x_i + sum_j P_ij z_j
+//   H   <- lambda^L H + sum_j lambda^{L - p_j} y_j z_j^T
+// (a prefill's last chunk uses one power less throughout, so that S_final is not
+// decayed past its last token).  The powers come from a table computed in 64 bits,
+// and lambda^L enters the state as a sum of two floats: its rounding would add up
+// over hundreds of chunks of a slowly decaying head.
+//
+// A CTA owns 32 columns of one head's state and output: with four CTAs per head the
+// score tile is computed four times (it is a quarter of the work), and short
+// prompts of few heads still spread over the device.  Everything sits in shared
+// memory, 4 x 4 register tiles per thread.
+#include "decay_common.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kSimtThreads = 256;
+constexpr int kDz = 32;                      // columns of the state per CTA
+constexpr int kZSlices = kHeadDim / kDz;
+constexpr int kLdX = kHeadDim + 4;           // padded rows
+constexpr int kLdP = kChunk + 4;
+constexpr int kLdZ = kDz + 4;
+
+struct SimtSmem {
+    float x[kChunk][kLdX], y[kChunk][kLdX];
+    float z[kChunk][kLdZ];
+    float H[kHeadDim][kLdZ];
+    float P[kChunk][kLdP];
+    float pw[kChunk + 1];                    // lambda^0 .. lambda^64
+};
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T *p);
+template <> __device__ __forceinline__ float4 load4<float>(const float *p) {
+    return *reinterpret_cast<const float4 *>(p);
+}
+template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kSimtThreads)
+decay_walk_kernel(const DecayWalk w, bool state_only)
+{
+    extern __shared__ __align__(16) unsigned char raw[];
+    SimtSmem &sm = *reinterpret_cast<SimtSmem *>(raw);
+    const int tid = threadIdx.x;
+    const int h = blockIdx.x / kZSlices, z0 = (blockIdx.x - h * kZSlices) * kDz;
+    const WalkSpan sp = walk_span(w, blockIdx.y, state_only);
+    const size_t st = (size_t)kHeadDim * kHeadDim;
+    const double loglam = decay_log(w.decay[h]);
+
+    if (tid <= kChunk) sm.pw[tid] = (float)decay_pow(loglam, tid);
+    // ---- start state
+    if (w.nseg > 1 && !state_only) {
+        const int here = tokens_before(sp, w.rev, sp.c0);
+        for (int i = tid; i < kHeadDim * (kDz / 4); i += kSimtThreads) {
+            const int d = i >> 3, c = (i & 7) * 4;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int g = 0; g <= sp.seg; ++g) {          // entry g holds the walk up to segment g's start
+                const float f = (float)decay_pow(loglam, here - tokens_before(sp, w.rev, g * w.seg_chunks));
+                const float4 v = *reinterpret_cast<const float4 *>(
+                    w.seg + (((size_t)sp.b * w.nseg + g) * w.Hv + h) * st + (size_t)d * kHeadDim + z0 + c);
+                a.x = fmaf(f, v.x, a.x); a.y = fmaf(f, v.y, a.y);
+                a.z = fmaf(f, v.z, a.z); a.w = fmaf(f, v.w, a.w);
+            }
+            *reinterpret_cast<float4 *>(&sm.H[d][c]) = a;
+        }
+    } else {
+        const float *src = (w.init && (!state_only || sp.copy_init)) ? w.init + ((size_t)sp.b * w.Hv + h) * st : nullptr;
+        const float f = (w.init_decays && sp.L > 0) ? (float)decay_pow(loglam, 1.0) : 1.f;
+        for (int i = tid; i < kHeadDim * kDz; i += kSimtThreads) {
+            const int d = w.init_trans ? (i & (kHeadDim - 1)) : i / kDz;
+            const int c = w.init_trans ? i / kHeadDim : i % kDz;
+            const size_t at = w.init_trans ? (size_t)(z0 + c) * kHeadDim + d : (size_t)d * kHeadDim + z0 + c;
+            sm.H[d][c] = src ? f * src[at] : 0.f;
+        }
+    }
+    __syncthreads();
+
+    const T *x = static_cast<const T *>(w.x), *y = static_cast<const T *>(w.y), *z = static_cast<const T *>(w.z);
+    const int xh = h / (w.Hv / w.hx), yh = h / (w.Hv / w.hy), zh = h / (w.Hv / w.hz);
+    const int ti = tid >> 4, tj = tid & 15;      // 16 x 16 threads
+    for (int c = sp.c0; c < sp.c1; ++c) {
+        int t0;
+        const int L = chunk_rows(sp, w.rev, c, t0);
+        const size_t tok = (size_t)sp.bt * w.T + t0;
+        for (int i = tid; i < kChunk * (kHeadDim / 4); i += kSimtThreads) {
+            const int r = i >> 5, d = (i & 31) * 4;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+            if (r < L) {
+                if (!state_only) a = load4(x + ((tok + r) * w.hx + xh) * kHeadDim + d);
+                b = load4(y + ((tok + r) * w.hy + yh) * kHeadDim + d);
+            }
+            *reinterpret_cast<float4 *>(&sm.x[r][d]) = a;
+            *reinterpret_cast<float4 *>(&sm.y[r][d]) = b;
+        }
+        for (int i = tid; i < kChunk * (kDz / 4); i += kSimtThreads) {
+            const int r = i >> 3, d = (i & 7) * 4;
+            *reinterpret_cast<float4 *>(&sm.z[r][d]) =
+                r < L ? load4(z + ((tok + r) * w.hz + zh) * kHeadDim + z0 + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        __syncthreads();
+        if (!state_only) {
+            // ---- P: rows ti + 16 a, columns tj + 16 b
+            float p[4][4] = {};
+            for (int d = 0; d < kHeadDim; d += 4) {
+                float4 xv[4], yv[4];
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    xv[a] = *reinterpret_cast<const float4 *>(&sm.x[ti + 16 * a][d]);
+                    yv[a] = *reinterpret_cast<const float4 *>(&sm.y[tj + 16 * a][d]);
+                }
+#pragma unroll
+                for (int a = 0; a < 4; ++a)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        p[a][b] = fmaf(xv[a].x, yv[b].x, p[a][b]);
+                        p[a][b] = fmaf(xv[a].y, yv[b].y, p[a][b]);
+                        p[a][b] = fmaf(xv[a].z, yv[b].z, p[a][b]);
+                        p[a][b] = fmaf(xv[a].w, yv[b].w, p[a][b]);
+                    }
+            }
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const int i = ti + 16 * a, j = tj + 16 * b;
+                    const int e = w.rev ? j - i : i - j;
+                    sm.P[i][j] = e >= 0 ? sm.pw[max(e, 0)] * p[a][b] : 0.f;
+                }
+            __syncthreads();
+            // ---- o: rows r, r + 32, four columns
+            const int r = tid >> 3, cc = (tid & 7) * 4;
+            float acc[2][4] = {}, dia[2][4] = {};
+            for (int d = 0; d < kHeadDim; ++d) {
+                const float4 hv = *reinterpret_cast<const float4 *>(&sm.H[d][cc]);
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    const float xv = sm.x[r + 32 * a][d];
+                    acc[a][0] = fmaf(xv, hv.x, acc[a][0]); acc[a][1] = fmaf(xv, hv.y, acc[a][1]);
+                    acc[a][2] = fmaf(xv, hv.z, acc[a][2]); acc[a][3] = fmaf(xv, hv.w, acc[a][3]);
+                }
+            }
+            for (int j = 0; j < L; ++j) {
+                const float4 zv = *reinterpret_cast<const float4 *>(&sm.z[j][cc]);
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    const float pv = sm.P[r + 32 * a][j];
+                    dia[a][0] = fmaf(pv, zv.x, dia[a][0]); dia[a][1] = fmaf(pv, zv.y, dia[a][1]);
+                    dia[a][2] = fmaf(pv, zv.z, dia[a][2]); dia[a][3] = fmaf(pv, zv.w, dia[a][3]);
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                const int i = r + 32 * a;
+                if (i >= L) continue;
+                const float f = sm.pw[w.rev ? L - 1 - i : i];
+                const size_t at = ((tok + i) * w.Hv + h) * kHeadDim + z0 + cc;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v = fmaf(f, acc[a][e], dia[a][e]);
+                    if (w.o_f32) static_cast<float *>(w.o)[at + e] = v;
+                    else static_cast<T *>(w.o)[at + e] = from_f32<T>(v);
+                }
+            }
+            __syncthreads();
+        }
+        // ---- H: rows d0 .. d0 + 3, columns 4 (tid & 7) ..
+        {
+            const int back = (w.fin_back && !state_only && c == sp.nchunks - 1) ? 1 : 0;
+            const double pl = decay_pow(loglam, L - back);
+            const float hi = (float)pl, lo = (float)(pl - (double)hi);
+            const int d0 = (tid >> 3) * 4, cc = (tid & 7) * 4;
+            float acc[4][4] = {};
+            for (int j = 0; j < L; ++j) {
+                const float f = sm.pw[(w.rev ? j + 1 : L - j) - back];
+                const float4 yv = *reinterpret_cast<const float4 *>(&sm.y[j][d0]);
+                const float4 zv = *reinterpret_cast<const float4 *>(&sm.z[j][cc]);
+                const float yy[4] = {f * yv.x, f * yv.y, f * yv.z, f * yv.w};
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    acc[a][0] = fmaf(yy[a], zv.x, acc[a][0]); acc[a][1] = fmaf(yy[a], zv.y, acc[a][1]);
+                    acc[a][2] = fmaf(yy[a], zv.z, acc[a][2]); acc[a][3] = fmaf(yy[a], zv.w, acc[a][3]);
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float &hv = sm.H[d0 + a][cc + e];
+                    hv = fmaf(hi, hv, fmaf(lo, hv, acc[a][e]));
+                }
+        }
+        __syncthreads();
+    }
+    // ---- end state
+    float *dst = nullptr;
+    if (state_only) dst = w.seg + (((size_t)sp.b * w.nseg + sp.seg) * w.Hv + h) * st;
+    else if (w.fin && sp.c1 == sp.nchunks) dst = w.fin + ((size_t)sp.b * w.Hv + h) * st;
+    if (dst)
+        for (int i = tid; i < kHeadDim * (kDz / 4); i += kSimtThreads) {
+            const int d = i >> 3, cc = (i & 7) * 4;
+            *reinterpret_cast<float4 *>(dst + (size_t)d * kHeadDim + z0 + cc) =
+                *reinterpret_cast<const float4 *>(&sm.H[d][cc]);
+        }
+}
+
+template <typename T>
+cudaError_t launch_typed(const DecayWalk &w, cudaStream_t stream)
+{
+    cudaError_t err = cudaFuncSetAttribute(decay_walk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)sizeof(SimtSmem));
+    if (err != cudaSuccess) return err;
+    const dim3 grid((unsigned)w.Hv * kZSlices, (unsigned)(w.B * w.nseg));
+    if (w.nseg > 1) {
+        decay_walk_kernel<T><<<grid, kSimtThreads, sizeof(SimtSmem), stream>>>(w, true);
+        if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    }
+    decay_walk_kernel<T><<<grid, kSimtThreads, sizeof(SimtSmem), stream>>>(w, false);
+    return cudaGetLastError();
+}
+
+// One thread per four columns of an output row.
+template <typename T>
+__global__ void __launch_bounds__(256)
+head_sum_kernel(const float *__restrict__ part, T *__restrict__ out, long long n4, int Hqk, int G)
+{
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n4; i += (long long)gridDim.x * 256) {
+        const long long row = i >> 5;                    // token * Hqk + head
+        const int d = (int)(i & 31) * 4;
+        const float *p = part + row * G * kHeadDim + d;  // V heads of a QK head are contiguous
+        float4 a = __ldcs(reinterpret_cast<const float4 *>(p));
+        for (int g = 1; g < G; ++g) {
+            const float4 b = __ldcs(reinterpret_cast<const float4 *>(p + (size_t)g * kHeadDim));
+            a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+        }
+        T *dst = out + row * kHeadDim + d;
+        dst[0] = from_f32<T>(a.x); dst[1] = from_f32<T>(a.y);
+        dst[2] = from_f32<T>(a.z); dst[3] = from_f32<T>(a.w);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_decay_walk_simt(const DecayWalk &w, gdn_dtype dtype, cudaStream_t stream)
+{
+    return dtype == GDN_BF16 ? launch_typed<__nv_bfloat16>(w, stream) : launch_typed<float>(w, stream);
+}
+
+cudaError_t launch_head_sum(const float *part, void *out, long long rows, int Hqk, int Hv, gdn_dtype dtype,
+                            cudaStream_t stream)
+{
+    const long long n4 = rows * Hqk * (kHeadDim / 4);
+    const unsigned grid = (unsigned)((n4 + 255) / 256 < 148 * 16 ? (n4 + 255) / 256 : 148 * 16);
+    if (dtype == GDN_BF16)
+        head_sum_kernel<<<grid, 256, 0, stream>>>(part, (__nv_bfloat16 *)out, n4, Hqk, Hv / Hqk);
+    else
+        head_sum_kernel<<<grid, 256, 0, stream>>>(part, (float *)out, n4, Hqk, Hv / Hqk);
+    return cudaGetLastError();
+}
+
+}  // namespace gdn

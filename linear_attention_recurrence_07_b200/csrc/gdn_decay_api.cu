@@ -1,0 +1,339 @@
+// C ABI of the constant-decay linear attention, the draft trees and the 8-bit state
+// cache: argument checks and dispatch.  See include/gdn.h.
+#include "gdn_internal.cuh"
+
+namespace {
+
+using gdn::DecayWalk;
+using gdn::launch_status;
+
+bool misaligned(const void *p, uintptr_t to) { return p && (reinterpret_cast<uintptr_t>(p) & (to - 1)); }
+
+gdn_status check_sizes(int Hqk, int Hv, int dk, int dv)
+{
+    if (Hqk <= 0 || Hv <= 0 || dk <= 0 || dv <= 0) return GDN_ERR_INVALID_ARG;
+    if (Hv % Hqk != 0 || dk != gdn::kHeadDim || dv != gdn::kHeadDim) return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+bool is_dtype(gdn_dtype d) { return d == GDN_F32 || d == GDN_BF16; }
+
+int sm_count()
+{
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 148;
+    }
+    return sms;
+}
+
+constexpr size_t kStateBytes = (size_t)gdn::kHeadDim * gdn::kHeadDim * sizeof(float);
+constexpr int kMaxDecaySegments = 16;
+constexpr int kMinSegmentChunks = 4;
+
+// Segments of a dense walk: as many as fill the device with one CTA (fp32: one head's
+// four half-SM CTAs) per head and segment, of at least four chunks, because the launch
+// that computes their start states reads y and z once more.
+void choose_segments(DecayWalk &w, gdn_dtype dtype)
+{
+    const int nchunks = (w.T + gdn::kChunk - 1) / gdn::kChunk;
+    const long long units = (long long)w.B * w.Hv * (dtype == GDN_F32 ? 2 : 1);
+    long long n = sm_count() / units;
+    if (n > kMaxDecaySegments) n = kMaxDecaySegments;
+    if (n < 1) n = 1;
+    int per = (int)((nchunks + n - 1) / n);
+    if (per < kMinSegmentChunks) per = kMinSegmentChunks;
+    w.seg_chunks = per;
+    w.nseg = (nchunks + per - 1) / per;
+    if (w.nseg < 1) w.nseg = 1;
+}
+size_t segment_bytes(const DecayWalk &w)
+{
+    return w.nseg > 1 ? (size_t)w.B * w.nseg * w.Hv * kStateBytes : 0;
+}
+
+cudaError_t launch_walk(const DecayWalk &w, gdn_dtype dtype, cudaStream_t s)
+{
+    return gdn::launch_decay_walk_simt(w, dtype, s);
+}
+
+// T == 0: the state passes through.
+gdn_status pass_state(float *dst, const float *src, int B, int Hv, cudaStream_t s)
+{
+    if (!dst || dst == src) return GDN_OK;
+    const size_t bytes = (size_t)B * Hv * kStateBytes;
+    return launch_status(src ? cudaMemcpyAsync(dst, src, bytes, cudaMemcpyDeviceToDevice, s)
+                             : cudaMemsetAsync(dst, 0, bytes, s));
+}
+
+gdn_status fwd_common(const void *q, const void *k, const void *v, const float *decay, const float *S0, void *o,
+                      float *S_final, const int *cu, int B, int T, int Hqk, int Hv, int dk, int dv, gdn_dtype dtype,
+                      void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (B < 0 || T < 0 || !is_dtype(dtype)) return GDN_ERR_INVALID_ARG;
+    gdn_status st = check_sizes(Hqk, Hv, dk, dv);
+    if (st != GDN_OK) return st;
+    if (B > 65535 || Hv > 65535) return GDN_ERR_UNSUPPORTED;
+    if (B == 0) return GDN_OK;
+    const void *ptrs[] = {q, k, v, decay, S0, o, S_final};
+    for (const void *p : ptrs)
+        if (misaligned(p, 16)) return GDN_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 0) return pass_state(S_final, S0, B, Hv, s);
+    if (!q || !k || !v || !decay || !o) return GDN_ERR_INVALID_ARG;
+    DecayWalk w{};
+    w.x = q; w.y = k; w.z = v;
+    w.hx = w.hy = Hqk; w.hz = Hv;
+    w.o = o;
+    w.decay = decay;
+    w.init = S0;
+    w.init_decays = true;
+    w.fin = S_final;
+    w.fin_back = true;
+    w.B = B; w.T = T; w.Hv = Hv;
+    w.cu_seqlens = cu;
+    w.nseg = 1;
+    w.seg_chunks = (T + gdn::kChunk - 1) / gdn::kChunk;
+    if (!cu) {
+        choose_segments(w, dtype);
+        const size_t need = segment_bytes(w);
+        if (need > 0) {
+            if (!workspace || workspace_bytes < need || misaligned(workspace, 256)) return GDN_ERR_INVALID_ARG;
+            w.seg = static_cast<float *>(workspace);
+        }
+    }
+    return launch_status(launch_walk(w, dtype, s));
+}
+
+gdn_status check_token_op(int B, int Hqk, int Hv, int dk, int dv, gdn_dtype dtype, long long ctas_per_head)
+{
+    if (B < 0 || !is_dtype(dtype)) return GDN_ERR_INVALID_ARG;
+    gdn_status st = check_sizes(Hqk, Hv, dk, dv);
+    if (st != GDN_OK) return st;
+    return (long long)B * Hv * ctas_per_head > 0x7fffffffLL ? GDN_ERR_UNSUPPORTED : GDN_OK;
+}
+
+gdn_status decode_common(const void *q, const void *k, const void *v, const float *decay, const float *S, void *o,
+                         float *S_new, const int *slots, int B, int n_slots, int Hqk, int Hv, int dk, int dv,
+                         gdn_dtype dtype, void *stream)
+{
+    gdn_status st = check_token_op(B, Hqk, Hv, dk, dv, dtype, 4);
+    if (st != GDN_OK) return st;
+    if (B == 0) return GDN_OK;
+    const bool states = n_slots > 0 || !slots;
+    if (!q || !k || !v || !decay || !o || (states && (!S || !S_new))) return GDN_ERR_INVALID_ARG;
+    const void *ptrs[] = {q, k, v, decay, S, o, S_new};
+    for (const void *p : ptrs)
+        if (misaligned(p, 16)) return GDN_ERR_INVALID_ARG;
+    if (misaligned(slots, 4)) return GDN_ERR_INVALID_ARG;
+    gdn::DecayDecodeArgs a{q, k, v, decay, S, o, S_new, B, Hqk, Hv, slots, n_slots};
+    return launch_status(gdn::launch_decay_decode(a, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+// q, o null for the commit, accepted null for the verification; alpha and beta, or decay.
+gdn_status tree_common(gdn::TreeArgs a, bool commit, int dk, int dv, gdn_dtype dtype, void *stream)
+{
+    gdn_status st = check_token_op(a.B, a.Hqk, a.Hv, dk, dv, dtype, 1);
+    if (st != GDN_OK) return st;
+    if (a.n < 1 || a.n_slots < 0) return GDN_ERR_INVALID_ARG;
+    if (a.n > gdn::kMaxTreeNodes) return GDN_ERR_UNSUPPORTED;
+    if (a.B == 0) return GDN_OK;
+    if (!a.k || !a.v || !a.parents || (commit ? !a.accepted : (!a.q || !a.o))) return GDN_ERR_INVALID_ARG;
+    if (a.n_slots > 0 && !(commit ? a.pool_out : a.pool)) return GDN_ERR_INVALID_ARG;
+    if (!a.slots && a.n_slots < a.B) return GDN_ERR_INVALID_ARG;
+    const void *ptrs[] = {a.q, a.k, a.v, a.alpha, a.beta, a.decay, a.pool, a.pool_out, a.o};
+    for (const void *p : ptrs)
+        if (misaligned(p, 16)) return GDN_ERR_INVALID_ARG;
+    if (misaligned(a.parents, 4) || misaligned(a.accepted, 4) || misaligned(a.slots, 4)) return GDN_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return launch_status(commit ? gdn::launch_tree_commit(a, dtype, s) : gdn::launch_tree(a, dtype, s));
+}
+
+gdn_status check_cache(const void *pool, const int *slots, const void *codes, const float *scales,
+                       const int *cache_slots, int N, int n_slots, int n_cache, int Hv, int dk, int dv, gdn_code code)
+{
+    if (N < 0 || n_slots < 0 || n_cache < 0 || (code != GDN_CODE_INT8 && code != GDN_CODE_E4M3)) return GDN_ERR_INVALID_ARG;
+    gdn_status st = check_sizes(1, Hv, dk, dv);
+    if (st != GDN_OK) return st;
+    if ((long long)N * Hv * 4 > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+    if (N == 0) return GDN_OK;
+    if (!slots || !cache_slots || (n_slots > 0 && !pool) || (n_cache > 0 && (!codes || !scales))) return GDN_ERR_INVALID_ARG;
+    if (misaligned(pool, 16) || misaligned(codes, 16) || misaligned(scales, 16) || misaligned(slots, 4) ||
+        misaligned(cache_slots, 4))
+        return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gdn_decay_fwd_workspace(int B, int T, int Hv, int dk, int dv, gdn_dtype dtype)
+{
+    if (B <= 0 || T <= 0 || Hv <= 0 || dk != gdn::kHeadDim || dv != gdn::kHeadDim || !is_dtype(dtype)) return 0;
+    DecayWalk w{};
+    w.B = B; w.T = T; w.Hv = Hv;
+    choose_segments(w, dtype);
+    return segment_bytes(w);
+}
+
+gdn_status gdn_decay_fwd(const void *q, const void *k, const void *v, const float *decay, const float *S0, void *o,
+                         float *S_final, int B, int T, int Hqk, int Hv, int dk, int dv, gdn_dtype dtype,
+                         void *workspace, size_t workspace_bytes, void *stream)
+{
+    return fwd_common(q, k, v, decay, S0, o, S_final, nullptr, B, T, Hqk, Hv, dk, dv, dtype, workspace,
+                      workspace_bytes, stream);
+}
+
+gdn_status gdn_decay_fwd_varlen(const void *q, const void *k, const void *v, const float *decay, const float *S0,
+                                void *o, float *S_final, const int *cu_seqlens, int N, int T_total, int Hqk, int Hv,
+                                int dk, int dv, gdn_dtype dtype, void *stream)
+{
+    if (N > 0 && T_total > 0 && (!cu_seqlens || misaligned(cu_seqlens, 4))) return GDN_ERR_INVALID_ARG;
+    return fwd_common(q, k, v, decay, S0, o, S_final, cu_seqlens, N, T_total, Hqk, Hv, dk, dv, dtype, nullptr, 0, stream);
+}
+
+gdn_status gdn_decay_decode_step(const void *q, const void *k, const void *v, const float *decay, const float *S,
+                                 void *o, float *S_new, int B, int Hqk, int Hv, int dk, int dv, gdn_dtype dtype,
+                                 void *stream)
+{
+    return decode_common(q, k, v, decay, S, o, S_new, nullptr, B, 0, Hqk, Hv, dk, dv, dtype, stream);
+}
+
+gdn_status gdn_decay_decode_step_slots(const void *q, const void *k, const void *v, const float *decay,
+                                       float *state_pool, const int *slots, void *o, int B, int n_slots, int Hqk,
+                                       int Hv, int dk, int dv, gdn_dtype dtype, void *stream)
+{
+    if (n_slots < 0 || (B > 0 && !slots)) return GDN_ERR_INVALID_ARG;
+    return decode_common(q, k, v, decay, state_pool, o, state_pool, slots, B, n_slots, Hqk, Hv, dk, dv, dtype, stream);
+}
+
+size_t gdn_decay_bwd_workspace(int B, int T, int Hqk, int Hv, int dk, int dv, gdn_dtype dtype)
+{
+    if (B <= 0 || T <= 0 || Hqk <= 0 || Hv <= 0 || Hv % Hqk || dk != gdn::kHeadDim || dv != gdn::kHeadDim ||
+        !is_dtype(dtype))
+        return 0;
+    const size_t rows = Hv == Hqk ? 0 : (size_t)B * T * Hv * gdn::kHeadDim * sizeof(float);
+    return gdn_decay_fwd_workspace(B, T, Hv, dk, dv, dtype) + rows;
+}
+
+gdn_status gdn_decay_bwd(const void *q, const void *k, const void *v, const float *decay, const float *S0,
+                         const void *dO, const float *dS_final, void *dq, void *dk, void *dv, float *dS0, int B, int T,
+                         int Hqk, int Hv, int dk_, int dv_, gdn_dtype dtype, void *workspace, size_t workspace_bytes,
+                         void *stream)
+{
+    if (B < 0 || T < 0 || !is_dtype(dtype)) return GDN_ERR_INVALID_ARG;
+    gdn_status st = check_sizes(Hqk, Hv, dk_, dv_);
+    if (st != GDN_OK) return st;
+    if (B > 65535 || Hv > 65535) return GDN_ERR_UNSUPPORTED;
+    if (B == 0) return GDN_OK;
+    const void *ptrs[] = {q, k, v, decay, S0, dO, dS_final, dq, dk, dv, dS0};
+    for (const void *p : ptrs)
+        if (misaligned(p, 16)) return GDN_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 0) return pass_state(dS0, dS_final, B, Hv, s);
+    if (!q || !k || !v || !decay || !dO || !dq || !dk || !dv) return GDN_ERR_INVALID_ARG;
+
+    DecayWalk w{};
+    w.decay = decay;
+    w.B = B; w.T = T; w.Hv = Hv;
+    choose_segments(w, dtype);
+    const size_t seg = segment_bytes(w);
+    const bool shared = Hv != Hqk;
+    const size_t need = gdn_decay_bwd_workspace(B, T, Hqk, Hv, dk_, dv_, dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need || misaligned(workspace, 256))) return GDN_ERR_INVALID_ARG;
+    w.seg = static_cast<float *>(workspace);
+    float *rows = shared ? reinterpret_cast<float *>(static_cast<char *>(workspace) + seg) : nullptr;
+    const long long tokens = (long long)B * T;
+    cudaError_t err;
+
+    // dq_t = S_t dO_t: the walk of S^T (row = v's dimension)
+    DecayWalk wq = w;
+    wq.x = dO; wq.y = v; wq.z = k;
+    wq.hx = wq.hy = Hv; wq.hz = Hqk;
+    wq.init = S0; wq.init_trans = true; wq.init_decays = true;
+    wq.o = shared ? static_cast<void *>(rows) : dq;
+    wq.o_f32 = shared;
+    err = launch_walk(wq, dtype, s);
+    if (err == cudaSuccess && shared) err = gdn::launch_head_sum(rows, dq, tokens, Hqk, Hv, dtype, s);
+    // dk_t = G_t v_t: backwards, the walk of G^T; before dv's, whose end state may replace dS_final
+    DecayWalk wk = w;
+    wk.rev = true;
+    wk.x = v; wk.y = dO; wk.z = q;
+    wk.hx = wk.hy = Hv; wk.hz = Hqk;
+    wk.init = dS_final; wk.init_trans = true;
+    wk.o = shared ? static_cast<void *>(rows) : dk;
+    wk.o_f32 = shared;
+    if (err == cudaSuccess) err = launch_walk(wk, dtype, s);
+    if (err == cudaSuccess && shared) err = gdn::launch_head_sum(rows, dk, tokens, Hqk, Hv, dtype, s);
+    // dv_t = G_t^T k_t, and dS0 = lambda G_0
+    DecayWalk wv = w;
+    wv.rev = true;
+    wv.x = k; wv.y = q; wv.z = dO;
+    wv.hx = wv.hy = Hqk; wv.hz = Hv;
+    wv.init = dS_final;
+    wv.fin = dS0;
+    wv.o = dv;
+    if (err == cudaSuccess) err = launch_walk(wv, dtype, s);
+    return launch_status(err);
+}
+
+gdn_status gdn_decode_tree(const void *q, const void *k, const void *v, const float *alpha, const float *beta,
+                           const int *parents, const float *state_pool, const int *slots, void *o, int B, int n,
+                           int n_slots, int Hqk, int Hv, int dk, int dv, gdn_dtype dtype, void *stream)
+{
+    if (B > 0 && (!alpha || !beta)) return GDN_ERR_INVALID_ARG;
+    gdn::TreeArgs a{q, k, v, alpha, beta, nullptr, parents, nullptr, slots, state_pool, nullptr, o, B, n, n_slots, Hqk, Hv};
+    return tree_common(a, false, dk, dv, dtype, stream);
+}
+
+gdn_status gdn_decay_decode_tree(const void *q, const void *k, const void *v, const float *decay, const int *parents,
+                                 const float *state_pool, const int *slots, void *o, int B, int n, int n_slots,
+                                 int Hqk, int Hv, int dk, int dv, gdn_dtype dtype, void *stream)
+{
+    if (B > 0 && !decay) return GDN_ERR_INVALID_ARG;
+    gdn::TreeArgs a{q, k, v, nullptr, nullptr, decay, parents, nullptr, slots, state_pool, nullptr, o, B, n, n_slots, Hqk, Hv};
+    return tree_common(a, false, dk, dv, dtype, stream);
+}
+
+gdn_status gdn_tree_commit(const void *k, const void *v, const float *alpha, const float *beta, const int *parents,
+                           const int *accepted, float *state_pool, const int *slots, int B, int n, int n_slots,
+                           int Hqk, int Hv, int dk, int dv, gdn_dtype dtype, void *stream)
+{
+    if (B > 0 && (!alpha || !beta)) return GDN_ERR_INVALID_ARG;
+    gdn::TreeArgs a{nullptr, k, v, alpha, beta, nullptr, parents, accepted, slots, nullptr, state_pool, nullptr, B, n, n_slots, Hqk, Hv};
+    return tree_common(a, true, dk, dv, dtype, stream);
+}
+
+gdn_status gdn_decay_tree_commit(const void *k, const void *v, const float *decay, const int *parents,
+                                 const int *accepted, float *state_pool, const int *slots, int B, int n, int n_slots,
+                                 int Hqk, int Hv, int dk, int dv, gdn_dtype dtype, void *stream)
+{
+    if (B > 0 && !decay) return GDN_ERR_INVALID_ARG;
+    gdn::TreeArgs a{nullptr, k, v, nullptr, nullptr, decay, parents, accepted, slots, nullptr, state_pool, nullptr, B, n, n_slots, Hqk, Hv};
+    return tree_common(a, true, dk, dv, dtype, stream);
+}
+
+gdn_status gdn_state_store(const float *state_pool, const int *slots, void *codes, float *scales,
+                           const int *cache_slots, int N, int n_slots, int n_cache, int Hv, int dk, int dv,
+                           gdn_code code, void *stream)
+{
+    gdn_status st = check_cache(state_pool, slots, codes, scales, cache_slots, N, n_slots, n_cache, Hv, dk, dv, code);
+    if (st != GDN_OK || N == 0) return st;
+    gdn::StateCacheArgs a{state_pool, nullptr, slots, cache_slots, codes, scales, N, n_slots, n_cache, Hv};
+    return launch_status(gdn::launch_state_store(a, code, static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_state_load(const void *codes, const float *scales, const int *cache_slots, float *state_pool,
+                          const int *slots, int N, int n_slots, int n_cache, int Hv, int dk, int dv, gdn_code code,
+                          void *stream)
+{
+    gdn_status st = check_cache(state_pool, slots, codes, scales, cache_slots, N, n_slots, n_cache, Hv, dk, dv, code);
+    if (st != GDN_OK || N == 0) return st;
+    gdn::StateCacheArgs a{nullptr, state_pool, slots, cache_slots, const_cast<void *>(codes),
+                          const_cast<float *>(scales), N, n_slots, n_cache, Hv};
+    return launch_status(gdn::launch_state_load(a, code, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -74,6 +74,79 @@ cudaError_t chunk_pipe_take_error(unsigned *out);
 cudaError_t chunk_tc_take_error(unsigned *out);
 cudaError_t split_take_error(unsigned *out);
 
+// ---- linear attention with a constant decay per head (gdn_decay.cu, gdn_decay_tc.cu)
+// One walk over the tokens of every (sequence, V head), forwards or backwards (rev),
+// with operands x, y, z of 128 columns each and the state H (128 x 128, row = y's
+// dimension, column = z's), which always includes the decay to the next token:
+//   forwards:  o_t = H^T x_t + sum_{s <= t} lambda^{t-s} (x_t . y_s) z_s  (H at each chunk's start)
+//   backwards: the same with the tokens in reverse order.
+// Prefill is (x, y, z) = (q, k, v); the gradients are the same walk with
+//   dq: (dO, v, k) forwards,  dk: (v, dO, q) and dv: (k, q, dO) backwards.
+struct DecayWalk {
+    const void *x, *y, *z;
+    int hx, hy, hz;                  // heads of each operand: V head h reads head h / (Hv / heads)
+    void *o = nullptr;               // [B, T, Hv, 128] of the operands' type, or fp32 (o_f32)
+    bool o_f32 = false;
+    const float *decay;
+    const float *init = nullptr;     // [B, Hv, 128, 128] or null (zeros)
+    bool init_trans = false;         // init is stored transposed (row = z's dimension)
+    bool init_decays = false;        // init still lacks one decay (H = lambda init)
+    float *fin = nullptr;            // end state, or null
+    bool fin_back = false;           // end state without the decay to the next token
+    int B, T, Hv;
+    bool rev = false;
+    const int *cu_seqlens = nullptr; // packed sequences (see ChunkArgs), forwards only
+    // Segments (dense only): nseg > 1 pieces of seg_chunks chunks.  A first launch writes
+    // seg [B, nseg, Hv, 128, 128]: entry 0 the start state, entry g the state that segment
+    // g - 1 adds on its own; the main launch starts segment g from the decayed sum of 0 .. g.
+    int nseg = 1, seg_chunks = 0;
+    float *seg = nullptr;
+};
+cudaError_t launch_decay_walk_simt(const DecayWalk &w, gdn_dtype dtype, cudaStream_t stream);
+// out [rows, Hqk, 128] = sum over each QK head's V heads of part [rows, Hv, 128]
+cudaError_t launch_head_sum(const float *part, void *out, long long rows, int Hqk, int Hv,
+                            gdn_dtype dtype, cudaStream_t stream);
+
+struct DecayDecodeArgs {
+    const void *q, *k, *v;
+    const float *decay, *S;
+    void *o;
+    float *S_new;
+    int B, Hqk, Hv;
+    const int *slots = nullptr;
+    int n_slots = 0;
+};
+cudaError_t launch_decay_decode(const DecayDecodeArgs &a, gdn_dtype dtype, cudaStream_t stream);
+
+// ---- draft trees (gdn_tree.cu): alpha/beta (delta rule) or decay (then alpha, beta null)
+struct TreeArgs {
+    const void *q, *k, *v;
+    const float *alpha, *beta, *decay;
+    const int *parents, *accepted, *slots;
+    const float *pool;
+    float *pool_out;                 // commit
+    void *o;                         // verification
+    int B, n, n_slots, Hqk, Hv;
+};
+constexpr int kMaxTreeNodes = 64;
+cudaError_t launch_tree(const TreeArgs &a, gdn_dtype dtype, cudaStream_t stream);
+cudaError_t launch_tree_commit(const TreeArgs &a, gdn_dtype dtype, cudaStream_t stream);
+
+// ---- 8-bit state cache (gdn_state_cache.cu)
+struct StateCacheArgs {
+    const float *pool_in;
+    float *pool_out;
+    const int *slots, *cache_slots;
+    void *codes;
+    float *scales;
+    int N, n_slots, n_cache, Hv;
+};
+cudaError_t launch_state_store(const StateCacheArgs &a, gdn_code code, cudaStream_t stream);
+cudaError_t launch_state_load(const StateCacheArgs &a, gdn_code code, cudaStream_t stream);
+
+// Status of a launch for the C entries (remembers the error for gdn_last_cuda_error).
+gdn_status launch_status(cudaError_t err);
+
 // sst: null, or where the first segments write S_start(1)^T in bf16 (see TcParams).
 cudaError_t launch_chunk_tc_segments(const ChunkArgs &a, int seg_len, int nseg, float *segD,
                                      float *segM, __nv_bfloat16 *R, __nv_bfloat16 *sst,

@@ -1,0 +1,143 @@
+// 8-bit state cache: fp32 state rows to codes with one scale per row, and back.
+//
+// A row is one key dimension of a state: 128 values, one per lane and float4
+// component, so a warp reads a row as 512 contiguous bytes, finds its largest
+// magnitude with one integer reduction (the bits of |x| order like the values,
+// and NaN above infinity above every number) and writes 128 bytes of codes.
+// Pure HBM stream: 640 bytes and a scale per row against a few instructions per
+// value.  The quotients are per row, correctly rounded, and the codes one product
+// and one rounding per value, so that codes are reproducible bit for bit.
+#include <cuda_fp8.h>
+
+#include "gdn_internal.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kCacheThreads = 256;
+constexpr int kRowsPerWarp = 4;                                  // rows in flight per warp
+constexpr int kRowsPerCta = kCacheThreads / 32 * kRowsPerWarp;   // 32: four CTAs per head's state
+constexpr float kTinyRow = 1e-30f;
+
+template <bool E4M3>
+__device__ __forceinline__ uint32_t encode4(float4 x, float inv)
+{
+    const float a = __fmul_rn(x.x, inv), b = __fmul_rn(x.y, inv), c = __fmul_rn(x.z, inv),
+                d = __fmul_rn(x.w, inv);
+    if (E4M3) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+        return lo | (hi << 16);
+    }
+    // |x * inv| <= 127 (1 + 2^-23): the nearest integer never leaves [-127, 127]
+    const uint32_t ia = (uint32_t)__float2int_rn(a) & 0xffu, ib = (uint32_t)__float2int_rn(b) & 0xffu;
+    const uint32_t ic = (uint32_t)__float2int_rn(c) & 0xffu, id = (uint32_t)__float2int_rn(d) & 0xffu;
+    return ia | (ib << 8) | (ic << 16) | (id << 24);
+}
+
+template <bool E4M3>
+__device__ __forceinline__ float4 decode4(uint32_t c, float s)
+{
+    float4 r;
+    if (E4M3) {
+        const __half2 lo(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3));
+        const __half2 hi(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> 16), __NV_E4M3));
+        const float2 a = __half22float2(lo), b = __half22float2(hi);
+        r = make_float4(a.x, a.y, b.x, b.y);
+    } else {
+        r = make_float4((float)(int8_t)c, (float)(int8_t)(c >> 8), (float)(int8_t)(c >> 16),
+                        (float)(int8_t)(c >> 24));
+    }
+    return make_float4(__fmul_rn(r.x, s), __fmul_rn(r.y, s), __fmul_rn(r.z, s), __fmul_rn(r.w, s));
+}
+
+// Row indices of this warp in the pool and the cache; false for a skipped entry.
+__device__ __forceinline__ bool entry_rows(const int *slots, const int *cache_slots, int n_slots,
+                                           int n_cache, int Hv, size_t &pool_row, size_t &cache_row)
+{
+    const unsigned per = (unsigned)Hv * (kHeadDim / kRowsPerCta);   // CTAs per entry
+    const unsigned i = blockIdx.x / per, r = blockIdx.x - i * per;
+    const int s = slots[i], c = cache_slots[i];
+    if (s < 0 || s >= n_slots || c < 0 || c >= n_cache) return false;
+    const size_t row = (size_t)r * kRowsPerCta + (threadIdx.x >> 5) * kRowsPerWarp;
+    pool_row = (size_t)s * Hv * kHeadDim + row;
+    cache_row = (size_t)c * Hv * kHeadDim + row;
+    return true;
+}
+
+template <bool E4M3>
+__global__ void __launch_bounds__(kCacheThreads)
+store_kernel(const float *__restrict__ pool, const int *__restrict__ slots, uint32_t *__restrict__ codes,
+             float *__restrict__ scales, const int *__restrict__ cache_slots, int n_slots, int n_cache, int Hv)
+{
+    size_t pr, cr;
+    if (!entry_rows(slots, cache_slots, n_slots, n_cache, Hv, pr, cr)) return;
+    const int lane = threadIdx.x & 31;
+    const float qmax = E4M3 ? 448.0f : 127.0f;
+    float4 x[kRowsPerWarp];
+#pragma unroll
+    for (int m = 0; m < kRowsPerWarp; ++m)
+        x[m] = __ldcs(reinterpret_cast<const float4 *>(pool) + (pr + m) * 32 + lane);
+    float mine = 0.f;
+#pragma unroll
+    for (int m = 0; m < kRowsPerWarp; ++m) {
+        const uint32_t ax = __float_as_uint(x[m].x) & 0x7fffffffu, ay = __float_as_uint(x[m].y) & 0x7fffffffu;
+        const uint32_t az = __float_as_uint(x[m].z) & 0x7fffffffu, aw = __float_as_uint(x[m].w) & 0x7fffffffu;
+        const uint32_t bits = __reduce_max_sync(0xffffffffu, max(max(ax, ay), max(az, aw)));
+        const float amax = __uint_as_float(bits);
+        float scale = 0.f;
+        uint32_t c = 0;
+        if (bits >= 0x7f800000u) {
+            scale = __uint_as_float(0x7fffffffu);
+        } else if (amax >= kTinyRow) {
+            scale = __fdiv_rn(amax, qmax);
+            c = encode4<E4M3>(x[m], __fdiv_rn(qmax, amax));
+        }
+        __stcs(codes + (cr + m) * 32 + lane, c);
+        if (lane == m) mine = scale;
+    }
+    if (lane < kRowsPerWarp) scales[cr + lane] = mine;
+}
+
+template <bool E4M3>
+__global__ void __launch_bounds__(kCacheThreads)
+load_kernel(const uint32_t *__restrict__ codes, const float *__restrict__ scales,
+            const int *__restrict__ cache_slots, float *__restrict__ pool, const int *__restrict__ slots,
+            int n_slots, int n_cache, int Hv)
+{
+    size_t pr, cr;
+    if (!entry_rows(slots, cache_slots, n_slots, n_cache, Hv, pr, cr)) return;
+    const int lane = threadIdx.x & 31;
+    uint32_t c[kRowsPerWarp];
+    float s[kRowsPerWarp];
+#pragma unroll
+    for (int m = 0; m < kRowsPerWarp; ++m) {
+        c[m] = __ldcs(codes + (cr + m) * 32 + lane);
+        s[m] = scales[cr + m];
+    }
+#pragma unroll
+    for (int m = 0; m < kRowsPerWarp; ++m)
+        __stcs(reinterpret_cast<float4 *>(pool) + (pr + m) * 32 + lane, decode4<E4M3>(c[m], s[m]));
+}
+
+unsigned cache_grid(const StateCacheArgs &a) { return (unsigned)a.N * a.Hv * (kHeadDim / kRowsPerCta); }
+
+}  // namespace
+
+cudaError_t launch_state_store(const StateCacheArgs &a, gdn_code code, cudaStream_t stream)
+{
+    auto *kernel = code == GDN_CODE_E4M3 ? store_kernel<true> : store_kernel<false>;
+    kernel<<<cache_grid(a), kCacheThreads, 0, stream>>>(a.pool_in, a.slots, (uint32_t *)a.codes, a.scales,
+                                                        a.cache_slots, a.n_slots, a.n_cache, a.Hv);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_state_load(const StateCacheArgs &a, gdn_code code, cudaStream_t stream)
+{
+    auto *kernel = code == GDN_CODE_E4M3 ? load_kernel<true> : load_kernel<false>;
+    kernel<<<cache_grid(a), kCacheThreads, 0, stream>>>((const uint32_t *)a.codes, a.scales, a.cache_slots,
+                                                        a.pool_out, a.slots, a.n_slots, a.n_cache, a.Hv);
+    return cudaGetLastError();
+}
+
+}  // namespace gdn

@@ -1,0 +1,485 @@
+// Trees of drafted tokens over a pool of recurrent states: outputs of every node in
+// one pass over each state (verification), and the update of the states along the
+// accepted path (commit).  Gated delta rule, or decay rule (u = v).
+//
+// Verification.  With path(i) the nodes from the root to i, Gam_ij the product of
+// the gates after j down to i (j on path(i)) and root_i the product along all of
+// path(i), the recurrence along every path at once is the chunk form with "earlier
+// token" replaced by "ancestor":
+//   u_i = beta_i (v_i - root_i S^T k_i - sum_{j strict ancestor} Gam_ij (k_i . k_j) u_j)
+//   o_i = root_i S^T q_i + sum_{j on path(i)} Gam_ij (q_i . k_j) u_j
+// K S and Q S are warp MMAs on bf16 pieces of S (two pieces for bf16 inputs: 16 bits,
+// against the 8 of the output; three, all 24 bits, for fp32 inputs, whose rows are
+// cut in three as well).  A state is 64 KiB and n is at most 64 rows, so the products
+// are short next to the state's load, and M = 2n rows do not fill a 128-row tcgen05
+// tile: fragments come straight from the fp32 state in shared memory, which saves
+// the pass that would lay the pieces out for it.  The sums over ancestors run over
+// each node's path list, not over all earlier nodes: a bushy tree costs its depths.
+#include "gdn_internal.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kTreeThreads = 256;
+constexpr int kLdS = kHeadDim + 4;       // floats per row of S, U, QS in shared memory
+constexpr int kLdK = kHeadDim + 8;       // bf16 per row of K and Q
+constexpr float kLog2Clamp = -87.0f * 1.4426950408889634f;
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                 ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], const void *p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"((uint32_t)__cvta_generic_to_shared(p)) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The bf16 pieces of a pair: the upper 16 bits of what the pieces before left over
+// (exact remainders: three pieces are all 24 bits).
+__device__ __forceinline__ uint32_t take_piece(float &a, float &b) {
+    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+    a -= __uint_as_float(ua & 0xffff0000u);
+    b -= __uint_as_float(ub & 0xffff0000u);
+    return __byte_perm(ua, ub, 0x7632);
+}
+
+template <typename T> struct TreeTypes;
+template <> struct TreeTypes<__nv_bfloat16> { static constexpr int kPlanes = 1, kPieces = 2; };
+template <> struct TreeTypes<float> { static constexpr int kPlanes = 3, kPieces = 3; };
+
+template <typename T, int N>
+struct TreeSmem {
+    static constexpr int kPlanes = TreeTypes<T>::kPlanes;
+    union {
+        float S[kHeadDim][kLdS];
+        struct { float U[N][kLdS], QS[N][kLdS]; } r;     // after the products with S
+    };
+    __nv_bfloat16 kq[kPlanes][2][N][kLdK];               // k rows, q rows
+    float A[N][N + 4], P[N][N + 4];                      // by position in the node's path list
+    double b[N];                                         // log2 of root_i
+    unsigned long long mask[N];                          // path(i), bit j; 0 for padding
+    float beta[N], root[N];
+    int jump[N];
+    unsigned char list[N][N];                            // path(i) in node order
+    unsigned char len[N];
+};
+
+template <typename T, bool DELTA, int N>
+__global__ void __launch_bounds__(kTreeThreads)
+tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+            const float *__restrict__ alpha, const float *__restrict__ beta, const float *__restrict__ decay,
+            const int *__restrict__ parents, const float *__restrict__ pool, const int *__restrict__ slots,
+            T *__restrict__ o, int n, int n_slots, int Hqk, int Hv)
+{
+    using Sm = TreeSmem<T, N>;
+    constexpr int kPlanes = Sm::kPlanes, kPieces = TreeTypes<T>::kPieces, MT = N / 16;
+    extern __shared__ __align__(16) unsigned char raw[];
+    Sm &sm = *reinterpret_cast<Sm *>(raw);
+    const unsigned bh = blockIdx.x;
+    const int b = (int)(bh / (unsigned)Hv), h = (int)(bh - (unsigned)b * Hv), hq = h / (Hv / Hqk);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int slot = slots ? slots[b] : b;
+    if (slot < 0 || slot >= n_slots) return;
+
+    const float *S = pool + ((size_t)slot * Hv + h) * (kHeadDim * kHeadDim);
+#pragma unroll
+    for (int m = 0; m < 16; ++m)
+        cp_async16(&sm.S[warp + 8 * m][4 * lane], S + (warp + 8 * m) * kHeadDim + 4 * lane);
+
+    if (warp == 0) {
+        // ---- paths and gates by pointer jumping: after round r, mask and b cover 2^r steps.
+        //      jump: next node up, -1 past the root, -2 padding.
+        for (int i = lane; i < N; i += 32) {
+            int p = i < n ? parents[(size_t)b * n + i] : -2;
+            if (p < -1 || p >= i) p = -2;
+            sm.jump[i] = p;
+            sm.mask[i] = 1ull << i;
+            double g = 0.0;
+            float be = 0.f;
+            if (i < n) {
+                const size_t at = ((size_t)b * n + i) * Hv + h;
+                g = (double)fmaxf(log2f(DELTA ? alpha[at] : decay[h]), kLog2Clamp);
+                if (DELTA) be = beta[at];
+            }
+            sm.b[i] = g;
+            sm.beta[i] = be;
+        }
+        __syncwarp();
+        constexpr int kPer = (N + 31) / 32;
+#pragma unroll 1
+        for (int step = 1; step < N; step <<= 1) {
+            unsigned long long m2[kPer];
+            double b2[kPer];
+            int j2[kPer];
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) {
+                const int i = lane + 32 * x;
+                m2[x] = 0; b2[x] = 0.0; j2[x] = -1;
+                if (i < N) {
+                    const int j = sm.jump[i];
+                    j2[x] = j;
+                    if (j >= 0) { m2[x] = sm.mask[j]; b2[x] = sm.b[j]; j2[x] = sm.jump[j]; }
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) {
+                const int i = lane + 32 * x;
+                if (i < N) { sm.mask[i] |= m2[x]; sm.b[i] += b2[x]; sm.jump[i] = j2[x]; }
+            }
+            __syncwarp();
+        }
+        for (int i = lane; i < N; i += 32) {
+            unsigned long long m = sm.jump[i] == -1 ? sm.mask[i] : 0ull;   // -2 reached: padding
+            sm.mask[i] = m;
+            sm.root[i] = exp2f((float)sm.b[i]);
+            int c = 0;
+            while (m) {
+                sm.list[i][c++] = (unsigned char)(__ffsll((long long)m) - 1);
+                m &= m - 1;
+            }
+            sm.len[i] = (unsigned char)c;
+        }
+    } else {
+        // ---- k and q rows as bf16 planes; rows past n are zeros
+        for (int i = tid - 32; i < 2 * N * (kHeadDim / 4); i += kTreeThreads - 32) {
+            const int which = i / (N * (kHeadDim / 4)), r = (i / (kHeadDim / 4)) % N, d = (i % (kHeadDim / 4)) * 4;
+            const T *src = which ? q : k;
+            const size_t at = (((size_t)b * n + r) * Hqk + hq) * kHeadDim + d;
+            if constexpr (kPlanes == 1) {
+                uint2 u = make_uint2(0u, 0u);
+                if (r < n) u = *reinterpret_cast<const uint2 *>(src + at);
+                *reinterpret_cast<uint2 *>(&sm.kq[0][which][r][d]) = u;
+            } else {
+                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r < n) f = *reinterpret_cast<const float4 *>(src + at);
+#pragma unroll
+                for (int pl = 0; pl < kPlanes; ++pl) {
+                    const uint32_t lo = take_piece(f.x, f.y), hi = take_piece(f.z, f.w);
+                    *reinterpret_cast<uint2 *>(&sm.kq[pl][which][r][d]) = make_uint2(lo, hi);
+                }
+            }
+        }
+    }
+    cp_async_wait_all();
+    __syncthreads();
+
+    const int role = warp >> 2, cb = warp & 3;           // role 0: k rows, 1: q rows
+    const int g = lane >> 2, t = lane & 3;
+    const int lrow = lane & 15, lcol = (lane >> 4) * 8;  // ldmatrix addresses
+    // ---- grams with k -> coefficients of the path sums
+    if (DELTA || role == 1) {
+        for (int nt = cb; nt < N / 8; nt += 4) {
+#pragma unroll 1
+            for (int mt = nt / 2; mt < MT; ++mt) {       // j <= i only
+                float acc[4] = {};
+#pragma unroll
+                for (int pa = 0; pa < kPlanes; ++pa)
+#pragma unroll
+                    for (int pb = 0; pa + pb < kPlanes; ++pb)
+#pragma unroll
+                        for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+                            uint32_t a[4];
+                            ldmatrix_x4(a, &sm.kq[pa][role][mt * 16 + lrow][ks * 16 + lcol]);
+                            const __nv_bfloat16 *kr = &sm.kq[pb][0][nt * 8 + g][ks * 16 + 2 * t];
+                            mma16816(acc, a, *reinterpret_cast<const uint32_t *>(kr),
+                                     *reinterpret_cast<const uint32_t *>(kr + 8));
+                        }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = mt * 16 + g + (e >> 1) * 8, j = nt * 8 + 2 * t + (e & 1);
+                    const unsigned long long m = sm.mask[i];
+                    if (((m >> j) & 1ull) && (role == 1 || j < i)) {
+                        const int at = __popcll(m & ((1ull << j) - 1ull));
+                        const float x = exp2f((float)(sm.b[i] - sm.b[j])) * acc[e];
+                        if (role == 0) sm.A[i][at] = sm.beta[i] * x;
+                        else sm.P[i][at] = x;
+                    }
+                }
+            }
+        }
+    }
+    // ---- rows times S: this warp's 32 columns, thread (g, t) the columns 4g .. 4g+3 of B
+    float acc[MT][4][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[mt][j][e] = 0.f;
+    if (DELTA || role == 1) {
+#pragma unroll 1
+        for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+            float4 s0 = *reinterpret_cast<const float4 *>(&sm.S[ks * 16 + 2 * t][32 * cb + 4 * g]);
+            float4 s1 = *reinterpret_cast<const float4 *>(&sm.S[ks * 16 + 2 * t + 1][32 * cb + 4 * g]);
+            float4 s2 = *reinterpret_cast<const float4 *>(&sm.S[ks * 16 + 2 * t + 8][32 * cb + 4 * g]);
+            float4 s3 = *reinterpret_cast<const float4 *>(&sm.S[ks * 16 + 2 * t + 9][32 * cb + 4 * g]);
+            uint32_t bp[kPieces][4][2];
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) {
+                bp[p][0][0] = take_piece(s0.x, s1.x); bp[p][0][1] = take_piece(s2.x, s3.x);
+                bp[p][1][0] = take_piece(s0.y, s1.y); bp[p][1][1] = take_piece(s2.y, s3.y);
+                bp[p][2][0] = take_piece(s0.z, s1.z); bp[p][2][1] = take_piece(s2.z, s3.z);
+                bp[p][3][0] = take_piece(s0.w, s1.w); bp[p][3][1] = take_piece(s2.w, s3.w);
+            }
+#pragma unroll
+            for (int pa = 0; pa < kPlanes; ++pa)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    uint32_t a[4];
+                    ldmatrix_x4(a, &sm.kq[pa][role][mt * 16 + lrow][ks * 16 + lcol]);
+#pragma unroll
+                    for (int p = 0; p < kPieces; ++p)
+                        if (pa + p < kPieces) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) mma16816(acc[mt][j], a, bp[p][j][0], bp[p][j][1]);
+                        }
+                }
+        }
+    }
+    __syncthreads();                                     // S read; A and P written
+    // ---- accumulators: rows g, g + 8 of each tile, columns 32 cb + 8t .. + 7
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int i = mt * 16 + g + 8 * half, c = 32 * cb + 8 * t;
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[j] = acc[mt][j][2 * half];
+                x[4 + j] = acc[mt][j][2 * half + 1];
+            }
+            if (role == 0) {
+                const bool on = i < n && sm.mask[i] != 0;
+                const T *vr = v + (((size_t)b * n + i) * Hv + h) * kHeadDim + c;
+                const float f = sm.root[i], be = sm.beta[i];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float vv = on ? to_f32(vr[j]) : 0.f;
+                    x[j] = DELTA ? be * (vv - f * x[j]) : vv;
+                }
+            }
+            float *dst = role == 0 ? &sm.r.U[i][c] : &sm.r.QS[i][c];
+            *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4 *>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        }
+    __syncthreads();
+    // ---- u_i down the tree, one column per thread
+    if (DELTA) {
+        if (tid < kHeadDim) {
+#pragma unroll 1
+            for (int i = 1; i < n; ++i) {
+                const int strict = (int)sm.len[i] - 1;
+                if (strict <= 0) continue;
+                float s = 0.f;
+                for (int d = 0; d < strict; ++d) s = fmaf(sm.A[i][d], sm.r.U[sm.list[i][d]][tid], s);
+                sm.r.U[i][tid] -= s;
+            }
+        }
+        __syncthreads();
+    }
+    // ---- outputs: two columns per thread, every fourth node
+    {
+        const int c = 2 * (tid & 63);
+#pragma unroll 1
+        for (int i = tid >> 6; i < n; i += 4) {
+            const int len = sm.len[i];
+            if (len == 0) continue;                      // padding: the row stays as it was
+            const float2 r = *reinterpret_cast<const float2 *>(&sm.r.QS[i][c]);
+            float s0 = sm.root[i] * r.x, s1 = sm.root[i] * r.y;
+            for (int d = 0; d < len; ++d) {
+                const float p = sm.P[i][d];
+                const float2 u = *reinterpret_cast<const float2 *>(&sm.r.U[sm.list[i][d]][c]);
+                s0 = fmaf(p, u.x, s0);
+                s1 = fmaf(p, u.y, s1);
+            }
+            T *dst = o + (((size_t)b * n + i) * Hv + h) * kHeadDim + c;
+            if constexpr (kPlanes == 1) {
+                *reinterpret_cast<__nv_bfloat162 *>(dst) = __floats2bfloat162_rn(s0, s1);
+            } else {
+                *reinterpret_cast<float2 *>(dst) = make_float2(s0, s1);
+            }
+        }
+    }
+}
+
+template <typename T, bool DELTA, int N>
+cudaError_t launch_tree_n(const TreeArgs &a, cudaStream_t stream)
+{
+    const int smem = (int)sizeof(TreeSmem<T, N>);
+    cudaError_t err = cudaFuncSetAttribute(tree_kernel<T, DELTA, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    tree_kernel<T, DELTA, N><<<(unsigned)((size_t)a.B * a.Hv), kTreeThreads, smem, stream>>>(
+        (const T *)a.q, (const T *)a.k, (const T *)a.v, a.alpha, a.beta, a.decay, a.parents, a.pool, a.slots, (T *)a.o,
+        a.n, a.n_slots, a.Hqk, a.Hv);
+    return cudaGetLastError();
+}
+
+template <typename T, bool DELTA>
+cudaError_t launch_tree_typed(const TreeArgs &a, cudaStream_t stream)
+{
+    if (a.n <= 16) return launch_tree_n<T, DELTA, 16>(a, stream);
+    if (a.n <= 32) return launch_tree_n<T, DELTA, 32>(a, stream);
+    return launch_tree_n<T, DELTA, 64>(a, stream);
+}
+
+// ------------------------------------------------------------------ commit
+// One CTA per (sequence, V head): the state in registers as in the decode kernel
+// (warp w rows w, w + 8, ..., lane l columns 4l .. 4l + 3), read and written once.  The
+// path's nodes are taken four at a time: their products with the state share one
+// pass over the registers and one reduction, the delta rule inside the four is a
+// 4 x 4 substitution per column, and one pass applies the four writes.
+constexpr int kGroup = 4;
+
+template <typename T, bool DELTA>
+__global__ void __launch_bounds__(kTreeThreads, 2)
+commit_kernel(const T *__restrict__ k, const T *__restrict__ v, const float *__restrict__ alpha,
+              const float *__restrict__ beta, const float *__restrict__ decay, const int *__restrict__ parents,
+              const int *__restrict__ accepted, float *pool, const int *__restrict__ slots, int n, int n_slots,
+              int Hqk, int Hv)
+{
+    __shared__ int path[kMaxTreeNodes], par[kMaxTreeNodes];
+    __shared__ int path_len;
+    __shared__ float sk[kGroup][kHeadDim];
+    __shared__ float4 part[8][kGroup][32];
+    __shared__ float su[kGroup][kHeadDim];
+    __shared__ float skk[kGroup][kGroup];
+    const unsigned bh = blockIdx.x;
+    const int b = (int)(bh / (unsigned)Hv), h = (int)(bh - (unsigned)b * Hv), hq = h / (Hv / Hqk);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int slot = slots ? slots[b] : b, leaf = accepted[b];
+    if (slot < 0 || slot >= n_slots || leaf < 0 || leaf >= n) return;
+    if (tid < n) par[tid] = parents[(size_t)b * n + tid];
+    float4 *S4 = reinterpret_cast<float4 *>(pool + ((size_t)slot * Hv + h) * (kHeadDim * kHeadDim));
+    float4 s[16];
+#pragma unroll
+    for (int m = 0; m < 16; ++m) s[m] = __ldcs(S4 + (warp + 8 * m) * 32 + lane);
+    __syncthreads();
+    if (tid == 0) {
+        int len = 0, i = leaf;
+        while (i >= 0) {                                 // parents are smaller: at most n steps
+            path[len++] = i;
+            const int p = par[i];
+            i = (p < -1 || p >= i) ? -2 : p;
+        }
+        path_len = i == -1 ? len : 0;                    // -2: below a padding node
+    }
+    __syncthreads();
+    const int len = path_len;
+    if (len == 0) return;
+    for (int d0 = 0; d0 < len; d0 += kGroup) {
+        const int m = min(kGroup, len - d0);
+        // rows of the group (root first); missing nodes get k = 0 and no write
+        for (int i = tid; i < kGroup * kHeadDim; i += kTreeThreads) {
+            const int j = i / kHeadDim, d = i % kHeadDim;
+            float x = 0.f;
+            if (j < m) x = to_f32(k[(((size_t)b * n + path[len - 1 - d0 - j]) * Hqk + hq) * kHeadDim + d]);
+            sk[j][d] = x;
+        }
+        float a[kGroup];                                 // gates; 1 for missing nodes
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) {
+            a[j] = 1.f;
+            if (j < m)
+                a[j] = fmaxf(DELTA ? alpha[((size_t)b * n + path[len - 1 - d0 - j]) * Hv + h] : decay[h], 1.6458114e-38f);
+        }
+        __syncthreads();
+        if (DELTA) {
+            if (warp < 6) {                              // k_i . k_j, i > j, one pair per warp
+                const int i = warp < 1 ? 1 : warp < 3 ? 2 : 3, j = warp - (i * (i - 1)) / 2;
+                float x = 0.f;
+#pragma unroll
+                for (int d = 0; d < 4; ++d) x = fmaf(sk[i][lane + 32 * d], sk[j][lane + 32 * d], x);
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+                if (lane == 0) skk[i][j] = x;
+            }
+            float4 pp[kGroup];
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) pp[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j) {
+                    const float ki = sk[j][warp + 8 * r];
+                    pp[j].x = fmaf(s[r].x, ki, pp[j].x); pp[j].y = fmaf(s[r].y, ki, pp[j].y);
+                    pp[j].z = fmaf(s[r].z, ki, pp[j].z); pp[j].w = fmaf(s[r].w, ki, pp[j].w);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) part[warp][j][lane] = pp[j];
+            __syncthreads();
+        }
+        if (tid < kHeadDim) {
+            float u[kGroup];
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) {
+                u[j] = 0.f;
+                if (j < m) {
+                    const size_t at = ((size_t)b * n + path[len - 1 - d0 - j]) * Hv + h;
+                    u[j] = to_f32(v[at * kHeadDim + tid]);
+                    if (DELTA) {
+                        float p = 0.f;
+#pragma unroll
+                        for (int w = 0; w < 8; ++w) p += reinterpret_cast<const float *>(&part[w][j][0])[tid];
+#pragma unroll
+                        for (int i = 0; i < j; ++i) p = fmaf(a[i], p, skk[j][i] * u[i]);   // S after node i, times k_j
+                        u[j] = beta[at] * (u[j] - a[j] * p);
+                    }
+                }
+                su[j][tid] = u[j];
+            }
+        }
+        __syncthreads();
+        float4 u4[kGroup];
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) u4[j] = *reinterpret_cast<const float4 *>(&su[j][4 * lane]);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) {
+                const float ki = sk[j][warp + 8 * r];
+                s[r].x = fmaf(a[j], s[r].x, ki * u4[j].x); s[r].y = fmaf(a[j], s[r].y, ki * u4[j].y);
+                s[r].z = fmaf(a[j], s[r].z, ki * u4[j].z); s[r].w = fmaf(a[j], s[r].w, ki * u4[j].w);
+            }
+        }
+        __syncthreads();                                 // sk, su, part are written again
+    }
+#pragma unroll
+    for (int m = 0; m < 16; ++m) __stcs(S4 + (warp + 8 * m) * 32 + lane, s[m]);
+}
+
+template <typename T, bool DELTA>
+cudaError_t launch_commit_typed(const TreeArgs &a, cudaStream_t stream)
+{
+    commit_kernel<T, DELTA><<<(unsigned)((size_t)a.B * a.Hv), kTreeThreads, 0, stream>>>(
+        (const T *)a.k, (const T *)a.v, a.alpha, a.beta, a.decay, a.parents, a.accepted, a.pool_out, a.slots, a.n,
+        a.n_slots, a.Hqk, a.Hv);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_tree(const TreeArgs &a, gdn_dtype dtype, cudaStream_t stream)
+{
+    if (dtype == GDN_BF16)
+        return a.decay ? launch_tree_typed<__nv_bfloat16, false>(a, stream) : launch_tree_typed<__nv_bfloat16, true>(a, stream);
+    return a.decay ? launch_tree_typed<float, false>(a, stream) : launch_tree_typed<float, true>(a, stream);
+}
+
+cudaError_t launch_tree_commit(const TreeArgs &a, gdn_dtype dtype, cudaStream_t stream)
+{
+    if (dtype == GDN_BF16)
+        return a.decay ? launch_commit_typed<__nv_bfloat16, false>(a, stream) : launch_commit_typed<__nv_bfloat16, true>(a, stream);
+    return a.decay ? launch_commit_typed<float, false>(a, stream) : launch_commit_typed<float, true>(a, stream);
+}
+
+}  // namespace gdn
