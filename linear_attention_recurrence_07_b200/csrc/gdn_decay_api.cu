@@ -55,6 +55,7 @@ size_t segment_bytes(const DecayWalk &w)
 
 cudaError_t launch_walk(const DecayWalk &w, gdn_dtype dtype, cudaStream_t s)
 {
+    if (dtype == GDN_BF16 && gdn::chunk_tc_available()) return gdn::launch_decay_walk_tc(w, s);
     return gdn::launch_decay_walk_simt(w, dtype, s);
 }
 

@@ -103,6 +103,8 @@ struct DecayWalk {
     float *seg = nullptr;
 };
 cudaError_t launch_decay_walk_simt(const DecayWalk &w, gdn_dtype dtype, cudaStream_t stream);
+cudaError_t launch_decay_walk_tc(const DecayWalk &w, cudaStream_t stream);   // bf16 operands
+cudaError_t decay_tc_take_error(unsigned *out);
 // out [rows, Hqk, 128] = sum over each QK head's V heads of part [rows, Hv, 128]
 cudaError_t launch_head_sum(const float *part, void *out, long long rows, int Hqk, int Hv,
                             gdn_dtype dtype, cudaStream_t stream);

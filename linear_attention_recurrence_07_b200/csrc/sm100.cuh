@@ -225,6 +225,14 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *r) {
         : "memory");
 }
 
+// 8 consecutive 32-bit columns, same lane mapping.
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
+}
+
 // 32 consecutive 32-bit columns of packed data (e.g. bf16 pairs), same lane mapping.
 __device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t *r) {
     tmem_st32(taddr, reinterpret_cast<const float *>(r));
