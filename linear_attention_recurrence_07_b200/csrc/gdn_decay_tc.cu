@@ -5,35 +5,36 @@
 // Per chunk of L <= 64 tokens, H the state at its start (decayed to its first token),
 // p_i = i forwards, L - 1 - i backwards:
 //   G    = X Y^T                                        M=64  N=64  K=128
-//   P_ij = lambda^{|i-j|} G_ij, j at or before i        (bf16)
-//   OX^T = H^T X^T   (H^T in two bf16 pieces)           M=128 N=64  K=2x128
-//   OI^T = Z^T P^T                                      M=128 N=64  K=64
-//   O    = diag(lambda^p) OX + OI
-//   D^T  = Z'^T Y, Z' = diag(lambda^{L-p}) Z in three bf16 pieces (all 24 bits)
-//                                                       M=128 N=128 K=3x64
+//   P_ij = lambda^{-p_j} G_ij, j at or before i         (two bf16 pieces)
+//   O^T  = (H^T X^T + Z^T P^T) diag(lambda^p)           M=128 N=64  K=2x128 + 2x64
+//   D^T  = Z'^T Y, Z' = diag(lambda^{L-p}) Z in NZ bf16 pieces
+//                                                       M=128 N=128 K=NZ x 64
 //   H^T <- lambda^L H^T + D^T                           (fp32 registers)
 // Unlike the delta rule, D does not depend on the state: the chain from chunk to chunk
 // is one fused multiply-add per state element.  The state therefore lives in registers
 // (64 per thread over 256 threads), and only its two bf16 pieces go to the tensor core.
-// Its rounding: the pieces drop 2^-17 of the state in O (a bf16 result); D enters the
-// state with all its bits, small pieces first, because the tensor core truncates when
-// it accumulates.  P is rounded to bf16 once, like every operand of a bf16 attention.
+//
+// Roundings: two pieces carry 16 bits of H and of P, against the 8 of O.  Z' has three
+// pieces, all 24 bits, where an end state is wanted, two where the state only feeds O;
+// small pieces are accumulated first, because the tensor core truncates.  lambda^{-p_j}
+// grows to lambda^{-63}: below lambda = 2^-(100/63) the scale is held at 2^100, which
+// replaces a factor lambda^p < 2^-100 on H's share of a row by 2^-100.
 //
 // One CTA per (sequence or segment, V head), warp-specialised:
 //   warp 0      TMA producer: X, Y, Z tiles, four stages of 48 KB
-//   warp 1      MMA issuer (one thread), event-driven: D, OX, OI, G as inputs get ready
-//   warps 2-9   state: thread = TMEM lane (z dimension) and half of the 128 columns;
+//   warp 1      issues the D MMAs, warp 2 the G and O MMAs (one thread each, in order)
+//   warps 4-11  state: thread = TMEM lane (z dimension) and half of the 128 columns;
 //               decays Z into its pieces (TMEM), adds D to the state, writes its pieces
-//   warps 10-13 output: G -> P (shared memory), O epilogue (stmatrix, TMA store)
-// Bound: 1 KiB of HBM traffic per token and head against about 1700 tensor cycles and
-// 1500 issue slots per chunk and SM; the loads are four chunks ahead.
+//   warps 12-15 output: G -> P (shared memory), O epilogue (stmatrix, TMA store)
+#include <type_traits>
+
 #include "tc_common.cuh"
 #include "decay_common.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kDtThreads = 448;
+constexpr int kDtThreads = 512;
 constexpr int kStages = 4;
 constexpr uint32_t kStageBytes = 6 * TILE;            // [X0][X1][Y0][Y1][Z0][Z1], 64 columns each
 
@@ -41,28 +42,29 @@ constexpr uint32_t kStageBytes = 6 * TILE;            // [X0][X1][Y0][Y1][Z0][Z1
 constexpr uint32_t T_D = 0;        // D^T, 128 fp32 columns
 constexpr uint32_t T_H = 128;      // H^T pieces: high at 128, low at 192 (64 packed columns each)
 constexpr uint32_t T_Z = 256;      // Z'^T pieces, 32 packed columns each
-constexpr uint32_t T_G = 352;      // G, then OI^T (G is read before the OI MMAs are issued)
-constexpr uint32_t T_OX = 416;     // OX^T
+constexpr uint32_t T_G = 352;
+constexpr uint32_t T_O = 416;
 constexpr uint32_t T_COLS = 512;
 
-constexpr uint32_t DOFF_P = kStages * kStageBytes;
-constexpr uint32_t DOFF_O = DOFF_P + TILE;
-constexpr uint32_t DOFF_TAB = DOFF_O + 2 * TILE;      // pw[0..64]; wtab[2][64]; gtab[2][64]
-constexpr uint32_t TAB_FLOATS = 68 + 4 * 64;
+constexpr uint32_t DOFF_P = kStages * kStageBytes;    // P pieces: high, low
+constexpr uint32_t DOFF_O = DOFF_P + 2 * TILE;
+constexpr uint32_t DOFF_TAB = DOFF_O + 2 * TILE;      // powers; per token: Z weights, O scales, P scales
+constexpr uint32_t TAB_PW = 0, TAB_W = 68, TAB_F = 68 + 128, TAB_C = 68 + 256, TAB_L = 68 + 3 * 128,
+                   TAB_SEG = TAB_L + 4, TAB_FLOATS = TAB_SEG + 16;
 constexpr uint32_t DOFF_BAR = DOFF_TAB + TAB_FLOATS * 4;
 enum : int {
     D_FULL = 0,                    // x4: tiles of a stage landed
-    D_EMPTY = 4,                   // x4: stage no longer read
+    D_EMPTY = 4,                   // x4: stage no longer read (both issuers)
     D_ZP = 8,                      // Z' pieces written, D of the chunk before read (8 warps)
     D_DFULL = 9,                   // D done
     D_HREADY = 10,                 // pieces of H written (8 warps)
-    D_XFULL = 11,                  // OX done
+    D_XFULL = 11,                  // H's share of O done
     D_GFULL = 12,                  // G done
     D_PREADY = 13,                 // P written, G read (4 warps)
-    D_OFULL = 14,                  // OX and OI done
-    D_OFREE = 15,                  // OX and OI read (4 warps)
-    D_DRAIN = 16,
-    D_NBAR = 17
+    D_OFULL = 14,                  // O done
+    D_OFREE = 15,                  // O read (4 warps)
+    D_DRAIN = 16,                  // x2: last MMAs of either issuer
+    D_NBAR = 18
 };
 constexpr uint32_t DOFF_MISC = DOFF_BAR + D_NBAR * 8;
 constexpr uint32_t D_SMEM = DOFF_MISC + 16 + 1024;
@@ -73,70 +75,114 @@ constexpr uint32_t IDD_G = idesc_bf16(64, 64, false, false);
 constexpr uint32_t IDD_OX = idesc_bf16(128, 64, false, false);
 constexpr uint32_t IDD_OI = idesc_bf16(128, 64, true, false);
 constexpr uint32_t IDD_D = idesc_bf16(128, 128, false, true);
+// Registers per thread: 512 x 128 at launch; the first warpgroup gives most of its share to
+// the two that hold the state (a spilled register is an L2 round trip here, because the
+// shared memory leaves no L1): 128 x (56 + 2 x 168 + 112) = 64512 <= 65536.
+constexpr int kRegsIssue = 56, kRegsState = 168, kRegsOut = 112;
+constexpr double kScaleFloor = -69.31471805599453;    // log of 2^-100
+
+template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Two fp32 operations per instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 
 struct DecayCtl {
     uint64_t *bar;
     volatile int *abort_flag;
+    // One thread.  (Inlined and short: a call would not let ptxas give the roles their own
+    // register counts.)  A try suspends for up to 20 us, so the limit is about two seconds.
+    __device__ __forceinline__ bool wait_one(int i, uint32_t parity) const {
+        if (mbar_try_wait(&bar[i], parity)) return true;
+#pragma unroll 1
+        for (int k = 0; k < 100000; ++k) {
+            if (mbar_try_wait_suspend(&bar[i], parity, 20000)) return true;
+            if (*abort_flag) return false;
+        }
+        *abort_flag = 1;
+        atomicOr(&g_tc_error, 1u);
+        return false;
+    }
     // All lanes of the warp wait; the answer is the same for all of them.  Roles that meet at
     // a named barrier agree on it there before any of them leaves.
     __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
-        const bool got = mbar_try_wait(&bar[i], parity) || wait_loop(i, parity);
-        return __all_sync(0xffffffffu, got);
-    }
-    __device__ __noinline__ bool wait_loop(int i, uint32_t parity) const {
-        const long long t0 = clock64();
-        for (;;) {
-            if (mbar_try_wait_suspend(&bar[i], parity, 20000)) return true;
-            if (*abort_flag) return false;
-            if (clock64() - t0 > (1ll << 32)) {
-                *abort_flag = 1;
-                atomicOr(&g_tc_error, 1u);
-                return false;
-            }
-        }
+        return __all_sync(0xffffffffu, wait_one(i, parity));
     }
 };
 
 // Upper 16 bits of two floats as a bf16 pair, and their exact remainders.
-__device__ __forceinline__ uint32_t split_pair(float &a, float &b) {
+__device__ __forceinline__ uint32_t split_pair(uint64_t &v) {
+    float a, b;
+    unpack2(v, a, b);
     const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-    a -= __uint_as_float(ua & 0xffff0000u);
-    b -= __uint_as_float(ub & 0xffff0000u);
+    v = sub2(v, pack2(__uint_as_float(ua & 0xffff0000u), __uint_as_float(ub & 0xffff0000u)));
     return __byte_perm(ua, ub, 0x7632);
+}
+// Upper 16 bits (the last of exact pieces), and rounded to bf16.
+__device__ __forceinline__ uint32_t high_pair(uint64_t v) {
+    float a, b;
+    unpack2(v, a, b);
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ uint32_t round_pair(uint64_t v) {
+    float a, b;
+    unpack2(v, a, b);
+    return pack_bf16x2(a, b);
 }
 
 // Rows of O from the accumulators one column (token) at a time: ragged chunks of packed
 // sequences, and fp32 partial rows (a warp writes 32 consecutive values of a row).
 template <typename OT>
-__device__ __noinline__ void store_rows(OT *dst, uint32_t t_lane, const float *gt, int rows, size_t stride) {
+__device__ __forceinline__ void store_rows(OT *dst, uint32_t t_lane, const float *gt, int rows, size_t stride) {
 #pragma unroll 1
     for (int r0 = 0; r0 < C; r0 += 32) {
-        float x[32], y[32];
-        tmem_ld32(t_lane + T_OX + r0, x);
-        tmem_ld32(t_lane + T_G + r0, y);
+        float x[32];
+        tmem_ld32(t_lane + T_O + r0, x);
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 32; ++e)
-            if (r0 + e < rows) dst[(size_t)(r0 + e) * stride] = from_f32<OT>(fmaf(gt[r0 + e], x[e], y[e]));
+            if (r0 + e < rows) dst[(size_t)(r0 + e) * stride] = from_f32<OT>(gt[r0 + e] * x[e]);
     }
 }
 
+template <bool STATE_ONLY, int NZ>
 __global__ void __launch_bounds__(kDtThreads, 1)
 decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
                 const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_o,
-                const DecayWalk w, const int state_only)
+                const DecayWalk w)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + DOFF_BAR);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + DOFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + DOFF_MISC + 4);
-    float *pw = reinterpret_cast<float *>(sm + DOFF_TAB);   // lambda^0 .. lambda^64
-    float *wtab = pw + 68, *gtab = wtab + 128;               // [0]: full chunks, [1]: the special one
+    float *tab = reinterpret_cast<float *>(sm + DOFF_TAB);
     const DecayCtl ctl{bar, abort_flag};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x;
-    const WalkSpan sp = walk_span(w, blockIdx.y, state_only != 0);
+    const WalkSpan sp = walk_span(w, blockIdx.y, STATE_ONLY);
     const int n = sp.c1 - sp.c0;                             // chunks of this CTA
     const uint32_t sbase = smem_u32(sm);
     const size_t hstate = (size_t)kHeadDim * kHeadDim;
@@ -145,15 +191,17 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
     // whose end state may be wanted undecayed.  It is the walk's last (forwards) or first (backwards).
     const int special = w.rev ? 0 : sp.nchunks - 1;
     const int tail = sp.L - (sp.nchunks - 1) * C;
-    const int back = (w.fin_back && !state_only) ? 1 : 0;
+    const int back = (w.fin_back && !STATE_ONLY) ? 1 : 0;
     const double loglam = decay_log(w.decay[h]);
+    const bool strong = 63.0 * loglam < kScaleFloor;         // lambda^63 below the scales' floor
 
     if (tid == 0) {
-        if (!state_only) { prefetch_tensormap(&tm_x); prefetch_tensormap(&tm_o); }
+        if (!STATE_ONLY) { prefetch_tensormap(&tm_x); prefetch_tensormap(&tm_o); }
         prefetch_tensormap(&tm_y);
         prefetch_tensormap(&tm_z);
         for (int i = 0; i < (int)D_NBAR; ++i)
-            mbar_init(&bar[i], i == D_ZP || i == D_HREADY ? 8 : i == D_PREADY || i == D_OFREE ? 4 : 1);
+            mbar_init(&bar[i], i == D_ZP || i == D_HREADY ? 8 : i == D_PREADY || i == D_OFREE ? 4
+                               : i >= D_EMPTY && i < D_EMPTY + kStages && !STATE_ONLY ? 2 : 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -161,45 +209,58 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
         tmem_alloc(tmem_slot, T_COLS);
         tmem_relinquish();
     }
-    for (int i = tid - 64; i >= 0 && i < 65 + 256; i += kDtThreads) {
+    // tables: [0] of each pair for full chunks, [1] for the special one
+    for (int i = tid - 32; i >= 0 && i < 65 + 3 * 128; i += kDtThreads - 32) {
+        double e;
+        uint32_t at;
         if (i < 65) {
-            pw[i] = (float)decay_pow(loglam, i);
+            e = i;
+            at = TAB_PW + i;
         } else {
-            const int t = (i - 65) & 63, which = (i - 65) >> 6;          // w full, w special, g full, g special
+            const int t = (i - 65) & 63, which = (i - 65) >> 6;          // w, w', f, f', c, c'
             const int L = (which & 1) ? tail : C, bk = (which & 1) ? back : 0;
-            int e;
-            if (which < 2) e = w.rev ? t + 1 : L - t - bk;
-            else e = w.rev ? L - 1 - t : t;
-            (which < 2 ? wtab : gtab)[(which & 1) * 64 + t] = (float)decay_pow(loglam, max(e, 0));
+            const int p = w.rev ? L - 1 - t : t;                         // tokens since the chunk's start
+            e = which < 2 ? max(L - p - bk, 0) : which < 4 ? p : -p;
+            at = TAB_W + (i - 65);
+            if (which >= 2 && which < 4) e = fmin(e, kScaleFloor / loglam);   // loglam < 0 or 0: +-inf
         }
+        tab[at] = (float)decay_pow(loglam, e);
+    }
+    if (tid < 18 && tid >= 2) {      // decay of segment tid - 2's start state up to this segment
+        const int g = tid - 2, here = tokens_before(sp, w.rev, sp.c0);
+        if (w.nseg > 1 && g <= sp.seg)
+            tab[TAB_SEG + g] = (float)decay_pow(loglam, here - tokens_before(sp, w.rev, g * w.seg_chunks));
+    } else if (tid < 2) {            // lambda^L of full chunks and of the special one, in two floats
+        const double p = decay_pow(loglam, tid ? tail - back : C);
+        tab[TAB_L + 2 * tid] = (float)p;
+        tab[TAB_L + 2 * tid + 1] = (float)(p - (double)(float)p);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 0) {
-        // ======================================================== TMA producer
-        if (lane == 0) {
+    // Every warpgroup changes its share, whether or not it has work below: the state's increase
+    // waits for the others' decrease.
+    if (warp < 4) {
+        regs_dec<kRegsIssue>();
+        if (warp == 0 && lane == 0) {
+            // ==================================================== TMA producer
             const int hx = h / (w.Hv / w.hx), hy = h / (w.Hv / w.hy), hz = h / (w.Hv / w.hz);
             int c = 0;
             for (; c < n; ++c) {
                 const int s = c % kStages;
-                if (c >= kStages) {
-                    bool got = mbar_try_wait(&bar[D_EMPTY + s], ((c / kStages) - 1) & 1) ||
-                               ctl.wait_loop(D_EMPTY + s, ((c / kStages) - 1) & 1);
-                    if (!got) break;
-                }
+                if (c >= kStages && !ctl.wait_one(D_EMPTY + s, ((c / kStages) - 1) & 1)) break;
                 int t0;
                 chunk_rows(sp, w.rev, sp.c0 + c, t0);
                 unsigned char *st = sm + s * kStageBytes;
                 uint64_t *full = &bar[D_FULL + s];
-                mbar_arrive_expect_tx(full, state_only ? 4 * TILE : kStageBytes);
+                mbar_arrive_expect_tx(full, STATE_ONLY ? 4 * TILE : kStageBytes);
                 tma_load_4d(st + 2 * TILE, &tm_y, full, 0, hy, t0, sp.bt);
                 tma_load_4d(st + 3 * TILE, &tm_y, full, 64, hy, t0, sp.bt);
                 tma_load_4d(st + 4 * TILE, &tm_z, full, 0, hz, t0, sp.bt);
                 tma_load_4d(st + 5 * TILE, &tm_z, full, 64, hz, t0, sp.bt);
-                if (!state_only) {
+                if (!STATE_ONLY) {
                     tma_load_4d(st + 0 * TILE, &tm_x, full, 0, hx, t0, sp.bt);
                     tma_load_4d(st + 1 * TILE, &tm_x, full, 64, hx, t0, sp.bt);
                 }
@@ -209,207 +270,201 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                 for (int i = max(0, c - kStages); i < c; ++i)
                     mbar_wait(&bar[D_FULL + i % kStages], (i / kStages) & 1, 1ll << 28);
         }
-    } else if (warp == 1) {
-        // ======================================================== MMA issuer
-        if (lane == 0) {
-            int ng = 0, nd = 0, nx = 0, np = 0, ne = 0;
-            if (state_only) ng = nx = np = n;
-            long long idle_since = clock64();
-            while (nd < n || np < n || nx < n) {
-                if (*abort_flag) break;
-                bool issued = false;
-                if (nd < n && mbar_test(&bar[D_ZP], nd & 1)) {
-                    // Z' written implies its tiles landed and D of the chunk before read
-                    const uint32_t st = sbase + (nd % kStages) * kStageBytes;
-                    tc_fence_after();
+        if (warp == 1 && lane == 0) {
+            // ==================================================== MMA issuer: D
+            for (int c = 0; c < n; ++c) {
+                // Z' written: its tiles have landed and D of the chunk before has been read
+                if (!ctl.wait_one(D_ZP, c & 1)) break;
+                const uint32_t st = sbase + (c % kStages) * kStageBytes;
+                tc_fence_after();
 #pragma unroll
-                    for (int pc = 2; pc >= 0; --pc)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16_ts(tmem + T_D, tmem + T_Z + pc * 32 + k * 8,
-                                        smem_desc_sw128(st + 2 * TILE + k * 2048, TILE, 1024), IDD_D, pc < 2 || k > 0);
-                    mma_commit(&bar[D_DFULL]);
-                    ++nd;
-                    issued = true;
-                } else if (np < ng && mbar_test(&bar[D_PREADY], np & 1)) {
-                    const uint32_t st = sbase + (np % kStages) * kStageBytes;
-                    tc_fence_after();
+                for (int pc = NZ - 1; pc >= 0; --pc)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_bf16(tmem + T_G, smem_desc_sw128(st + 4 * TILE + k * 2048, TILE, 1024),
-                                 smem_desc_sw128(sbase + DOFF_P + k * 32, 16, 1024), IDD_OI, k > 0);
-                    ++np;
-                    if (nx >= np) mma_commit(&bar[D_OFULL]);
-                    issued = true;
-                } else if (nx < n && mbar_test(&bar[D_HREADY], nx & 1) &&
-                           mbar_test(&bar[D_FULL + nx % kStages], (nx / kStages) & 1) &&
-                           (nx < 1 || mbar_test(&bar[D_OFREE], (nx - 1) & 1))) {
-                    const uint32_t st = sbase + (nx % kStages) * kStageBytes;
-                    tc_fence_after();
-#pragma unroll
-                    for (int pc = 1; pc >= 0; --pc)
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma_bf16_ts(tmem + T_OX, tmem + T_H + pc * 64 + k * 8,
-                                        smem_desc_sw128(st + (k >> 2) * TILE + (k & 3) * 32, 16, 1024), IDD_OX,
-                                        pc < 1 || k > 0);
-                    mma_commit(&bar[D_XFULL]);
-                    ++nx;
-                    if (np >= nx) mma_commit(&bar[D_OFULL]);
-                    issued = true;
-                } else if (ng < n && mbar_test(&bar[D_FULL + ng % kStages], (ng / kStages) & 1) &&
-                           (ng < 1 || mbar_test(&bar[D_OFREE], (ng - 1) & 1)) &&
-                           // rows past a packed sequence's end are zeroed before Z' is announced
-                           (!w.cu_seqlens || ng < nd)) {
-                    const uint32_t st = sbase + (ng % kStages) * kStageBytes;
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t koff = (k >> 2) * TILE + (k & 3) * 32;
-                        mma_bf16(tmem + T_G, smem_desc_sw128(st + koff, 16, 1024),
-                                 smem_desc_sw128(st + 2 * TILE + koff, 16, 1024), IDD_G, k > 0);
-                    }
-                    mma_commit(&bar[D_GFULL]);
-                    ++ng;
-                    issued = true;
-                }
-                while (ne < nd && ne < np && ne < nx) {          // every read of the stage is issued
-                    mma_commit(&bar[D_EMPTY + ne % kStages]);
-                    ++ne;
-                }
-                if (issued) {
-                    idle_since = clock64();
-                } else {
-                    __nanosleep(32);
-                    if (clock64() - idle_since > (1ll << 32)) {
-                        *abort_flag = 1;
-                        atomicOr(&g_tc_error, 1u);
-                        break;
-                    }
-                }
+                        mma_bf16_ts(tmem + T_D, tmem + T_Z + pc * 32 + k * 8,
+                                    smem_desc_sw128(st + 2 * TILE + k * 2048, TILE, 1024), IDD_D,
+                                    pc < NZ - 1 || k > 0);
+                mma_commit(&bar[D_DFULL]);
+                mma_commit(&bar[D_EMPTY + c % kStages]);
             }
             mma_commit(&bar[D_DRAIN]);
             mbar_wait(&bar[D_DRAIN], 0, 1ll << 30);
         }
-    } else if (warp < 10) {
+        if (!STATE_ONLY && warp == 2 && lane == 0) {
+            // ==================================================== MMA issuer: G and O
+            for (int c = 0; c < n; ++c) {
+                const int s = c % kStages;
+                const uint32_t st = sbase + s * kStageBytes;
+                // rows past a packed sequence's end are zeroed before Z' is announced
+                if (!ctl.wait_one(D_FULL + s, (c / kStages) & 1)) break;
+                if (w.cu_seqlens && sp.c0 + c == special && !ctl.wait_one(D_ZP, c & 1)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t koff = (k >> 2) * TILE + (k & 3) * 32;
+                    mma_bf16(tmem + T_G, smem_desc_sw128(st + koff, 16, 1024),
+                             smem_desc_sw128(st + 2 * TILE + koff, 16, 1024), IDD_G, k > 0);
+                }
+                mma_commit(&bar[D_GFULL]);
+                if (!ctl.wait_one(D_HREADY, c & 1)) break;
+                if (c > 0 && !ctl.wait_one(D_OFREE, (c - 1) & 1)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int pc = 1; pc >= 0; --pc)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_bf16_ts(tmem + T_O, tmem + T_H + pc * 64 + k * 8,
+                                    smem_desc_sw128(st + (k >> 2) * TILE + (k & 3) * 32, 16, 1024), IDD_OX,
+                                    pc < 1 || k > 0);
+                mma_commit(&bar[D_XFULL]);
+                if (!ctl.wait_one(D_PREADY, c & 1)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int pc = 1; pc >= 0; --pc)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16(tmem + T_O, smem_desc_sw128(st + 4 * TILE + k * 2048, TILE, 1024),
+                                 smem_desc_sw128(sbase + DOFF_P + pc * TILE + k * 32, 16, 1024), IDD_OI, true);
+                mma_commit(&bar[D_OFULL]);
+                mma_commit(&bar[D_EMPTY + s]);
+            }
+            mma_commit(&bar[D_DRAIN + 1]);
+            mbar_wait(&bar[D_DRAIN + 1], 0, 1ll << 30);
+        }
+    } else if (warp < 12) {
         // ======================================================== state
-        const int q4 = warp & 3, hf = (warp - 2) >> 2;
+        regs_inc<kRegsState>();
+        const int q4 = warp & 3, hf = (warp - 4) >> 2;
         const int dz = q4 * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(q4 * 32) << 16);
-        float H[64];                                         // H^T[dz][64 hf + e]
+        uint64_t H[32];                                      // H^T[dz][64 hf + 2 e], +1
 #pragma unroll
-        for (int e = 0; e < 64; ++e) H[e] = 0.f;
-        if (w.nseg > 1 && !state_only) {
-            const int here = tokens_before(sp, w.rev, sp.c0);
+        for (int e = 0; e < 32; ++e) H[e] = 0;
+        if (w.nseg > 1 && !STATE_ONLY) {
 #pragma unroll 1
             for (int g = 0; g <= sp.seg; ++g) {
-                const float f = (float)decay_pow(loglam, here - tokens_before(sp, w.rev, g * w.seg_chunks));
+                const float f = tab[TAB_SEG + g];
                 const float *src = w.seg + (((size_t)sp.b * w.nseg + g) * w.Hv + h) * hstate + (size_t)64 * hf * kHeadDim + dz;
 #pragma unroll
-                for (int e = 0; e < 64; ++e) H[e] = fmaf(f, src[(size_t)e * kHeadDim], H[e]);
+                for (int e = 0; e < 32; ++e)
+                    H[e] = fma2(pack2(f, f), pack2(src[(size_t)(2 * e) * kHeadDim], src[(size_t)(2 * e + 1) * kHeadDim]), H[e]);
             }
-        } else if (w.init && (!state_only || sp.copy_init)) {
-            const float f = (w.init_decays && sp.L > 0) ? pw[1] : 1.f;
+        } else if (w.init && (!STATE_ONLY || sp.copy_init)) {
+            const float f = (w.init_decays && sp.L > 0) ? tab[TAB_PW + 1] : 1.f;
             const float *src = w.init + ((size_t)sp.b * w.Hv + h) * hstate;
             if (w.init_trans) {
                 const float4 *row = reinterpret_cast<const float4 *>(src + (size_t)dz * kHeadDim + 64 * hf);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const float4 v = row[e];
-                    H[4 * e] = f * v.x; H[4 * e + 1] = f * v.y; H[4 * e + 2] = f * v.z; H[4 * e + 3] = f * v.w;
+                    H[2 * e] = pack2(f * v.x, f * v.y);
+                    H[2 * e + 1] = pack2(f * v.z, f * v.w);
                 }
             } else {
 #pragma unroll
-                for (int e = 0; e < 64; ++e) H[e] = f * src[(size_t)(64 * hf + e) * kHeadDim + dz];
+                for (int e = 0; e < 32; ++e) {
+                    const float *at = src + (size_t)(64 * hf + 2 * e) * kHeadDim + dz;
+                    H[e] = pack2(f * at[0], f * at[kHeadDim]);
+                }
             }
         }
         auto write_pieces = [&]() {
 #pragma unroll
-            for (int e0 = 0; e0 < 64; e0 += 32) {
+            for (int e0 = 0; e0 < 32; e0 += 16) {
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    float a = H[e0 + 2 * e], b = H[e0 + 2 * e + 1];
-                    hi[e] = split_pair(a, b);
-                    lo[e] = pack_bf16x2(a, b);
+                    uint64_t v = H[e0 + e];
+                    hi[e] = split_pair(v);
+                    lo[e] = round_pair(v);
                 }
-                tmem_st16u(t_lane + T_H + 32 * hf + (e0 >> 1), hi);
-                tmem_st16u(t_lane + T_H + 64 + 32 * hf + (e0 >> 1), lo);
+                tmem_st16u(t_lane + T_H + 32 * hf + e0, hi);
+                tmem_st16u(t_lane + T_H + 64 + 32 * hf + e0, lo);
             }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[D_HREADY]);
         };
-        // Z'^T pieces of this thread's 32 tokens, from column dz of the Z tile
-        auto write_z = [&](int c) -> bool {
+        // Z'^T pieces of this thread's 32 tokens, from column dz of the Z tile, in registers
+        uint32_t zp[NZ][16];
+        auto make_z = [&](int c) -> bool {
             const int s = c % kStages;
             if (!ctl.wait(D_FULL + s, (c / kStages) & 1)) return false;
             unsigned char *st = sm + s * kStageBytes;
             int t0;
             const int cw = sp.c0 + c, rows = chunk_rows(sp, w.rev, cw, t0);
             if (w.cu_seqlens && rows < C) {                  // the next sequence's rows: out of the products
-                for (int i = tid - 64; i < (C - rows) * 4 * 8; i += 256) {
+                for (int i = tid - 128; i < (C - rows) * 4 * 8; i += 256) {
                     const int r = rows + (i >> 5), tile = (i >> 3) & 3, ch = i & 7;
                     *reinterpret_cast<uint4 *>(st + (2 + tile) * TILE + r * 128 + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
             }
-            const float *wt = wtab + (cw == special ? 64 : 0) + 32 * hf;
-            const unsigned char *zt = st + (4 + (dz >> 6)) * TILE;
-            const uint32_t zc = (dz & 63) >> 3, zb = (dz & 7) * 2;
+            const float *wt = tab + TAB_W + (cw == special ? 64 : 0) + 32 * hf;
+            const unsigned char *zt = st + (4 + (dz >> 6)) * TILE + (32 * hf) * 128;
+            const uint32_t zc = ((dz & 63) >> 3) << 4, zb = (dz & 7) * 2;
 #pragma unroll
-            for (int b0 = 0; b0 < 32; b0 += 16) {
-                uint32_t p0[8], p1[8], p2[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int t = 32 * hf + b0 + 2 * e;
-                    const float2 ww = *reinterpret_cast<const float2 *>(wt + b0 + 2 * e);
-                    const uint32_t ua = *reinterpret_cast<const uint16_t *>(zt + t * 128 + ((zc ^ (t & 7)) << 4) + zb);
-                    const uint32_t ub = *reinterpret_cast<const uint16_t *>(zt + (t + 1) * 128 + ((zc ^ ((t + 1) & 7)) << 4) + zb);
-                    float a = t < rows ? ww.x * __uint_as_float(ua << 16) : 0.f;
-                    float b = t + 1 < rows ? ww.y * __uint_as_float(ub << 16) : 0.f;
-                    p0[e] = split_pair(a, b);
-                    p1[e] = split_pair(a, b);
-                    p2[e] = split_pair(a, b);
-                }
-                const uint32_t col = t_lane + T_Z + 16 * hf + (b0 >> 1);
-                tmem_st8u(col, p0);
-                tmem_st8u(col + 32, p1);
-                tmem_st8u(col + 64, p2);
+            for (int e = 0; e < 16; ++e) {
+                const int t = 2 * e;
+                const float2 ww = *reinterpret_cast<const float2 *>(wt + t);
+                const uint32_t ua = *reinterpret_cast<const uint16_t *>(zt + t * 128 + ((zc ^ ((t & 7) << 4)) + zb));
+                const uint32_t ub = *reinterpret_cast<const uint16_t *>(zt + (t + 1) * 128 + ((zc ^ (((t + 1) & 7) << 4)) + zb));
+                uint64_t v = mul2(pack2(ww.x, ww.y), pack2(__uint_as_float(ua << 16), __uint_as_float(ub << 16)));
+                zp[0][e] = split_pair(v);
+                if (NZ == 3) zp[1][e] = split_pair(v);
+                zp[NZ - 1][e] = NZ == 3 ? high_pair(v) : round_pair(v);
             }
+            if (rows < C) {                                  // (a weight of zero would keep a NaN)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int left = rows - (32 * hf + 2 * e);
+                    const uint32_t keep = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+#pragma unroll
+                    for (int pc = 0; pc < NZ; ++pc) zp[pc][e] &= keep;
+                }
+            }
+            return true;
+        };
+        auto store_z = [&]() {
+#pragma unroll
+            for (int pc = 0; pc < NZ; ++pc) tmem_st16u(t_lane + T_Z + 32 * pc + 16 * hf, zp[pc]);
+        };
+        auto announce_z = [&]() {
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[D_ZP]);
-            return true;
         };
         bool ok = true;
         if (n > 0) {
-            if (!state_only) write_pieces();
-            ok = write_z(0);
+            if (!STATE_ONLY) write_pieces();
+            ok = make_z(0);
+            if (ok) {
+                store_z();
+                announce_z();
+            }
         }
-        const double p64 = decay_pow(loglam, C), psp = decay_pow(loglam, tail - back);
-        const float fh = (float)p64, fl = (float)(p64 - (double)fh);
-        const float sh = (float)psp, sl = (float)(psp - (double)sh);
         for (int c = 0; c < n && ok; ++c) {
-            ok = ctl.wait(D_DFULL, c & 1);
-            if (!ok) break;
+            if (c + 1 < n && !(ok = make_z(c + 1))) break;   // while D of this chunk runs
+            if (!(ok = ctl.wait(D_DFULL, c & 1))) break;
             tc_fence_after();
+            if (c + 1 < n) store_z();
             const bool is_special = sp.c0 + c == special;
-            const float ph = is_special ? sh : fh, pl = is_special ? sl : fl;
+            const float2 pf = *reinterpret_cast<const float2 *>(tab + TAB_L + (is_special ? 2 : 0));
+            const uint64_t ph = pack2(pf.x, pf.x), pl = pack2(pf.y, pf.y);
 #pragma unroll
-            for (int e0 = 0; e0 < 64; e0 += 32) {
+            for (int e0 = 0; e0 < 32; e0 += 16) {
                 float d[32];
-                tmem_ld32(t_lane + T_D + 64 * hf + e0, d);
+                tmem_ld32(t_lane + T_D + 64 * hf + 2 * e0, d);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) H[e0 + e] = fmaf(ph, H[e0 + e], fmaf(pl, H[e0 + e], d[e]));
+                for (int e = 0; e < 16; ++e)
+                    H[e0 + e] = fma2(ph, H[e0 + e], fma2(pl, H[e0 + e], pack2(d[2 * e], d[2 * e + 1])));
             }
-            tc_fence_before();
             if (c + 1 < n) {
-                if (!(ok = write_z(c + 1))) break;
-                if (!state_only) {
+                announce_z();
+                if (!STATE_ONLY) {
                     if (!(ok = ctl.wait(D_XFULL, c & 1))) break;
                     tc_fence_after();
                     write_pieces();
@@ -417,21 +472,30 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             }
         }
         float *dst = nullptr;
-        if (state_only) dst = w.seg + (((size_t)sp.b * w.nseg + sp.seg) * w.Hv + h) * hstate;
+        if (STATE_ONLY) dst = w.seg + (((size_t)sp.b * w.nseg + sp.seg) * w.Hv + h) * hstate;
         else if (w.fin && sp.c1 == sp.nchunks) dst = w.fin + ((size_t)sp.b * w.Hv + h) * hstate;
         if (ok && dst) {
 #pragma unroll
-            for (int e = 0; e < 64; ++e) dst[(size_t)(64 * hf + e) * kHeadDim + dz] = H[e];
+            for (int e = 0; e < 32; ++e) {
+                float a, b;
+                unpack2(H[e], a, b);
+                float *at = dst + (size_t)(64 * hf + 2 * e) * kHeadDim + dz;
+                at[0] = a;
+                at[kHeadDim] = b;
+            }
         }
-    } else if (!state_only) {
+    } else {
         // ======================================================== output
+        regs_dec<kRegsOut>();
         const int q4 = warp & 3;
         const uint32_t t_lane = tmem + ((uint32_t)(q4 * 32) << 16);
-        const bool leader = tid == 320;
+        const bool leader = tid == 384;
         const int g = lane >> 2, t = lane & 3;
         const size_t stride = (size_t)w.Hv * kHeadDim;
         bool ok = true;
-        for (int c = 0; c < n && ok; ++c) {
+        for (int c = 0; c < n && ok && !STATE_ONLY; ++c) {
+            const int cw = sp.c0 + c;
+            const float *ct = tab + TAB_C + (cw == special ? 64 : 0), *ft = tab + TAB_F + (cw == special ? 64 : 0);
             // ---- G -> P: M = 64 accumulators sit in lanes 0-15 of every quarter
             if (!(ok = named_and(2, 128, ctl.wait(D_GFULL, c & 1)))) break;
             tc_fence_after();
@@ -441,19 +505,33 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                 tmem_ld16x256b_x4(t_lane + T_G + 32, rb);
                 tmem_wait_ld();
                 unsigned char *pt = sm + DOFF_P;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int i = 16 * q4 + g + 8 * half;
+                const int i0 = 16 * q4 + g;
+                auto make_p = [&](auto strong_tag) {
+                    const float r0 = strong_tag ? 1.f / ft[i0] : 0.f, r1 = strong_tag ? 1.f / ft[i0 + 8] : 0.f;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const uint32_t *rr = k < 4 ? ra : rb;
                         const int j = 8 * k + 2 * t, kk = k & 3;
-                        const int e = w.rev ? j - i : i - j, e1 = w.rev ? e + 1 : e - 1;
-                        const float a = e >= 0 ? pw[max(e, 0)] * __uint_as_float(rr[4 * kk + 2 * half]) : 0.f;
-                        const float b = e1 >= 0 ? pw[max(e1, 0)] * __uint_as_float(rr[4 * kk + 2 * half + 1]) : 0.f;
-                        *reinterpret_cast<uint32_t *>(pt + i * 128 + ((k ^ (i & 7)) << 4) + 4 * t) = pack_bf16x2(a, b);
+                        float2 sc = *reinterpret_cast<const float2 *>(ct + j);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const int i = i0 + 8 * half;
+                            const int e = w.rev ? j - i : i - j, e1 = w.rev ? e + 1 : e - 1;
+                            if (strong_tag) {
+                                const float r = half ? r1 : r0;
+                                sc.x = tab[TAB_PW + max(e, 0)] * r;
+                                sc.y = tab[TAB_PW + max(e1, 0)] * r;
+                            }
+                            uint64_t v = pack2(e >= 0 ? sc.x * __uint_as_float(rr[4 * kk + 2 * half]) : 0.f,
+                                               e1 >= 0 ? sc.y * __uint_as_float(rr[4 * kk + 2 * half + 1]) : 0.f);
+                            unsigned char *at = pt + i * 128 + ((k ^ (i & 7)) << 4) + 4 * t;
+                            *reinterpret_cast<uint32_t *>(at) = split_pair(v);
+                            *reinterpret_cast<uint32_t *>(at + TILE) = round_pair(v);
+                        }
                     }
-                }
+                };
+                if (strong) make_p(std::true_type{});
+                else make_p(std::false_type{});
             }
             fence_proxy_async_smem();
             tc_fence_before();
@@ -464,54 +542,52 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             if (!(ok = named_and(2, 128, ctl.wait(D_OFULL, c & 1)))) break;
             tc_fence_after();
             int t0;
-            const int cw = sp.c0 + c, rows = chunk_rows(sp, w.rev, cw, t0);
-            const float *gt = gtab + (cw == special ? 64 : 0);
-            const size_t at = ((size_t)sp.bt * w.T + t0) * stride + (size_t)h * kHeadDim + q4 * 32 + lane;
-            if (w.o_f32) {
-                store_rows(static_cast<float *>(w.o) + at, t_lane, gt, rows, stride);
-            } else if (rows < C && w.cu_seqlens) {
-                store_rows(static_cast<__nv_bfloat16 *>(w.o) + at, t_lane, gt, rows, stride);
-            } else {
-                const uint32_t stage = smem_u32(sm + DOFF_O);
-                const int mt = lane >> 3, mi = lane & 7;     // stored row mi of matrix mt
-#pragma unroll 1
-                for (int it = 0; it < 4; ++it) {             // 16-lane slab, 32-token block
-                    const int slab = it >> 1, cb = it & 1;
-                    uint32_t rx[16], ri[16];
-                    const uint32_t ta = t_lane + ((uint32_t)(16 * slab) << 16) + 32 * cb;
-                    tmem_ld16x256b_x4(ta + T_OX, rx);
-                    tmem_ld16x256b_x4(ta + T_G, ri);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk) {
-                        uint32_t m[4];
-#pragma unroll
-                        for (int mm = 0; mm < 4; ++mm) {
-                            const int k = 2 * kk + (mm >> 1), gg = mm & 1;
-                            const float2 gm = *reinterpret_cast<const float2 *>(gt + 32 * cb + 8 * k + 2 * t);
-                            m[mm] = pack_bf16x2(
-                                fmaf(gm.x, __uint_as_float(rx[4 * k + 2 * gg]), __uint_as_float(ri[4 * k + 2 * gg])),
-                                fmaf(gm.y, __uint_as_float(rx[4 * k + 2 * gg + 1]), __uint_as_float(ri[4 * k + 2 * gg + 1])));
-                        }
-                        const int k = 2 * kk + (mt >> 1), gg = mt & 1;
-                        const int orow = 32 * cb + 8 * k + mi;          // token
-                        const int jst = q4 * 32 + 16 * slab + 8 * gg;   // first z of the block
-                        stmatrix_x4_trans(stage + (jst >> 6) * TILE + sw128_chunk(orow, (jst & 63) >> 3),
-                                          m[0], m[1], m[2], m[3]);
-                    }
-                }
+            const int rows = chunk_rows(sp, w.rev, cw, t0);
+            if (w.o_f32 || (rows < C && w.cu_seqlens)) {
+                const size_t at = ((size_t)sp.bt * w.T + t0) * stride + (size_t)h * kHeadDim + q4 * 32 + lane;
+                if (w.o_f32) store_rows(static_cast<float *>(w.o) + at, t_lane, ft, rows, stride);
+                else store_rows(static_cast<__nv_bfloat16 *>(w.o) + at, t_lane, ft, rows, stride);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[D_OFREE]);
+                continue;
             }
+            uint32_t r[4][16];                               // 16-lane slab x 32-token block
+#pragma unroll
+            for (int it = 0; it < 4; ++it)
+                tmem_ld16x256b_x4(t_lane + ((uint32_t)(16 * (it >> 1)) << 16) + T_O + 32 * (it & 1), r[it]);
+            tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[D_OFREE]);
-            if (!w.o_f32 && !(rows < C && w.cu_seqlens)) {
-                fence_proxy_async_smem();
-                named_sync(2, 128);
-                if (leader) {
-                    tma_store_4d(&tm_o, sm + DOFF_O, 0, h, t0, sp.bt);
-                    tma_store_4d(&tm_o, sm + DOFF_O + TILE, 64, h, t0, sp.bt);
-                    bulk_commit_group();
+            const uint32_t stage = smem_u32(sm + DOFF_O);
+            const int mt = lane >> 3, mi = lane & 7;         // stored row mi of matrix mt
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const int slab = it >> 1, cb = it & 1;
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    uint32_t m[4];
+#pragma unroll
+                    for (int mm = 0; mm < 4; ++mm) {
+                        const int k = 2 * kk + (mm >> 1), gg = mm & 1;
+                        const float2 f = *reinterpret_cast<const float2 *>(ft + 32 * cb + 8 * k + 2 * t);
+                        m[mm] = round_pair(mul2(pack2(f.x, f.y), pack2(__uint_as_float(r[it][4 * k + 2 * gg]),
+                                                                       __uint_as_float(r[it][4 * k + 2 * gg + 1]))));
+                    }
+                    const int k = 2 * kk + (mt >> 1), gg = mt & 1;
+                    const int orow = 32 * cb + 8 * k + mi;          // token
+                    const int jst = q4 * 32 + 16 * slab + 8 * gg;   // first z of the block
+                    stmatrix_x4_trans(stage + (jst >> 6) * TILE + sw128_chunk(orow, (jst & 63) >> 3),
+                                      m[0], m[1], m[2], m[3]);
                 }
+            }
+            fence_proxy_async_smem();
+            named_sync(2, 128);
+            if (leader) {
+                tma_store_4d(&tm_o, sm + DOFF_O, 0, h, t0, sp.bt);
+                tma_store_4d(&tm_o, sm + DOFF_O + TILE, 64, h, t0, sp.bt);
+                bulk_commit_group();
             }
         }
         if (leader) bulk_wait_group0();
@@ -522,6 +598,18 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
         tc_fence_after();
         tmem_dealloc(tmem, T_COLS);
     }
+}
+
+template <bool STATE_ONLY, int NZ>
+cudaError_t launch_tc(const CUtensorMap &tx, const CUtensorMap &ty, const CUtensorMap &tz, const CUtensorMap &to,
+                      const DecayWalk &w, cudaStream_t stream)
+{
+    cudaError_t err = cudaFuncSetAttribute(decay_tc_kernel<STATE_ONLY, NZ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)D_SMEM);
+    if (err != cudaSuccess) return err;
+    decay_tc_kernel<STATE_ONLY, NZ><<<dim3((unsigned)w.Hv, (unsigned)(w.B * w.nseg)), kDtThreads, D_SMEM, stream>>>(
+        tx, ty, tz, to, w);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -544,15 +632,11 @@ cudaError_t launch_decay_walk_tc(const DecayWalk &w, cudaStream_t stream)
         return cudaErrorInvalidValue;
     if (w.o_f32) to = tx;                        // not used
     else if (!make_map(&to, w.o, rows_b, w.T, w.Hv)) return cudaErrorInvalidValue;
-    cudaError_t err = cudaFuncSetAttribute(decay_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)D_SMEM);
+    const bool ends = w.fin != nullptr;          // an end state is wanted: its increments with all 24 bits
+    cudaError_t err = cudaSuccess;
+    if (w.nseg > 1) err = ends ? launch_tc<true, 3>(tx, ty, tz, to, w, stream) : launch_tc<true, 2>(tx, ty, tz, to, w, stream);
     if (err != cudaSuccess) return err;
-    const dim3 grid((unsigned)w.Hv, (unsigned)(w.B * w.nseg));
-    if (w.nseg > 1) {
-        decay_tc_kernel<<<grid, kDtThreads, D_SMEM, stream>>>(tx, ty, tz, to, w, 1);
-        if ((err = cudaGetLastError()) != cudaSuccess) return err;
-    }
-    decay_tc_kernel<<<grid, kDtThreads, D_SMEM, stream>>>(tx, ty, tz, to, w, 0);
-    return cudaGetLastError();
+    return ends ? launch_tc<false, 3>(tx, ty, tz, to, w, stream) : launch_tc<false, 2>(tx, ty, tz, to, w, stream);
 }
 
 }  // namespace gdn
