@@ -22,10 +22,11 @@
 //
 // One CTA per (sequence or segment, V head), warp-specialised:
 //   warp 0      TMA producer: X, Y, Z tiles, four stages of 48 KB
-//   warp 1      issues the D MMAs, warp 2 the G and O MMAs (one thread each, in order)
+//   warp 1      issues the D MMAs, warp 2 the G and O MMAs (one elected thread each, in order)
 //   warps 4-11  state: thread = TMEM lane (z dimension) and half of the 128 columns;
 //               decays Z into its pieces (TMEM), adds D to the state, writes its pieces
-//   warps 12-15 output: G -> P (shared memory), O epilogue (stmatrix, TMA store)
+//   warps 12-15 G -> P (shared memory)
+//   warps 16-19 O epilogue (stmatrix, TMA store)
 #include <type_traits>
 
 #include "tc_common.cuh"
@@ -34,7 +35,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kDtThreads = 512;
+constexpr int kDtThreads = 640;
 constexpr int kStages = 4;
 constexpr uint32_t kStageBytes = 6 * TILE;            // [X0][X1][Y0][Y1][Z0][Z1], 64 columns each
 
@@ -75,10 +76,10 @@ constexpr uint32_t IDD_G = idesc_bf16(64, 64, false, false);
 constexpr uint32_t IDD_OX = idesc_bf16(128, 64, false, false);
 constexpr uint32_t IDD_OI = idesc_bf16(128, 64, true, false);
 constexpr uint32_t IDD_D = idesc_bf16(128, 128, false, true);
-// Registers per thread: 512 x 128 at launch; the first warpgroup gives most of its share to
-// the two that hold the state (a spilled register is an L2 round trip here, because the
-// shared memory leaves no L1): 128 x (56 + 2 x 168 + 112) = 64512 <= 65536.
-constexpr int kRegsIssue = 56, kRegsState = 168, kRegsOut = 112;
+// Registers per thread: 640 x 96 at launch; the warpgroups without state give part of their
+// share to the two that hold it (a spilled register is an L2 round trip here, because the
+// shared memory leaves no L1): 48 + 2 x 144 + 2 x 72 = 5 x 96.
+constexpr int kRegsIssue = 48, kRegsState = 144, kRegsOut = 72;
 constexpr double kScaleFloor = -69.31471805599453;    // log of 2^-100
 
 template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -270,66 +271,84 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                 for (int i = max(0, c - kStages); i < c; ++i)
                     mbar_wait(&bar[D_FULL + i % kStages], (i / kStages) & 1, 1ll << 28);
         }
-        if (warp == 1 && lane == 0) {
+        if (warp == 1) {
             // ==================================================== MMA issuer: D
             for (int c = 0; c < n; ++c) {
                 // Z' written: its tiles have landed and D of the chunk before has been read
-                if (!ctl.wait_one(D_ZP, c & 1)) break;
+                if (!ctl.wait(D_ZP, c & 1)) break;
                 const uint32_t st = sbase + (c % kStages) * kStageBytes;
                 tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int pc = NZ - 1; pc >= 0; --pc)
+                    for (int pc = NZ - 1; pc >= 0; --pc)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_bf16_ts(tmem + T_D, tmem + T_Z + pc * 32 + k * 8,
-                                    smem_desc_sw128(st + 2 * TILE + k * 2048, TILE, 1024), IDD_D,
-                                    pc < NZ - 1 || k > 0);
-                mma_commit(&bar[D_DFULL]);
-                mma_commit(&bar[D_EMPTY + c % kStages]);
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16_ts(tmem + T_D, tmem + T_Z + pc * 32 + k * 8,
+                                        smem_desc_sw128(st + 2 * TILE + k * 2048, TILE, 1024), IDD_D,
+                                        pc < NZ - 1 || k > 0);
+                    mma_commit(&bar[D_DFULL]);
+                    mma_commit(&bar[D_EMPTY + c % kStages]);
+                }
+                __syncwarp();
             }
-            mma_commit(&bar[D_DRAIN]);
-            mbar_wait(&bar[D_DRAIN], 0, 1ll << 30);
+            if (elect_one()) {
+                mma_commit(&bar[D_DRAIN]);
+                mbar_wait(&bar[D_DRAIN], 0, 1ll << 30);
+            }
+            __syncwarp();
         }
-        if (!STATE_ONLY && warp == 2 && lane == 0) {
+        if (!STATE_ONLY && warp == 2) {
             // ==================================================== MMA issuer: G and O
             for (int c = 0; c < n; ++c) {
                 const int s = c % kStages;
                 const uint32_t st = sbase + s * kStageBytes;
                 // rows past a packed sequence's end are zeroed before Z' is announced
-                if (!ctl.wait_one(D_FULL + s, (c / kStages) & 1)) break;
-                if (w.cu_seqlens && sp.c0 + c == special && !ctl.wait_one(D_ZP, c & 1)) break;
+                if (!ctl.wait(D_FULL + s, (c / kStages) & 1)) break;
+                if (w.cu_seqlens && sp.c0 + c == special && !ctl.wait(D_ZP, c & 1)) break;
                 tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t koff = (k >> 2) * TILE + (k & 3) * 32;
-                    mma_bf16(tmem + T_G, smem_desc_sw128(st + koff, 16, 1024),
-                             smem_desc_sw128(st + 2 * TILE + koff, 16, 1024), IDD_G, k > 0);
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t koff = (k >> 2) * TILE + (k & 3) * 32;
+                        mma_bf16(tmem + T_G, smem_desc_sw128(st + koff, 16, 1024),
+                                 smem_desc_sw128(st + 2 * TILE + koff, 16, 1024), IDD_G, k > 0);
+                    }
+                    mma_commit(&bar[D_GFULL]);
                 }
-                mma_commit(&bar[D_GFULL]);
-                if (!ctl.wait_one(D_HREADY, c & 1)) break;
-                if (c > 0 && !ctl.wait_one(D_OFREE, (c - 1) & 1)) break;
+                __syncwarp();
+                if (!ctl.wait(D_HREADY, c & 1)) break;
+                if (c > 0 && !ctl.wait(D_OFREE, (c - 1) & 1)) break;
                 tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int pc = 1; pc >= 0; --pc)
+                    for (int pc = 1; pc >= 0; --pc)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_bf16_ts(tmem + T_O, tmem + T_H + pc * 64 + k * 8,
-                                    smem_desc_sw128(st + (k >> 2) * TILE + (k & 3) * 32, 16, 1024), IDD_OX,
-                                    pc < 1 || k > 0);
-                mma_commit(&bar[D_XFULL]);
-                if (!ctl.wait_one(D_PREADY, c & 1)) break;
+                        for (int k = 0; k < 8; ++k)
+                            mma_bf16_ts(tmem + T_O, tmem + T_H + pc * 64 + k * 8,
+                                        smem_desc_sw128(st + (k >> 2) * TILE + (k & 3) * 32, 16, 1024), IDD_OX,
+                                        pc < 1 || k > 0);
+                    mma_commit(&bar[D_XFULL]);
+                }
+                __syncwarp();
+                if (!ctl.wait(D_PREADY, c & 1)) break;
                 tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int pc = 1; pc >= 0; --pc)
+                    for (int pc = 1; pc >= 0; --pc)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_bf16(tmem + T_O, smem_desc_sw128(st + 4 * TILE + k * 2048, TILE, 1024),
-                                 smem_desc_sw128(sbase + DOFF_P + pc * TILE + k * 32, 16, 1024), IDD_OI, true);
-                mma_commit(&bar[D_OFULL]);
-                mma_commit(&bar[D_EMPTY + s]);
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16(tmem + T_O, smem_desc_sw128(st + 4 * TILE + k * 2048, TILE, 1024),
+                                     smem_desc_sw128(sbase + DOFF_P + pc * TILE + k * 32, 16, 1024), IDD_OI, true);
+                    mma_commit(&bar[D_OFULL]);
+                    mma_commit(&bar[D_EMPTY + s]);
+                }
+                __syncwarp();
             }
-            mma_commit(&bar[D_DRAIN + 1]);
-            mbar_wait(&bar[D_DRAIN + 1], 0, 1ll << 30);
+            if (elect_one()) {
+                mma_commit(&bar[D_DRAIN + 1]);
+                mbar_wait(&bar[D_DRAIN + 1], 0, 1ll << 30);
+            }
+            __syncwarp();
         }
     } else if (warp < 12) {
         // ======================================================== state
@@ -454,12 +473,12 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             const float2 pf = *reinterpret_cast<const float2 *>(tab + TAB_L + (is_special ? 2 : 0));
             const uint64_t ph = pack2(pf.x, pf.x), pl = pack2(pf.y, pf.y);
 #pragma unroll
-            for (int e0 = 0; e0 < 32; e0 += 16) {
-                float d[32];
-                tmem_ld32(t_lane + T_D + 64 * hf + 2 * e0, d);
+            for (int e0 = 0; e0 < 32; e0 += 8) {
+                float d[16];
+                tmem_ld16(t_lane + T_D + 64 * hf + 2 * e0, d);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
+                for (int e = 0; e < 8; ++e)
                     H[e0 + e] = fma2(ph, H[e0 + e], fma2(pl, H[e0 + e], pack2(d[2 * e], d[2 * e + 1])));
             }
             if (c + 1 < n) {
@@ -484,65 +503,79 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                 at[kHeadDim] = b;
             }
         }
-    } else {
-        // ======================================================== output
+    } else if (warp < 16) {
+        // ======================================================== P
         regs_dec<kRegsOut>();
         const int q4 = warp & 3;
         const uint32_t t_lane = tmem + ((uint32_t)(q4 * 32) << 16);
-        const bool leader = tid == 384;
-        const int g = lane >> 2, t = lane & 3;
-        const size_t stride = (size_t)w.Hv * kHeadDim;
-        bool ok = true;
-        for (int c = 0; c < n && ok && !STATE_ONLY; ++c) {
-            const int cw = sp.c0 + c;
-            const float *ct = tab + TAB_C + (cw == special ? 64 : 0), *ft = tab + TAB_F + (cw == special ? 64 : 0);
-            // ---- G -> P: M = 64 accumulators sit in lanes 0-15 of every quarter
-            if (!(ok = named_and(2, 128, ctl.wait(D_GFULL, c & 1)))) break;
+        const int g = lane >> 2, t = lane & 3, i0 = 16 * q4 + g;         // rows i0, i0 + 8
+        unsigned char *pt = sm + DOFF_P + i0 * 128 + 4 * t;
+        for (int c = 0; c < n && !STATE_ONLY; ++c) {
+            const bool sp_c = sp.c0 + c == special;
+            const float *ct = tab + TAB_C + (sp_c ? 64 : 0), *ft = tab + TAB_F + (sp_c ? 64 : 0);
+            // M = 64 accumulators sit in lanes 0-15 of every quarter
+            if (!ctl.wait(D_GFULL, c & 1)) break;
             tc_fence_after();
-            {
-                uint32_t ra[16], rb[16];
-                tmem_ld16x256b_x4(t_lane + T_G, ra);
-                tmem_ld16x256b_x4(t_lane + T_G + 32, rb);
-                tmem_wait_ld();
-                unsigned char *pt = sm + DOFF_P;
-                const int i0 = 16 * q4 + g;
-                auto make_p = [&](auto strong_tag) {
-                    const float r0 = strong_tag ? 1.f / ft[i0] : 0.f, r1 = strong_tag ? 1.f / ft[i0 + 8] : 0.f;
+            uint32_t r[32];
+            tmem_ld16x256b_x4(t_lane + T_G, r);
+            tmem_ld16x256b_x4(t_lane + T_G + 32, r + 16);
+            tmem_wait_ld();
+            auto make_p = [&](auto strong_tag) {             // r: pieces of P in place of G
+                const float r0 = strong_tag ? 1.f / ft[i0] : 0.f, r1 = strong_tag ? 1.f / ft[i0 + 8] : 0.f;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t *rr = k < 4 ? ra : rb;
-                        const int j = 8 * k + 2 * t, kk = k & 3;
-                        float2 sc = *reinterpret_cast<const float2 *>(ct + j);
+                for (int k = 0; k < 8; ++k) {
+                    const int j = 8 * k + 2 * t;
+                    float2 sc = *reinterpret_cast<const float2 *>(ct + j);
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const int i = i0 + 8 * half;
-                            const int e = w.rev ? j - i : i - j, e1 = w.rev ? e + 1 : e - 1;
-                            if (strong_tag) {
-                                const float r = half ? r1 : r0;
-                                sc.x = tab[TAB_PW + max(e, 0)] * r;
-                                sc.y = tab[TAB_PW + max(e1, 0)] * r;
-                            }
-                            uint64_t v = pack2(e >= 0 ? sc.x * __uint_as_float(rr[4 * kk + 2 * half]) : 0.f,
-                                               e1 >= 0 ? sc.y * __uint_as_float(rr[4 * kk + 2 * half + 1]) : 0.f);
-                            unsigned char *at = pt + i * 128 + ((k ^ (i & 7)) << 4) + 4 * t;
-                            *reinterpret_cast<uint32_t *>(at) = split_pair(v);
-                            *reinterpret_cast<uint32_t *>(at + TILE) = round_pair(v);
+                    for (int half = 0; half < 2; ++half) {
+                        const int i = i0 + 8 * half;
+                        const int e = w.rev ? j - i : i - j, e1 = w.rev ? e + 1 : e - 1;
+                        if (strong_tag) {
+                            const float rr = half ? r1 : r0;
+                            sc.x = tab[TAB_PW + max(e, 0)] * rr;
+                            sc.y = tab[TAB_PW + max(e1, 0)] * rr;
                         }
+                        uint32_t *v2 = r + 4 * k + 2 * half;
+                        uint64_t v = pack2(e >= 0 ? sc.x * __uint_as_float(v2[0]) : 0.f,
+                                           e1 >= 0 ? sc.y * __uint_as_float(v2[1]) : 0.f);
+                        v2[0] = split_pair(v);
+                        v2[1] = round_pair(v);
                     }
-                };
-                if (strong) make_p(std::true_type{});
-                else make_p(std::false_type{});
-            }
+                }
+            };
+            if (strong) make_p(std::true_type{});
+            else make_p(std::false_type{});
+            // the MMAs of the chunk before have read its P
+            if (c > 0 && !ctl.wait(D_OFULL, (c - 1) & 1)) break;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    unsigned char *at = pt + half * 1024 + ((k ^ g) << 4);   // (i0 + 8 half) & 7 = g
+                    *reinterpret_cast<uint32_t *>(at) = r[4 * k + 2 * half];
+                    *reinterpret_cast<uint32_t *>(at + TILE) = r[4 * k + 2 * half + 1];
+                }
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[D_PREADY]);
-            // ---- O
-            if (leader) bulk_wait_group_read0();             // the store before has read the staging tile
-            if (!(ok = named_and(2, 128, ctl.wait(D_OFULL, c & 1)))) break;
-            tc_fence_after();
+        }
+    } else {
+        // ======================================================== O
+        regs_dec<kRegsOut>();
+        const int q4 = warp & 3;
+        const uint32_t t_lane = tmem + ((uint32_t)(q4 * 32) << 16);
+        const bool leader = tid == 512;
+        const int t = lane & 3;
+        const size_t stride = (size_t)w.Hv * kHeadDim;
+        for (int c = 0; c < n && !STATE_ONLY; ++c) {
+            const int cw = sp.c0 + c;
+            const float *ft = tab + TAB_F + (cw == special ? 64 : 0);
             int t0;
             const int rows = chunk_rows(sp, w.rev, cw, t0);
+            if (leader) bulk_wait_group_read0();             // the store before has read the staging tile
+            if (!named_and(2, 128, ctl.wait(D_OFULL, c & 1))) break;
+            tc_fence_after();
             if (w.o_f32 || (rows < C && w.cu_seqlens)) {
                 const size_t at = ((size_t)sp.bt * w.T + t0) * stride + (size_t)h * kHeadDim + q4 * 32 + lane;
                 if (w.o_f32) store_rows(static_cast<float *>(w.o) + at, t_lane, ft, rows, stride);
@@ -552,34 +585,37 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                 if (lane == 0) mbar_arrive(&bar[D_OFREE]);
                 continue;
             }
-            uint32_t r[4][16];                               // 16-lane slab x 32-token block
-#pragma unroll
-            for (int it = 0; it < 4; ++it)
-                tmem_ld16x256b_x4(t_lane + ((uint32_t)(16 * (it >> 1)) << 16) + T_O + 32 * (it & 1), r[it]);
-            tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[D_OFREE]);
             const uint32_t stage = smem_u32(sm + DOFF_O);
             const int mt = lane >> 3, mi = lane & 7;         // stored row mi of matrix mt
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                const int slab = it >> 1, cb = it & 1;
+            for (int cb = 0; cb < 2; ++cb) {                 // 32 tokens
+                uint32_t r[2][16];                           // 16-lane slabs
+                tmem_ld16x256b_x4(t_lane + T_O + 32 * cb, r[0]);
+                tmem_ld16x256b_x4(t_lane + (16u << 16) + T_O + 32 * cb, r[1]);
+                tmem_wait_ld();
+                if (cb == 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[D_OFREE]);
+                }
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
-                    uint32_t m[4];
+                    const float2 f0 = *reinterpret_cast<const float2 *>(ft + 32 * cb + 16 * kk + 2 * t);
+                    const float2 f1 = *reinterpret_cast<const float2 *>(ft + 32 * cb + 16 * kk + 8 + 2 * t);
 #pragma unroll
-                    for (int mm = 0; mm < 4; ++mm) {
-                        const int k = 2 * kk + (mm >> 1), gg = mm & 1;
-                        const float2 f = *reinterpret_cast<const float2 *>(ft + 32 * cb + 8 * k + 2 * t);
-                        m[mm] = round_pair(mul2(pack2(f.x, f.y), pack2(__uint_as_float(r[it][4 * k + 2 * gg]),
-                                                                       __uint_as_float(r[it][4 * k + 2 * gg + 1]))));
+                    for (int slab = 0; slab < 2; ++slab) {
+                        uint32_t m[4];
+#pragma unroll
+                        for (int mm = 0; mm < 4; ++mm) {
+                            const uint32_t *v = r[slab] + 4 * (2 * kk + (mm >> 1)) + 2 * (mm & 1);
+                            const float2 f = mm >> 1 ? f1 : f0;
+                            m[mm] = round_pair(mul2(pack2(f.x, f.y), pack2(__uint_as_float(v[0]), __uint_as_float(v[1]))));
+                        }
+                        const int orow = 32 * cb + 8 * (2 * kk + (mt >> 1)) + mi;       // token
+                        const int jst = q4 * 32 + 16 * slab + 8 * (mt & 1);             // first z of the block
+                        stmatrix_x4_trans(stage + (jst >> 6) * TILE + sw128_chunk(orow, (jst & 63) >> 3),
+                                          m[0], m[1], m[2], m[3]);
                     }
-                    const int k = 2 * kk + (mt >> 1), gg = mt & 1;
-                    const int orow = 32 * cb + 8 * k + mi;          // token
-                    const int jst = q4 * 32 + 16 * slab + 8 * gg;   // first z of the block
-                    stmatrix_x4_trans(stage + (jst >> 6) * TILE + sw128_chunk(orow, (jst & 63) >> 3),
-                                      m[0], m[1], m[2], m[3]);
                 }
             }
             fence_proxy_async_smem();
