@@ -50,7 +50,7 @@ constexpr uint32_t T_COLS = 512;
 constexpr uint32_t DOFF_P = kStages * kStageBytes;    // P pieces: high, low
 constexpr uint32_t DOFF_O = DOFF_P + 2 * TILE;
 constexpr uint32_t DOFF_TAB = DOFF_O + 2 * TILE;      // powers; per token: Z weights, O scales, P scales
-constexpr uint32_t TAB_PW = 0, TAB_W = 68, TAB_F = 68 + 128, TAB_C = 68 + 256, TAB_L = 68 + 3 * 128,
+constexpr uint32_t TAB_PW = 0, TAB_W = 66, TAB_F = 66 + 128, TAB_C = 66 + 256, TAB_L = 66 + 3 * 128,
                    TAB_SEG = TAB_L + 4, TAB_FLOATS = TAB_SEG + 16;
 constexpr uint32_t DOFF_BAR = DOFF_TAB + TAB_FLOATS * 4;
 enum : int {
@@ -61,11 +61,12 @@ enum : int {
     D_HREADY = 10,                 // pieces of H written (8 warps)
     D_XFULL = 11,                  // H's share of O done
     D_GFULL = 12,                  // G done
-    D_PREADY = 13,                 // P written, G read (4 warps)
+    D_PREADY = 13,                 // P written (4 warps)
     D_OFULL = 14,                  // O done
     D_OFREE = 15,                  // O read (4 warps)
-    D_DRAIN = 16,                  // x2: last MMAs of either issuer
-    D_NBAR = 18
+    D_GFREE = 16,                  // G read (4 warps)
+    D_DRAIN = 17,                  // x2: last MMAs of either issuer
+    D_NBAR = 19
 };
 constexpr uint32_t DOFF_MISC = DOFF_BAR + D_NBAR * 8;
 constexpr uint32_t D_SMEM = DOFF_MISC + 16 + 1024;
@@ -201,7 +202,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
         prefetch_tensormap(&tm_y);
         prefetch_tensormap(&tm_z);
         for (int i = 0; i < (int)D_NBAR; ++i)
-            mbar_init(&bar[i], i == D_ZP || i == D_HREADY ? 8 : i == D_PREADY || i == D_OFREE ? 4
+            mbar_init(&bar[i], i == D_ZP || i == D_HREADY ? 8 : i == D_PREADY || i == D_OFREE || i == D_GFREE ? 4
                                : i >= D_EMPTY && i < D_EMPTY + kStages && !STATE_ONLY ? 2 : 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -279,12 +280,12 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                 const uint32_t st = sbase + (c % kStages) * kStageBytes;
                 tc_fence_after();
                 if (elect_one()) {
-#pragma unroll
+                    const uint64_t yd = smem_desc_sw128(st + 2 * TILE, TILE, 1024);
+#pragma unroll 1
                     for (int pc = NZ - 1; pc >= 0; --pc)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_bf16_ts(tmem + T_D, tmem + T_Z + pc * 32 + k * 8,
-                                        smem_desc_sw128(st + 2 * TILE + k * 2048, TILE, 1024), IDD_D,
+                            mma_bf16_ts(tmem + T_D, tmem + T_Z + pc * 32 + k * 8, yd + k * (2048 >> 4), IDD_D,
                                         pc < NZ - 1 || k > 0);
                     mma_commit(&bar[D_DFULL]);
                     mma_commit(&bar[D_EMPTY + c % kStages]);
@@ -299,46 +300,56 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
         }
         if (!STATE_ONLY && warp == 2) {
             // ==================================================== MMA issuer: G and O
-            for (int c = 0; c < n; ++c) {
+            // Short loops: this code and the other roles' share the instruction cache.
+            auto issue_g = [&](int c) -> bool {
                 const int s = c % kStages;
-                const uint32_t st = sbase + s * kStageBytes;
+                if (!ctl.wait(D_FULL + s, (c / kStages) & 1)) return false;
                 // rows past a packed sequence's end are zeroed before Z' is announced
-                if (!ctl.wait(D_FULL + s, (c / kStages) & 1)) break;
-                if (w.cu_seqlens && sp.c0 + c == special && !ctl.wait(D_ZP, c & 1)) break;
+                if (w.cu_seqlens && sp.c0 + c == special && !ctl.wait(D_ZP, c & 1)) return false;
+                if (c > 0 && !ctl.wait(D_GFREE, (c - 1) & 1)) return false;
                 tc_fence_after();
                 if (elect_one()) {
+                    const uint64_t xd = smem_desc_sw128(sbase + s * kStageBytes, 16, 1024);
+#pragma unroll 1
+                    for (int hk = 0; hk < 2; ++hk)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t koff = (k >> 2) * TILE + (k & 3) * 32;
-                        mma_bf16(tmem + T_G, smem_desc_sw128(st + koff, 16, 1024),
-                                 smem_desc_sw128(st + 2 * TILE + koff, 16, 1024), IDD_G, k > 0);
-                    }
+                        for (int k = 0; k < 4; ++k) {
+                            const uint64_t at = xd + hk * (TILE >> 4) + k * 2;
+                            mma_bf16(tmem + T_G, at, at + (2 * TILE >> 4), IDD_G, hk > 0 || k > 0);
+                        }
                     mma_commit(&bar[D_GFULL]);
                 }
                 __syncwarp();
+                return true;
+            };
+            bool ok = n > 0 && issue_g(0);
+            for (int c = 0; c < n && ok; ++c) {
+                const int s = c % kStages;
                 if (!ctl.wait(D_HREADY, c & 1)) break;
                 if (c > 0 && !ctl.wait(D_OFREE, (c - 1) & 1)) break;
                 tc_fence_after();
                 if (elect_one()) {
+                    const uint64_t xd = smem_desc_sw128(sbase + s * kStageBytes, 16, 1024);
+#pragma unroll 1
+                    for (int it = 3; it >= 0; --it)          // low pieces first
 #pragma unroll
-                    for (int pc = 1; pc >= 0; --pc)
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma_bf16_ts(tmem + T_O, tmem + T_H + pc * 64 + k * 8,
-                                        smem_desc_sw128(st + (k >> 2) * TILE + (k & 3) * 32, 16, 1024), IDD_OX,
-                                        pc < 1 || k > 0);
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16_ts(tmem + T_O, tmem + T_H + it * 32 + k * 8, xd + (it & 1) * (TILE >> 4) + k * 2,
+                                        IDD_OX, it < 3 || k > 0);
                     mma_commit(&bar[D_XFULL]);
                 }
                 __syncwarp();
+                if (c + 1 < n && !(ok = issue_g(c + 1))) break;
                 if (!ctl.wait(D_PREADY, c & 1)) break;
                 tc_fence_after();
                 if (elect_one()) {
-#pragma unroll
+                    const uint64_t zd = smem_desc_sw128(sbase + s * kStageBytes + 4 * TILE, TILE, 1024);
+                    const uint64_t pd = smem_desc_sw128(sbase + DOFF_P, 16, 1024);
+#pragma unroll 1
                     for (int pc = 1; pc >= 0; --pc)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_bf16(tmem + T_O, smem_desc_sw128(st + 4 * TILE + k * 2048, TILE, 1024),
-                                     smem_desc_sw128(sbase + DOFF_P + pc * TILE + k * 32, 16, 1024), IDD_OI, true);
+                            mma_bf16(tmem + T_O, zd + k * (2048 >> 4), pd + pc * (TILE >> 4) + k * 2, IDD_OI, true);
                     mma_commit(&bar[D_OFULL]);
                     mma_commit(&bar[D_EMPTY + s]);
                 }
@@ -520,6 +531,9 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             tmem_ld16x256b_x4(t_lane + T_G, r);
             tmem_ld16x256b_x4(t_lane + T_G + 32, r + 16);
             tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[D_GFREE]);
             auto make_p = [&](auto strong_tag) {             // r: pieces of P in place of G
                 const float r0 = strong_tag ? 1.f / ft[i0] : 0.f, r1 = strong_tag ? 1.f / ft[i0 + 8] : 0.f;
 #pragma unroll
@@ -556,7 +570,6 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                     *reinterpret_cast<uint32_t *>(at + TILE) = r[4 * k + 2 * half + 1];
                 }
             fence_proxy_async_smem();
-            tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[D_PREADY]);
         }
