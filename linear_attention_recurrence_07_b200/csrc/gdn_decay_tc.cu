@@ -6,17 +6,19 @@
 // p_i = i forwards, L - 1 - i backwards:
 //   G    = X Y^T                                        M=64  N=64  K=128
 //   P_ij = lambda^{-p_j} G_ij, j at or before i         (two bf16 pieces)
-//   O^T  = (H^T X^T + Z^T P^T) diag(lambda^p)           M=128 N=64  K=2x128 + 2x64
+//   O^T  = (H^T X^T + Z^T P^T) diag(lambda^p)           M=128 N=64  K=128 + 2x64
 //   D^T  = Z'^T Y, Z' = diag(lambda^{L-p}) Z in NZ bf16 pieces
 //                                                       M=128 N=128 K=NZ x 64
 //   H^T <- lambda^L H^T + D^T                           (fp32 registers)
 // Unlike the delta rule, D does not depend on the state: the chain from chunk to chunk
 // is one fused multiply-add per state element.  The state therefore lives in registers
-// (64 per thread over 256 threads), and only its two bf16 pieces go to the tensor core.
+// (64 per thread over 256 threads), and only its bf16 rounding goes to the tensor core.
 //
-// Roundings: two pieces carry 16 bits of H and of P, against the 8 of O.  Z' has three
-// pieces, all 24 bits, where an end state is wanted, two where the state only feeds O;
-// small pieces are accumulated first, because the tensor core truncates.  lambda^{-p_j}
+// Roundings: H is rounded to bf16 where it meets X, as every operand of a bf16 product: its
+// 128 terms average the rounding out to that of O itself.  P, of which a short sequence has
+// few terms, keeps 16 bits in two pieces.  Z' has three pieces, all 24 bits, where an end
+// state is wanted, two where the state only feeds O; small pieces are accumulated first,
+// because the tensor core truncates.  lambda^{-p_j}
 // grows to lambda^{-63}: below lambda = 2^-(100/63) the scale is held at 2^100, which
 // replaces a factor lambda^p < 2^-100 on H's share of a row by 2^-100.
 //
@@ -24,7 +26,7 @@
 //   warp 0      TMA producer: X, Y, Z tiles, four stages of 48 KB
 //   warp 1      issues the D MMAs, warp 2 the G and O MMAs (one elected thread each, in order)
 //   warps 4-11  state: thread = TMEM lane (z dimension) and half of the 128 columns;
-//               decays Z into its pieces (TMEM), adds D to the state, writes its pieces
+//               copies Z^T and its decayed pieces to TMEM, adds D to the state, writes H
 //   warps 12-15 G -> P (shared memory)
 //   warps 16-19 O epilogue (stmatrix, TMA store)
 #include <type_traits>
@@ -41,8 +43,9 @@ constexpr uint32_t kStageBytes = 6 * TILE;            // [X0][X1][Y0][Y1][Z0][Z1
 
 // TMEM columns
 constexpr uint32_t T_D = 0;        // D^T, 128 fp32 columns
-constexpr uint32_t T_H = 128;      // H^T pieces: high at 128, low at 192 (64 packed columns each)
-constexpr uint32_t T_Z = 256;      // Z'^T pieces, 32 packed columns each
+constexpr uint32_t T_H = 128;      // H^T rounded, 64 packed columns
+constexpr uint32_t T_Z = 192;      // Z'^T pieces, 32 packed columns each
+constexpr uint32_t T_ZR = 288;     // Z^T, 32 packed columns, two buffers
 constexpr uint32_t T_G = 352;
 constexpr uint32_t T_O = 416;
 constexpr uint32_t T_COLS = 512;
@@ -56,9 +59,9 @@ constexpr uint32_t DOFF_BAR = DOFF_TAB + TAB_FLOATS * 4;
 enum : int {
     D_FULL = 0,                    // x4: tiles of a stage landed
     D_EMPTY = 4,                   // x4: stage no longer read (both issuers)
-    D_ZP = 8,                      // Z' pieces written, D of the chunk before read (8 warps)
+    D_ZP = 8,                      // Z and Z' written, D of the chunk before read (8 warps)
     D_DFULL = 9,                   // D done
-    D_HREADY = 10,                 // pieces of H written (8 warps)
+    D_HREADY = 10,                 // H written (8 warps)
     D_XFULL = 11,                  // H's share of O done
     D_GFULL = 12,                  // G done
     D_PREADY = 13,                 // P written (4 warps)
@@ -74,8 +77,7 @@ static_assert(D_SMEM <= 232448, "shared memory per CTA");
 static_assert(DOFF_TAB % 16 == 0 && DOFF_BAR % 8 == 0, "alignment");
 
 constexpr uint32_t IDD_G = idesc_bf16(64, 64, false, false);
-constexpr uint32_t IDD_OX = idesc_bf16(128, 64, false, false);
-constexpr uint32_t IDD_OI = idesc_bf16(128, 64, true, false);
+constexpr uint32_t IDD_O = idesc_bf16(128, 64, false, false);
 constexpr uint32_t IDD_D = idesc_bf16(128, 128, false, true);
 // Registers per thread: 640 x 96 at launch; the warpgroups without state give part of their
 // share to the two that hold it (a spilled register is an L2 round trip here, because the
@@ -331,27 +333,28 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                 if (elect_one()) {
                     const uint64_t xd = smem_desc_sw128(sbase + s * kStageBytes, 16, 1024);
 #pragma unroll 1
-                    for (int it = 3; it >= 0; --it)          // low pieces first
+                    for (int hk = 0; hk < 2; ++hk)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_bf16_ts(tmem + T_O, tmem + T_H + it * 32 + k * 8, xd + (it & 1) * (TILE >> 4) + k * 2,
-                                        IDD_OX, it < 3 || k > 0);
+                            mma_bf16_ts(tmem + T_O, tmem + T_H + hk * 32 + k * 8, xd + hk * (TILE >> 4) + k * 2, IDD_O,
+                                        hk > 0 || k > 0);
                     mma_commit(&bar[D_XFULL]);
+                    mma_commit(&bar[D_EMPTY + s]);           // G was issued before
                 }
                 __syncwarp();
                 if (c + 1 < n && !(ok = issue_g(c + 1))) break;
                 if (!ctl.wait(D_PREADY, c & 1)) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t zd = smem_desc_sw128(sbase + s * kStageBytes + 4 * TILE, TILE, 1024);
+                    // H written (above) implies Z written
                     const uint64_t pd = smem_desc_sw128(sbase + DOFF_P, 16, 1024);
 #pragma unroll 1
                     for (int pc = 1; pc >= 0; --pc)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_bf16(tmem + T_O, zd + k * (2048 >> 4), pd + pc * (TILE >> 4) + k * 2, IDD_OI, true);
+                            mma_bf16_ts(tmem + T_O, tmem + T_ZR + (c & 1) * 32 + k * 8, pd + pc * (TILE >> 4) + k * 2, IDD_O,
+                                        true);
                     mma_commit(&bar[D_OFULL]);
-                    mma_commit(&bar[D_EMPTY + s]);
                 }
                 __syncwarp();
             }
@@ -398,67 +401,69 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                 }
             }
         }
-        auto write_pieces = [&]() {
+        auto write_h = [&]() {
+            uint32_t hp[32];
 #pragma unroll
-            for (int e0 = 0; e0 < 32; e0 += 16) {
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    uint64_t v = H[e0 + e];
-                    hi[e] = split_pair(v);
-                    lo[e] = round_pair(v);
-                }
-                tmem_st16u(t_lane + T_H + 32 * hf + e0, hi);
-                tmem_st16u(t_lane + T_H + 64 + 32 * hf + e0, lo);
-            }
+            for (int e = 0; e < 32; ++e) hp[e] = round_pair(H[e]);
+            tmem_st32u(t_lane + T_H + 32 * hf, hp);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[D_HREADY]);
         };
-        // Z'^T pieces of this thread's 32 tokens, from column dz of the Z tile, in registers
+        // This warp's block of Z^T (32 lanes x 32 tokens): as it is to TMEM, its decayed pieces
+        // in registers.  zp[.][8 l + 2 m + r]: lanes 16 l + 8 r + lane / 4, tokens 8 m + 2 (lane % 4), +1.
         uint32_t zp[NZ][16];
         auto make_z = [&](int c) -> bool {
             const int s = c % kStages;
             if (!ctl.wait(D_FULL + s, (c / kStages) & 1)) return false;
+            // the products that read this buffer two chunks ago
+            if (!STATE_ONLY && c >= 2 && !ctl.wait(D_OFULL, c & 1)) return false;
             unsigned char *st = sm + s * kStageBytes;
             int t0;
             const int cw = sp.c0 + c, rows = chunk_rows(sp, w.rev, cw, t0);
-            if (w.cu_seqlens && rows < C) {                  // the next sequence's rows: out of the products
-                for (int i = tid - 128; i < (C - rows) * 4 * 8; i += 256) {
-                    const int r = rows + (i >> 5), tile = (i >> 3) & 3, ch = i & 7;
+            if (w.cu_seqlens && rows < C) {                  // Y of the next sequence: out of the products
+                for (int i = tid - 128; i < (C - rows) * 2 * 8; i += 256) {
+                    const int r = rows + (i >> 4), tile = (i >> 3) & 1, ch = i & 7;
                     *reinterpret_cast<uint4 *>(st + (2 + tile) * TILE + r * 128 + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
             }
-            const float *wt = tab + TAB_W + (cw == special ? 64 : 0) + 32 * hf;
-            const unsigned char *zt = st + (4 + (dz >> 6)) * TILE + (32 * hf) * 128;
-            const uint32_t zc = ((dz & 63) >> 3) << 4, zb = (dz & 7) * 2;
+            // ldmatrix rows: lane i gives token 8 (i / 16) + i % 8 of an 8-column group (i / 8) % 2
+            const uint32_t zt = smem_u32(st + (4 + (q4 >> 1)) * TILE);
+            const float *wt = tab + TAB_W + (cw == special ? 64 : 0) + 32 * hf + 2 * (lane & 3);
+            const int row0 = 32 * hf + 8 * (lane >> 4) + (lane & 7), grp = 4 * (q4 & 1) + ((lane >> 3) & 1);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int t = 2 * e;
-                const float2 ww = *reinterpret_cast<const float2 *>(wt + t);
-                const uint32_t ua = *reinterpret_cast<const uint16_t *>(zt + t * 128 + ((zc ^ ((t & 7) << 4)) + zb));
-                const uint32_t ub = *reinterpret_cast<const uint16_t *>(zt + (t + 1) * 128 + ((zc ^ (((t + 1) & 7) << 4)) + zb));
-                uint64_t v = mul2(pack2(ww.x, ww.y), pack2(__uint_as_float(ua << 16), __uint_as_float(ub << 16)));
-                zp[0][e] = split_pair(v);
-                if (NZ == 3) zp[1][e] = split_pair(v);
-                zp[NZ - 1][e] = NZ == 3 ? high_pair(v) : round_pair(v);
-            }
-            if (rows < C) {                                  // (a weight of zero would keep a NaN)
+            for (int l = 0; l < 2; ++l) {
+                uint32_t z[8];
+                ldmatrix_x4_trans(z, zt + sw128_chunk(row0, grp + 2 * l));
+                ldmatrix_x4_trans(z + 4, zt + sw128_chunk(row0 + 16, grp + 2 * l));
+                if (rows < C) {                              // rows past the end (a weight of zero would keep a NaN)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int left = rows - (32 * hf + 2 * e);
-                    const uint32_t keep = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+                    for (int e = 0; e < 8; ++e) {
+                        const int left = rows - (32 * hf + 8 * (e >> 1) + 2 * (lane & 3));
+                        z[e] &= left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+                    }
+                }
+                if (!STATE_ONLY)
+                    tmem_st16x128b_x4(t_lane + ((uint32_t)(16 * l) << 16) + T_ZR + 32 * (c & 1) + 16 * hf, z);
 #pragma unroll
-                    for (int pc = 0; pc < NZ; ++pc) zp[pc][e] &= keep;
+                for (int e = 0; e < 8; ++e) {
+                    const float2 ww = *reinterpret_cast<const float2 *>(wt + 8 * (e >> 1));
+                    uint64_t v = mul2(pack2(ww.x, ww.y), pack2(__uint_as_float(z[e] << 16), __uint_as_float(z[e] & 0xffff0000u)));
+                    zp[0][8 * l + e] = split_pair(v);
+                    if (NZ == 3) zp[1][8 * l + e] = split_pair(v);
+                    zp[NZ - 1][8 * l + e] = NZ == 3 ? high_pair(v) : round_pair(v);
                 }
             }
             return true;
         };
         auto store_z = [&]() {
 #pragma unroll
-            for (int pc = 0; pc < NZ; ++pc) tmem_st16u(t_lane + T_Z + 32 * pc + 16 * hf, zp[pc]);
+            for (int pc = 0; pc < NZ; ++pc)
+#pragma unroll
+                for (int l = 0; l < 2; ++l)
+                    tmem_st16x128b_x4(t_lane + ((uint32_t)(16 * l) << 16) + T_Z + 32 * pc + 16 * hf, zp[pc] + 8 * l);
         };
         auto announce_z = [&]() {
             tmem_wait_st();
@@ -467,13 +472,10 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             if (lane == 0) mbar_arrive(&bar[D_ZP]);
         };
         bool ok = true;
-        if (n > 0) {
-            if (!STATE_ONLY) write_pieces();
-            ok = make_z(0);
-            if (ok) {
-                store_z();
-                announce_z();
-            }
+        if (n > 0 && (ok = make_z(0))) {
+            store_z();
+            announce_z();
+            if (!STATE_ONLY) write_h();
         }
         for (int c = 0; c < n && ok; ++c) {
             if (c + 1 < n && !(ok = make_z(c + 1))) break;   // while D of this chunk runs
@@ -484,12 +486,12 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             const float2 pf = *reinterpret_cast<const float2 *>(tab + TAB_L + (is_special ? 2 : 0));
             const uint64_t ph = pack2(pf.x, pf.x), pl = pack2(pf.y, pf.y);
 #pragma unroll
-            for (int e0 = 0; e0 < 32; e0 += 8) {
-                float d[16];
-                tmem_ld16(t_lane + T_D + 64 * hf + 2 * e0, d);
+            for (int e0 = 0; e0 < 32; e0 += 16) {
+                float d[32];
+                tmem_ld32(t_lane + T_D + 64 * hf + 2 * e0, d);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
+                for (int e = 0; e < 16; ++e)
                     H[e0 + e] = fma2(ph, H[e0 + e], fma2(pl, H[e0 + e], pack2(d[2 * e], d[2 * e + 1])));
             }
             if (c + 1 < n) {
@@ -497,7 +499,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                 if (!STATE_ONLY) {
                     if (!(ok = ctl.wait(D_XFULL, c & 1))) break;
                     tc_fence_after();
-                    write_pieces();
+                    write_h();
                 }
             }
         }

@@ -224,6 +224,20 @@ __device__ __forceinline__ void tmem_ld16x256b_x4(uint32_t taddr, uint32_t *r) {
           "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
+// 16 lanes x 128 bits, four times along the columns (16 columns), stored: thread t of the warp
+// gives, for k = 0..3, r[2k] = lane (base + t/4), column col + 4k + t%4, and r[2k+1] = the same
+// column of lane (base + 8 + t/4): pairs as ldmatrix.trans delivers them.
+__device__ __forceinline__ void tmem_st16x128b_x4(uint32_t taddr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// Four 8x8 bf16 matrices, loaded transposed: thread t gives the address of row t%8 of matrix
+// t/8 and gets, of matrix i, rows 2(t%4), +1 (low, high half) of column t/4.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t *r, uint32_t saddr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(saddr) : "memory");
+}
 // Four 8x8 bf16 matrices, stored transposed: register i of thread t holds row t/4,
 // columns 2(t%4), +1 of matrix i; thread t gives the address of stored row t%8 of
 // matrix t/8, which receives column t%8 of the matrix (16 bytes).
