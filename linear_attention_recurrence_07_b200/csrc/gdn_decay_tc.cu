@@ -65,9 +65,10 @@ enum : int {
     D_XFULL = 11,                  // H's share of O done
     D_GFULL = 12,                  // G done
     D_PREADY = 13,                 // P written (4 warps)
-    D_OFULL = 14,                  // O done
-    D_OFREE = 15,                  // O read (4 warps)
-    D_GFREE = 16,                  // G read (4 warps)
+    // x2, chunk c uses c % 2: O done.  (The state's warps wait for it up to two chunks late; on
+    // one barrier the phase after it could have completed by then.)
+    D_OFULL = 14,
+    D_OFREE = 16,                  // O read (4 warps)
     D_DRAIN = 17,                  // x2: last MMAs of either issuer
     D_NBAR = 19
 };
@@ -81,8 +82,8 @@ constexpr uint32_t IDD_O = idesc_bf16(128, 64, false, false);
 constexpr uint32_t IDD_D = idesc_bf16(128, 128, false, true);
 // Registers per thread: 640 x 96 at launch; the warpgroups without state give part of their
 // share to the two that hold it (a spilled register is an L2 round trip here, because the
-// shared memory leaves no L1): 48 + 2 x 144 + 2 x 72 = 5 x 96.
-constexpr int kRegsIssue = 48, kRegsState = 144, kRegsOut = 72;
+// shared memory leaves no L1): 40 + 2 x 152 + 72 + 64 = 5 x 96.
+constexpr int kRegsIssue = 40, kRegsState = 152, kRegsP = 72, kRegsOut = 64;
 constexpr double kScaleFloor = -69.31471805599453;    // log of 2^-100
 
 template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -204,7 +205,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
         prefetch_tensormap(&tm_y);
         prefetch_tensormap(&tm_z);
         for (int i = 0; i < (int)D_NBAR; ++i)
-            mbar_init(&bar[i], i == D_ZP || i == D_HREADY ? 8 : i == D_PREADY || i == D_OFREE || i == D_GFREE ? 4
+            mbar_init(&bar[i], i == D_ZP || i == D_HREADY ? 8 : i == D_PREADY || i == D_OFREE ? 4
                                : i >= D_EMPTY && i < D_EMPTY + kStages && !STATE_ONLY ? 2 : 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -308,8 +309,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                 if (!ctl.wait(D_FULL + s, (c / kStages) & 1)) return false;
                 // rows past a packed sequence's end are zeroed before Z' is announced
                 if (w.cu_seqlens && sp.c0 + c == special && !ctl.wait(D_ZP, c & 1)) return false;
-                if (c > 0 && !ctl.wait(D_GFREE, (c - 1) & 1)) return false;
-                tc_fence_after();
+                tc_fence_after();                            // G of the chunk before has been read
                 if (elect_one()) {
                     const uint64_t xd = smem_desc_sw128(sbase + s * kStageBytes, 16, 1024);
 #pragma unroll 1
@@ -342,7 +342,6 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                     mma_commit(&bar[D_EMPTY + s]);           // G was issued before
                 }
                 __syncwarp();
-                if (c + 1 < n && !(ok = issue_g(c + 1))) break;
                 if (!ctl.wait(D_PREADY, c & 1)) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -354,9 +353,10 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                         for (int k = 0; k < 4; ++k)
                             mma_bf16_ts(tmem + T_O, tmem + T_ZR + (c & 1) * 32 + k * 8, pd + pc * (TILE >> 4) + k * 2, IDD_O,
                                         true);
-                    mma_commit(&bar[D_OFULL]);
+                    mma_commit(&bar[D_OFULL + (c & 1)]);
                 }
                 __syncwarp();
+                if (c + 1 < n) ok = issue_g(c + 1);
             }
             if (elect_one()) {
                 mma_commit(&bar[D_DRAIN + 1]);
@@ -411,14 +411,13 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[D_HREADY]);
         };
-        // This warp's block of Z^T (32 lanes x 32 tokens): as it is to TMEM, its decayed pieces
-        // in registers.  zp[.][8 l + 2 m + r]: lanes 16 l + 8 r + lane / 4, tokens 8 m + 2 (lane % 4), +1.
-        uint32_t zp[NZ][16];
-        auto make_z = [&](int c) -> bool {
+        // This warp's block of Z^T (32 lanes x 32 tokens) to TMEM: as it is, and its decayed
+        // pieces.  D of the chunk before is done and has been read.
+        auto write_z = [&](int c) -> bool {
             const int s = c % kStages;
             if (!ctl.wait(D_FULL + s, (c / kStages) & 1)) return false;
-            // the products that read this buffer two chunks ago
-            if (!STATE_ONLY && c >= 2 && !ctl.wait(D_OFULL, c & 1)) return false;
+            // the products that read this buffer of Z^T two chunks ago
+            if (!STATE_ONLY && c >= 2 && !ctl.wait(D_OFULL + (c & 1), ((c >> 1) - 1) & 1)) return false;
             unsigned char *st = sm + s * kStageBytes;
             int t0;
             const int cw = sp.c0 + c, rows = chunk_rows(sp, w.rev, cw, t0);
@@ -433,55 +432,45 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             const uint32_t zt = smem_u32(st + (4 + (q4 >> 1)) * TILE);
             const float *wt = tab + TAB_W + (cw == special ? 64 : 0) + 32 * hf + 2 * (lane & 3);
             const int row0 = 32 * hf + 8 * (lane >> 4) + (lane & 7), grp = 4 * (q4 & 1) + ((lane >> 3) & 1);
-#pragma unroll
-            for (int l = 0; l < 2; ++l) {
-                uint32_t z[8];
-                ldmatrix_x4_trans(z, zt + sw128_chunk(row0, grp + 2 * l));
-                ldmatrix_x4_trans(z + 4, zt + sw128_chunk(row0 + 16, grp + 2 * l));
+            // 16 lanes x 16 tokens at a time (a short loop: the roles share the instruction cache)
+#pragma unroll 1
+            for (int it = 0; it < 4; ++it) {
+                const int l = it >> 1, k = it & 1;
+                uint32_t z[4], p1[4], p2[4];
+                ldmatrix_x4_trans(z, zt + sw128_chunk(row0 + 16 * k, grp + 2 * l));
+                const float2 w0 = *reinterpret_cast<const float2 *>(wt + 16 * k), w1 = *reinterpret_cast<const float2 *>(wt + 16 * k + 8);
                 if (rows < C) {                              // rows past the end (a weight of zero would keep a NaN)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int left = rows - (32 * hf + 8 * (e >> 1) + 2 * (lane & 3));
+                    for (int e = 0; e < 4; ++e) {
+                        const int left = rows - (32 * hf + 16 * k + 8 * (e >> 1) + 2 * (lane & 3));
                         z[e] &= left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
                     }
                 }
-                if (!STATE_ONLY)
-                    tmem_st16x128b_x4(t_lane + ((uint32_t)(16 * l) << 16) + T_ZR + 32 * (c & 1) + 16 * hf, z);
+                const uint32_t at = t_lane + ((uint32_t)(16 * l) << 16) + 16 * hf + 8 * k;
+                if (!STATE_ONLY) tmem_st16x128b_x2(at + T_ZR + 32 * (c & 1), z);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 ww = *reinterpret_cast<const float2 *>(wt + 8 * (e >> 1));
-                    uint64_t v = mul2(pack2(ww.x, ww.y), pack2(__uint_as_float(z[e] << 16), __uint_as_float(z[e] & 0xffff0000u)));
-                    zp[0][8 * l + e] = split_pair(v);
-                    if (NZ == 3) zp[1][8 * l + e] = split_pair(v);
-                    zp[NZ - 1][8 * l + e] = NZ == 3 ? high_pair(v) : round_pair(v);
+                for (int e = 0; e < 4; ++e) {
+                    const uint64_t ww = e < 2 ? pack2(w0.x, w0.y) : pack2(w1.x, w1.y);
+                    uint64_t v = mul2(ww, pack2(__uint_as_float(z[e] << 16), __uint_as_float(z[e] & 0xffff0000u)));
+                    z[e] = split_pair(v);
+                    if (NZ == 3) p1[e] = split_pair(v);
+                    p2[e] = NZ == 3 ? high_pair(v) : round_pair(v);
                 }
+                tmem_st16x128b_x2(at + T_Z, z);
+                if (NZ == 3) tmem_st16x128b_x2(at + T_Z + 32, p1);
+                tmem_st16x128b_x2(at + T_Z + 32 * (NZ - 1), p2);
             }
-            return true;
-        };
-        auto store_z = [&]() {
-#pragma unroll
-            for (int pc = 0; pc < NZ; ++pc)
-#pragma unroll
-                for (int l = 0; l < 2; ++l)
-                    tmem_st16x128b_x4(t_lane + ((uint32_t)(16 * l) << 16) + T_Z + 32 * pc + 16 * hf, zp[pc] + 8 * l);
-        };
-        auto announce_z = [&]() {
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[D_ZP]);
+            return true;
         };
         bool ok = true;
-        if (n > 0 && (ok = make_z(0))) {
-            store_z();
-            announce_z();
-            if (!STATE_ONLY) write_h();
-        }
+        if (n > 0 && (ok = write_z(0)) && !STATE_ONLY) write_h();
         for (int c = 0; c < n && ok; ++c) {
-            if (c + 1 < n && !(ok = make_z(c + 1))) break;   // while D of this chunk runs
             if (!(ok = ctl.wait(D_DFULL, c & 1))) break;
             tc_fence_after();
-            if (c + 1 < n) store_z();
             const bool is_special = sp.c0 + c == special;
             const float2 pf = *reinterpret_cast<const float2 *>(tab + TAB_L + (is_special ? 2 : 0));
             const uint64_t ph = pack2(pf.x, pf.x), pl = pack2(pf.y, pf.y);
@@ -495,7 +484,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                     H[e0 + e] = fma2(ph, H[e0 + e], fma2(pl, H[e0 + e], pack2(d[2 * e], d[2 * e + 1])));
             }
             if (c + 1 < n) {
-                announce_z();
+                if (!(ok = write_z(c + 1))) break;
                 if (!STATE_ONLY) {
                     if (!(ok = ctl.wait(D_XFULL, c & 1))) break;
                     tc_fence_after();
@@ -518,7 +507,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
         }
     } else if (warp < 16) {
         // ======================================================== P
-        regs_dec<kRegsOut>();
+        regs_dec<kRegsP>();
         const int q4 = warp & 3;
         const uint32_t t_lane = tmem + ((uint32_t)(q4 * 32) << 16);
         const int g = lane >> 2, t = lane & 3, i0 = 16 * q4 + g;         // rows i0, i0 + 8
@@ -529,51 +518,44 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             // M = 64 accumulators sit in lanes 0-15 of every quarter
             if (!ctl.wait(D_GFULL, c & 1)) break;
             tc_fence_after();
-            uint32_t r[32];
-            tmem_ld16x256b_x4(t_lane + T_G, r);
-            tmem_ld16x256b_x4(t_lane + T_G + 32, r + 16);
-            tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[D_GFREE]);
-            auto make_p = [&](auto strong_tag) {             // r: pieces of P in place of G
+            // the MMAs of the chunk before have read its P
+            if (c > 0 && !ctl.wait(D_OFULL + ((c - 1) & 1), ((c - 1) >> 1) & 1)) break;
+            auto make_p = [&](auto strong_tag) {
                 const float r0 = strong_tag ? 1.f / ft[i0] : 0.f, r1 = strong_tag ? 1.f / ft[i0 + 8] : 0.f;
+#pragma unroll 1
+                for (int hj = 0; hj < 2; ++hj) {             // 32 columns
+                    uint32_t r[16];
+                    tmem_ld16x256b_x4(t_lane + T_G + 32 * hj, r);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int j = 8 * k + 2 * t;
-                    float2 sc = *reinterpret_cast<const float2 *>(ct + j);
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const int k = 4 * hj + kk, j = 8 * k + 2 * t;
+                        float2 sc = *reinterpret_cast<const float2 *>(ct + j);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int i = i0 + 8 * half;
-                        const int e = w.rev ? j - i : i - j, e1 = w.rev ? e + 1 : e - 1;
-                        if (strong_tag) {
-                            const float rr = half ? r1 : r0;
-                            sc.x = tab[TAB_PW + max(e, 0)] * rr;
-                            sc.y = tab[TAB_PW + max(e1, 0)] * rr;
+                        for (int half = 0; half < 2; ++half) {
+                            const int i = i0 + 8 * half;
+                            const int e = w.rev ? j - i : i - j, e1 = w.rev ? e + 1 : e - 1;
+                            if (strong_tag) {
+                                const float rr = half ? r1 : r0;
+                                sc.x = tab[TAB_PW + max(e, 0)] * rr;
+                                sc.y = tab[TAB_PW + max(e1, 0)] * rr;
+                            }
+                            const uint32_t *v2 = r + 4 * kk + 2 * half;
+                            uint64_t v = pack2(e >= 0 ? sc.x * __uint_as_float(v2[0]) : 0.f,
+                                               e1 >= 0 ? sc.y * __uint_as_float(v2[1]) : 0.f);
+                            unsigned char *at = pt + half * 1024 + ((k ^ g) << 4);   // (i0 + 8 half) & 7 = g
+                            *reinterpret_cast<uint32_t *>(at) = split_pair(v);
+                            *reinterpret_cast<uint32_t *>(at + TILE) = round_pair(v);
                         }
-                        uint32_t *v2 = r + 4 * k + 2 * half;
-                        uint64_t v = pack2(e >= 0 ? sc.x * __uint_as_float(v2[0]) : 0.f,
-                                           e1 >= 0 ? sc.y * __uint_as_float(v2[1]) : 0.f);
-                        v2[0] = split_pair(v);
-                        v2[1] = round_pair(v);
                     }
                 }
             };
             if (strong) make_p(std::true_type{});
             else make_p(std::false_type{});
-            // the MMAs of the chunk before have read its P
-            if (c > 0 && !ctl.wait(D_OFULL, (c - 1) & 1)) break;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    unsigned char *at = pt + half * 1024 + ((k ^ g) << 4);   // (i0 + 8 half) & 7 = g
-                    *reinterpret_cast<uint32_t *>(at) = r[4 * k + 2 * half];
-                    *reinterpret_cast<uint32_t *>(at + TILE) = r[4 * k + 2 * half + 1];
-                }
+            tc_fence_before();
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[D_PREADY]);
+            if (lane == 0) mbar_arrive(&bar[D_PREADY]);      // and G is read
         }
     } else {
         // ======================================================== O
@@ -589,7 +571,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             int t0;
             const int rows = chunk_rows(sp, w.rev, cw, t0);
             if (leader) bulk_wait_group_read0();             // the store before has read the staging tile
-            if (!named_and(2, 128, ctl.wait(D_OFULL, c & 1))) break;
+            if (!named_and(2, 128, ctl.wait(D_OFULL + (c & 1), (c >> 1) & 1))) break;
             tc_fence_after();
             if (w.o_f32 || (rows < C && w.cu_seqlens)) {
                 const size_t at = ((size_t)sp.bt * w.T + t0) * stride + (size_t)h * kHeadDim + q4 * 32 + lane;
@@ -602,35 +584,31 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             }
             const uint32_t stage = smem_u32(sm + DOFF_O);
             const int mt = lane >> 3, mi = lane & 7;         // stored row mi of matrix mt
-#pragma unroll
-            for (int cb = 0; cb < 2; ++cb) {                 // 32 tokens
-                uint32_t r[2][16];                           // 16-lane slabs
-                tmem_ld16x256b_x4(t_lane + T_O + 32 * cb, r[0]);
-                tmem_ld16x256b_x4(t_lane + (16u << 16) + T_O + 32 * cb, r[1]);
+#pragma unroll 1
+            for (int it = 0; it < 4; ++it) {                 // 32-token block, 16-lane slab
+                const int cb = it >> 1, slab = it & 1;
+                uint32_t r[16];
+                tmem_ld16x256b_x4(t_lane + ((uint32_t)(16 * slab) << 16) + T_O + 32 * cb, r);
                 tmem_wait_ld();
-                if (cb == 1) {
+                if (it == 3) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar[D_OFREE]);
                 }
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
-                    const float2 f0 = *reinterpret_cast<const float2 *>(ft + 32 * cb + 16 * kk + 2 * t);
-                    const float2 f1 = *reinterpret_cast<const float2 *>(ft + 32 * cb + 16 * kk + 8 + 2 * t);
+                    uint32_t m[4];
 #pragma unroll
-                    for (int slab = 0; slab < 2; ++slab) {
-                        uint32_t m[4];
-#pragma unroll
-                        for (int mm = 0; mm < 4; ++mm) {
-                            const uint32_t *v = r[slab] + 4 * (2 * kk + (mm >> 1)) + 2 * (mm & 1);
-                            const float2 f = mm >> 1 ? f1 : f0;
-                            m[mm] = round_pair(mul2(pack2(f.x, f.y), pack2(__uint_as_float(v[0]), __uint_as_float(v[1]))));
-                        }
-                        const int orow = 32 * cb + 8 * (2 * kk + (mt >> 1)) + mi;       // token
-                        const int jst = q4 * 32 + 16 * slab + 8 * (mt & 1);             // first z of the block
-                        stmatrix_x4_trans(stage + (jst >> 6) * TILE + sw128_chunk(orow, (jst & 63) >> 3),
-                                          m[0], m[1], m[2], m[3]);
+                    for (int mm = 0; mm < 4; ++mm) {
+                        const int k = 2 * kk + (mm >> 1);
+                        const float2 f = *reinterpret_cast<const float2 *>(ft + 32 * cb + 8 * k + 2 * t);
+                        const uint32_t *v = r + 4 * k + 2 * (mm & 1);
+                        m[mm] = round_pair(mul2(pack2(f.x, f.y), pack2(__uint_as_float(v[0]), __uint_as_float(v[1]))));
                     }
+                    const int orow = 32 * cb + 8 * (2 * kk + (mt >> 1)) + mi;       // token
+                    const int jst = q4 * 32 + 16 * slab + 8 * (mt & 1);             // first z of the block
+                    stmatrix_x4_trans(stage + (jst >> 6) * TILE + sw128_chunk(orow, (jst & 63) >> 3),
+                                      m[0], m[1], m[2], m[3]);
                 }
             }
             fence_proxy_async_smem();
