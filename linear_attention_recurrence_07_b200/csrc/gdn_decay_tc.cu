@@ -12,7 +12,7 @@
 //   H^T <- lambda^L H^T + D^T                           (fp32 registers)
 // Unlike the delta rule, D does not depend on the state: the chain from chunk to chunk
 // is one fused multiply-add per state element.  The state therefore lives in registers
-// (64 per thread over 256 threads), and only its bf16 rounding goes to the tensor core.
+// (32 per thread over 512 threads), and only its bf16 rounding goes to the tensor core.
 //
 // Roundings: H is rounded to bf16 where it meets X, as every operand of a bf16 product: its
 // 128 terms average the rounding out to that of O itself.  P, of which a short sequence has
@@ -25,10 +25,10 @@
 // One CTA per (sequence or segment, V head), warp-specialised:
 //   warp 0      TMA producer: X, Y, Z tiles, four stages of 48 KB
 //   warp 1      issues the D MMAs, warp 2 the G and O MMAs (one elected thread each, in order)
-//   warps 4-11  state: thread = TMEM lane (z dimension) and half of the 128 columns;
+//   warps 4-19  state: thread = TMEM lane (z dimension) and a quarter of the 128 columns;
 //               copies Z^T and its decayed pieces to TMEM, adds D to the state, writes H
-//   warps 12-15 G -> P (shared memory)
-//   warps 16-19 O epilogue (stmatrix, TMA store)
+//   warps 20-23 G -> P (shared memory)
+//   warps 24-27 O epilogue (stmatrix, TMA store)
 #include <type_traits>
 
 #include "tc_common.cuh"
@@ -37,7 +37,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kDtThreads = 640;
+constexpr int kDtThreads = 896;
 constexpr int kStages = 4;
 constexpr uint32_t kStageBytes = 6 * TILE;            // [X0][X1][Y0][Y1][Z0][Z1], 64 columns each
 
@@ -59,9 +59,9 @@ constexpr uint32_t DOFF_BAR = DOFF_TAB + TAB_FLOATS * 4;
 enum : int {
     D_FULL = 0,                    // x4: tiles of a stage landed
     D_EMPTY = 4,                   // x4: stage no longer read (both issuers)
-    D_ZP = 8,                      // Z and Z' written, D of the chunk before read (8 warps)
+    D_ZP = 8,                      // Z and Z' written, D of the chunk before read (16 warps)
     D_DFULL = 9,                   // D done
-    D_HREADY = 10,                 // H written (8 warps)
+    D_HREADY = 10,                 // H written (16 warps)
     D_XFULL = 11,                  // H's share of O done
     D_GFULL = 12,                  // G done
     D_PREADY = 13,                 // P written (4 warps)
@@ -80,10 +80,10 @@ static_assert(DOFF_TAB % 16 == 0 && DOFF_BAR % 8 == 0, "alignment");
 constexpr uint32_t IDD_G = idesc_bf16(64, 64, false, false);
 constexpr uint32_t IDD_O = idesc_bf16(128, 64, false, false);
 constexpr uint32_t IDD_D = idesc_bf16(128, 128, false, true);
-// Registers per thread: 640 x 96 at launch; the warpgroups without state give part of their
-// share to the two that hold it (a spilled register is an L2 round trip here, because the
-// shared memory leaves no L1): 40 + 2 x 152 + 72 + 64 = 5 x 96.
-constexpr int kRegsIssue = 40, kRegsState = 152, kRegsP = 72, kRegsOut = 64;
+// Registers per thread: 896 x 72 at launch; the issuing warpgroup gives part of its share to
+// the four that hold the state (a spilled register is an L2 round trip here, because the
+// shared memory leaves no L1): 40 + 4 x 88 + 2 x 56 = 7 x 72.
+constexpr int kRegsIssue = 40, kRegsState = 88, kRegsP = 56, kRegsOut = 56;
 constexpr double kScaleFloor = -69.31471805599453;    // log of 2^-100
 
 template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -205,7 +205,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
         prefetch_tensormap(&tm_y);
         prefetch_tensormap(&tm_z);
         for (int i = 0; i < (int)D_NBAR; ++i)
-            mbar_init(&bar[i], i == D_ZP || i == D_HREADY ? 8 : i == D_PREADY || i == D_OFREE ? 4
+            mbar_init(&bar[i], i == D_ZP || i == D_HREADY ? 16 : i == D_PREADY || i == D_OFREE ? 4
                                : i >= D_EMPTY && i < D_EMPTY + kStages && !STATE_ONLY ? 2 : 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -364,56 +364,57 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             }
             __syncwarp();
         }
-    } else if (warp < 12) {
+    } else if (warp < 20) {
         // ======================================================== state
         regs_inc<kRegsState>();
-        const int q4 = warp & 3, hf = (warp - 4) >> 2;
+        const int q4 = warp & 3, part = (warp - 4) >> 2;
         const int dz = q4 * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(q4 * 32) << 16);
-        uint64_t H[32];                                      // H^T[dz][64 hf + 2 e], +1
+        uint64_t H[16];                                      // H^T[dz][32 part + 2 e], +1
 #pragma unroll
-        for (int e = 0; e < 32; ++e) H[e] = 0;
+        for (int e = 0; e < 16; ++e) H[e] = 0;
         if (w.nseg > 1 && !STATE_ONLY) {
 #pragma unroll 1
             for (int g = 0; g <= sp.seg; ++g) {
                 const float f = tab[TAB_SEG + g];
-                const float *src = w.seg + (((size_t)sp.b * w.nseg + g) * w.Hv + h) * hstate + (size_t)64 * hf * kHeadDim + dz;
+                const float *src = w.seg + (((size_t)sp.b * w.nseg + g) * w.Hv + h) * hstate + (size_t)32 * part * kHeadDim + dz;
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
+                for (int e = 0; e < 16; ++e)
                     H[e] = fma2(pack2(f, f), pack2(src[(size_t)(2 * e) * kHeadDim], src[(size_t)(2 * e + 1) * kHeadDim]), H[e]);
             }
         } else if (w.init && (!STATE_ONLY || sp.copy_init)) {
             const float f = (w.init_decays && sp.L > 0) ? tab[TAB_PW + 1] : 1.f;
             const float *src = w.init + ((size_t)sp.b * w.Hv + h) * hstate;
             if (w.init_trans) {
-                const float4 *row = reinterpret_cast<const float4 *>(src + (size_t)dz * kHeadDim + 64 * hf);
+                const float4 *row = reinterpret_cast<const float4 *>(src + (size_t)dz * kHeadDim + 32 * part);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
+                for (int e = 0; e < 8; ++e) {
                     const float4 v = row[e];
                     H[2 * e] = pack2(f * v.x, f * v.y);
                     H[2 * e + 1] = pack2(f * v.z, f * v.w);
                 }
             } else {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float *at = src + (size_t)(64 * hf + 2 * e) * kHeadDim + dz;
+                for (int e = 0; e < 16; ++e) {
+                    const float *at = src + (size_t)(32 * part + 2 * e) * kHeadDim + dz;
                     H[e] = pack2(f * at[0], f * at[kHeadDim]);
                 }
             }
         }
         auto write_h = [&]() {
-            uint32_t hp[32];
+            uint32_t hp[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) hp[e] = round_pair(H[e]);
-            tmem_st32u(t_lane + T_H + 32 * hf, hp);
+            for (int e = 0; e < 16; ++e) hp[e] = round_pair(H[e]);
+            tmem_st16u(t_lane + T_H + 16 * part, hp);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[D_HREADY]);
         };
-        // This warp's block of Z^T (32 lanes x 32 tokens) to TMEM: as it is, and its decayed
-        // pieces.  D of the chunk before is done and has been read.
-        auto write_z = [&](int c) -> bool {
+        // This warp's block of Z^T (32 lanes x 16 tokens): as it is to TMEM, its decayed pieces in
+        // registers (until D of the chunk before is done).
+        uint32_t zp[NZ][8];
+        auto make_z = [&](int c) -> bool {
             const int s = c % kStages;
             if (!ctl.wait(D_FULL + s, (c / kStages) & 1)) return false;
             // the products that read this buffer of Z^T two chunks ago
@@ -422,7 +423,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             int t0;
             const int cw = sp.c0 + c, rows = chunk_rows(sp, w.rev, cw, t0);
             if (w.cu_seqlens && rows < C) {                  // Y of the next sequence: out of the products
-                for (int i = tid - 128; i < (C - rows) * 2 * 8; i += 256) {
+                for (int i = tid - 128; i < (C - rows) * 2 * 8; i += 512) {
                     const int r = rows + (i >> 4), tile = (i >> 3) & 1, ch = i & 7;
                     *reinterpret_cast<uint4 *>(st + (2 + tile) * TILE + r * 128 + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
@@ -430,61 +431,69 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             }
             // ldmatrix rows: lane i gives token 8 (i / 16) + i % 8 of an 8-column group (i / 8) % 2
             const uint32_t zt = smem_u32(st + (4 + (q4 >> 1)) * TILE);
-            const float *wt = tab + TAB_W + (cw == special ? 64 : 0) + 32 * hf + 2 * (lane & 3);
-            const int row0 = 32 * hf + 8 * (lane >> 4) + (lane & 7), grp = 4 * (q4 & 1) + ((lane >> 3) & 1);
-            // 16 lanes x 16 tokens at a time (a short loop: the roles share the instruction cache)
-#pragma unroll 1
-            for (int it = 0; it < 4; ++it) {
-                const int l = it >> 1, k = it & 1;
-                uint32_t z[4], p1[4], p2[4];
-                ldmatrix_x4_trans(z, zt + sw128_chunk(row0 + 16 * k, grp + 2 * l));
-                const float2 w0 = *reinterpret_cast<const float2 *>(wt + 16 * k), w1 = *reinterpret_cast<const float2 *>(wt + 16 * k + 8);
+            const float *wt = tab + TAB_W + (cw == special ? 64 : 0) + 16 * part + 2 * (lane & 3);
+            const int row0 = 16 * part + 8 * (lane >> 4) + (lane & 7), grp = 4 * (q4 & 1) + ((lane >> 3) & 1);
+            const float2 w0 = *reinterpret_cast<const float2 *>(wt), w1 = *reinterpret_cast<const float2 *>(wt + 8);
+#pragma unroll
+            for (int l = 0; l < 2; ++l) {
+                uint32_t z[4];
+                ldmatrix_x4_trans(z, zt + sw128_chunk(row0, grp + 2 * l));
                 if (rows < C) {                              // rows past the end (a weight of zero would keep a NaN)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int left = rows - (32 * hf + 16 * k + 8 * (e >> 1) + 2 * (lane & 3));
+                        const int left = rows - (16 * part + 8 * (e >> 1) + 2 * (lane & 3));
                         z[e] &= left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
                     }
                 }
-                const uint32_t at = t_lane + ((uint32_t)(16 * l) << 16) + 16 * hf + 8 * k;
-                if (!STATE_ONLY) tmem_st16x128b_x2(at + T_ZR + 32 * (c & 1), z);
+                if (!STATE_ONLY) tmem_st16x128b_x2(t_lane + ((uint32_t)(16 * l) << 16) + T_ZR + 32 * (c & 1) + 8 * part, z);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const uint64_t ww = e < 2 ? pack2(w0.x, w0.y) : pack2(w1.x, w1.y);
                     uint64_t v = mul2(ww, pack2(__uint_as_float(z[e] << 16), __uint_as_float(z[e] & 0xffff0000u)));
-                    z[e] = split_pair(v);
-                    if (NZ == 3) p1[e] = split_pair(v);
-                    p2[e] = NZ == 3 ? high_pair(v) : round_pair(v);
+                    zp[0][4 * l + e] = split_pair(v);
+                    if (NZ == 3) zp[1][4 * l + e] = split_pair(v);
+                    zp[NZ - 1][4 * l + e] = NZ == 3 ? high_pair(v) : round_pair(v);
                 }
-                tmem_st16x128b_x2(at + T_Z, z);
-                if (NZ == 3) tmem_st16x128b_x2(at + T_Z + 32, p1);
-                tmem_st16x128b_x2(at + T_Z + 32 * (NZ - 1), p2);
             }
+            return true;
+        };
+        auto store_z = [&]() {
+#pragma unroll
+            for (int pc = 0; pc < NZ; ++pc)
+#pragma unroll
+                for (int l = 0; l < 2; ++l)
+                    tmem_st16x128b_x2(t_lane + ((uint32_t)(16 * l) << 16) + T_Z + 32 * pc + 8 * part, zp[pc] + 4 * l);
+        };
+        auto announce_z = [&]() {
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[D_ZP]);
-            return true;
         };
         bool ok = true;
-        if (n > 0 && (ok = write_z(0)) && !STATE_ONLY) write_h();
+        if (n > 0 && (ok = make_z(0))) {
+            store_z();
+            announce_z();
+            if (!STATE_ONLY) write_h();
+        }
         for (int c = 0; c < n && ok; ++c) {
+            if (c + 1 < n && !(ok = make_z(c + 1))) break;   // while D of this chunk runs
             if (!(ok = ctl.wait(D_DFULL, c & 1))) break;
             tc_fence_after();
+            if (c + 1 < n) store_z();
             const bool is_special = sp.c0 + c == special;
             const float2 pf = *reinterpret_cast<const float2 *>(tab + TAB_L + (is_special ? 2 : 0));
             const uint64_t ph = pack2(pf.x, pf.x), pl = pack2(pf.y, pf.y);
 #pragma unroll
-            for (int e0 = 0; e0 < 32; e0 += 16) {
-                float d[32];
-                tmem_ld32(t_lane + T_D + 64 * hf + 2 * e0, d);
+            for (int e0 = 0; e0 < 16; e0 += 8) {
+                float d[16];
+                tmem_ld16(t_lane + T_D + 32 * part + 2 * e0, d);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    H[e0 + e] = fma2(ph, H[e0 + e], fma2(pl, H[e0 + e], pack2(d[2 * e], d[2 * e + 1])));
+                for (int e = 0; e < 8; ++e) H[e0 + e] = fma2(ph, H[e0 + e], fma2(pl, H[e0 + e], pack2(d[2 * e], d[2 * e + 1])));
             }
             if (c + 1 < n) {
-                if (!(ok = write_z(c + 1))) break;
+                announce_z();
                 if (!STATE_ONLY) {
                     if (!(ok = ctl.wait(D_XFULL, c & 1))) break;
                     tc_fence_after();
@@ -497,15 +506,15 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
         else if (w.fin && sp.c1 == sp.nchunks) dst = w.fin + ((size_t)sp.b * w.Hv + h) * hstate;
         if (ok && dst) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < 16; ++e) {
                 float a, b;
                 unpack2(H[e], a, b);
-                float *at = dst + (size_t)(64 * hf + 2 * e) * kHeadDim + dz;
+                float *at = dst + (size_t)(32 * part + 2 * e) * kHeadDim + dz;
                 at[0] = a;
                 at[kHeadDim] = b;
             }
         }
-    } else if (warp < 16) {
+    } else if (warp < 24) {
         // ======================================================== P
         regs_dec<kRegsP>();
         const int q4 = warp & 3;
@@ -562,7 +571,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
         regs_dec<kRegsOut>();
         const int q4 = warp & 3;
         const uint32_t t_lane = tmem + ((uint32_t)(q4 * 32) << 16);
-        const bool leader = tid == 512;
+        const bool leader = tid == 768;
         const int t = lane & 3;
         const size_t stride = (size_t)w.Hv * kHeadDim;
         for (int c = 0; c < n && !STATE_ONLY; ++c) {
