@@ -12,7 +12,7 @@
 //   H^T <- lambda^L H^T + D^T                           (fp32 registers)
 // Unlike the delta rule, D does not depend on the state: the chain from chunk to chunk
 // is one fused multiply-add per state element.  The state therefore lives in registers
-// (32 per thread over 512 threads), and only its bf16 rounding goes to the tensor core.
+// (64 per thread over 256 threads), and only its bf16 rounding goes to the tensor core.
 //
 // Roundings: H is rounded to bf16 where it meets X, as every operand of a bf16 product: its
 // 128 terms average the rounding out to that of O itself.  P, of which a short sequence has
@@ -25,19 +25,17 @@
 // One CTA per (sequence or segment, V head), warp-specialised:
 //   warp 0      TMA producer: X, Y, Z tiles, four stages of 48 KB
 //   warp 1      issues the D MMAs, warp 2 the G and O MMAs (one elected thread each, in order)
-//   warps 4-19  state: thread = TMEM lane (z dimension) and a quarter of the 128 columns;
+//   warps 4-11  state: thread = TMEM lane (z dimension) and half of the 128 columns;
 //               copies Z^T and its decayed pieces to TMEM, adds D to the state, writes H
-//   warps 20-23 G -> P (shared memory)
-//   warps 24-27 O epilogue (stmatrix, TMA store)
-#include <type_traits>
-
+//   warps 12-15 G -> P (shared memory)
+//   warps 16-19 O epilogue (stmatrix, TMA store)
 #include "tc_common.cuh"
 #include "decay_common.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kDtThreads = 896;
+constexpr int kDtThreads = 640;
 constexpr int kStages = 4;
 constexpr uint32_t kStageBytes = 6 * TILE;            // [X0][X1][Y0][Y1][Z0][Z1], 64 columns each
 
@@ -59,9 +57,9 @@ constexpr uint32_t DOFF_BAR = DOFF_TAB + TAB_FLOATS * 4;
 enum : int {
     D_FULL = 0,                    // x4: tiles of a stage landed
     D_EMPTY = 4,                   // x4: stage no longer read (both issuers)
-    D_ZP = 8,                      // Z and Z' written, D of the chunk before read (16 warps)
+    D_ZP = 8,                      // Z and Z' written, D of the chunk before read (8 warps)
     D_DFULL = 9,                   // D done
-    D_HREADY = 10,                 // H written (16 warps)
+    D_HREADY = 10,                 // H written (8 warps)
     D_XFULL = 11,                  // H's share of O done
     D_GFULL = 12,                  // G done
     D_PREADY = 13,                 // P written (4 warps)
@@ -80,10 +78,10 @@ static_assert(DOFF_TAB % 16 == 0 && DOFF_BAR % 8 == 0, "alignment");
 constexpr uint32_t IDD_G = idesc_bf16(64, 64, false, false);
 constexpr uint32_t IDD_O = idesc_bf16(128, 64, false, false);
 constexpr uint32_t IDD_D = idesc_bf16(128, 128, false, true);
-// Registers per thread: 896 x 72 at launch; the issuing warpgroup gives part of its share to
-// the four that hold the state (a spilled register is an L2 round trip here, because the
-// shared memory leaves no L1): 40 + 4 x 88 + 2 x 56 = 7 x 72.
-constexpr int kRegsIssue = 40, kRegsState = 88, kRegsP = 56, kRegsOut = 56;
+// Registers per thread: 640 x 96 at launch; the warpgroups without state give part of their
+// share to the two that hold it (a spilled register is an L2 round trip here, because the
+// shared memory leaves no L1): 40 + 2 x 160 + 2 x 56 <= 5 x 96.
+constexpr int kRegsIssue = 40, kRegsState = 160, kRegsP = 56, kRegsOut = 56;
 constexpr double kScaleFloor = -69.31471805599453;    // log of 2^-100
 
 template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -118,17 +116,17 @@ struct DecayCtl {
     uint64_t *bar;
     volatile int *abort_flag;
     // One thread.  (Inlined and short: a call would not let ptxas give the roles their own
-    // register counts.)  A try suspends for up to 20 us, so the limit is about two seconds.
+    // register counts, and the loops of all roles share the instruction cache.)  A try
+    // suspends for up to 20 us, so the limit is about two seconds.
     __device__ __forceinline__ bool wait_one(int i, uint32_t parity) const {
-        if (mbar_try_wait(&bar[i], parity)) return true;
+        bool got = mbar_try_wait(&bar[i], parity);
 #pragma unroll 1
-        for (int k = 0; k < 100000; ++k) {
-            if (mbar_try_wait_suspend(&bar[i], parity, 20000)) return true;
-            if (*abort_flag) return false;
+        for (int k = 100000; !got && k > 0; --k) {
+            got = mbar_try_wait_suspend(&bar[i], parity, 20000);
+            if (*abort_flag) k = 0;
         }
-        *abort_flag = 1;
-        atomicOr(&g_tc_error, 1u);
-        return false;
+        if (!got) *abort_flag = 1;
+        return got;
     }
     // All lanes of the warp wait; the answer is the same for all of them.  Roles that meet at
     // a named barrier agree on it there before any of them leaves.
@@ -162,12 +160,12 @@ __device__ __forceinline__ uint32_t round_pair(uint64_t v) {
 template <typename OT>
 __device__ __forceinline__ void store_rows(OT *dst, uint32_t t_lane, const float *gt, int rows, size_t stride) {
 #pragma unroll 1
-    for (int r0 = 0; r0 < C; r0 += 32) {
-        float x[32];
-        tmem_ld32(t_lane + T_O + r0, x);
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+        float x[8];
+        tmem_ld8(t_lane + T_O + r0, x);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
+        for (int e = 0; e < 8; ++e)
             if (r0 + e < rows) dst[(size_t)(r0 + e) * stride] = from_f32<OT>(gt[r0 + e] * x[e]);
     }
 }
@@ -205,7 +203,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
         prefetch_tensormap(&tm_y);
         prefetch_tensormap(&tm_z);
         for (int i = 0; i < (int)D_NBAR; ++i)
-            mbar_init(&bar[i], i == D_ZP || i == D_HREADY ? 16 : i == D_PREADY || i == D_OFREE ? 4
+            mbar_init(&bar[i], i == D_ZP || i == D_HREADY ? 8 : i == D_PREADY || i == D_OFREE ? 4
                                : i >= D_EMPTY && i < D_EMPTY + kStages && !STATE_ONLY ? 2 : 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -364,95 +362,102 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             }
             __syncwarp();
         }
-    } else if (warp < 20) {
+    } else if (warp < 12) {
         // ======================================================== state
         regs_inc<kRegsState>();
         const int q4 = warp & 3, part = (warp - 4) >> 2;
         const int dz = q4 * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(q4 * 32) << 16);
-        uint64_t H[16];                                      // H^T[dz][32 part + 2 e], +1
+        uint64_t H[32];                                      // H^T[dz][64 part + 2 e], +1
 #pragma unroll
-        for (int e = 0; e < 16; ++e) H[e] = 0;
+        for (int e = 0; e < 32; ++e) H[e] = 0;
         if (w.nseg > 1 && !STATE_ONLY) {
 #pragma unroll 1
             for (int g = 0; g <= sp.seg; ++g) {
                 const float f = tab[TAB_SEG + g];
-                const float *src = w.seg + (((size_t)sp.b * w.nseg + g) * w.Hv + h) * hstate + (size_t)32 * part * kHeadDim + dz;
+                const float *src = w.seg + (((size_t)sp.b * w.nseg + g) * w.Hv + h) * hstate + (size_t)64 * part * kHeadDim + dz;
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
+                for (int e = 0; e < 32; ++e)
                     H[e] = fma2(pack2(f, f), pack2(src[(size_t)(2 * e) * kHeadDim], src[(size_t)(2 * e + 1) * kHeadDim]), H[e]);
             }
         } else if (w.init && (!STATE_ONLY || sp.copy_init)) {
             const float f = (w.init_decays && sp.L > 0) ? tab[TAB_PW + 1] : 1.f;
             const float *src = w.init + ((size_t)sp.b * w.Hv + h) * hstate;
             if (w.init_trans) {
-                const float4 *row = reinterpret_cast<const float4 *>(src + (size_t)dz * kHeadDim + 32 * part);
+                const float4 *row = reinterpret_cast<const float4 *>(src + (size_t)dz * kHeadDim + 64 * part);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < 16; ++e) {
                     const float4 v = row[e];
                     H[2 * e] = pack2(f * v.x, f * v.y);
                     H[2 * e + 1] = pack2(f * v.z, f * v.w);
                 }
             } else {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float *at = src + (size_t)(32 * part + 2 * e) * kHeadDim + dz;
+                for (int e = 0; e < 32; ++e) {
+                    const float *at = src + (size_t)(64 * part + 2 * e) * kHeadDim + dz;
                     H[e] = pack2(f * at[0], f * at[kHeadDim]);
                 }
             }
         }
         auto write_h = [&]() {
-            uint32_t hp[16];
+            uint32_t hp[32];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) hp[e] = round_pair(H[e]);
-            tmem_st16u(t_lane + T_H + 16 * part, hp);
+            for (int e = 0; e < 32; ++e) hp[e] = round_pair(H[e]);
+            tmem_st32u(t_lane + T_H + 32 * part, hp);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[D_HREADY]);
         };
-        // This warp's block of Z^T (32 lanes x 16 tokens): as it is to TMEM, its decayed pieces in
-        // registers (until D of the chunk before is done).
-        uint32_t zp[NZ][8];
+        // This warp's block of Z^T (32 lanes x 32 tokens): as it is to TMEM, its decayed pieces in
+        // registers (until D of the chunk before is done).  zp[.][8 l + 4 k + 2 m + r]: lanes
+        // 16 l + 8 r + lane / 4, tokens 16 k + 8 m + 2 (lane % 4), +1 of the block.
+        uint32_t zp[NZ][16];
+        // ldmatrix rows: lane i gives token 8 (i / 16) + i % 8 of an 8-column group (i / 8) % 2;
+        // the second 16 lanes' group differs in bit 1 of the chunk index, 32 in the address
+        const uint32_t z_at = sbase + (4 + (q4 >> 1)) * TILE +
+                              sw128_chunk(32 * part + 8 * (lane >> 4) + (lane & 7), 4 * (q4 & 1) + ((lane >> 3) & 1));
+        const int my_token = 32 * part + 2 * (lane & 3);
         auto make_z = [&](int c) -> bool {
             const int s = c % kStages;
             if (!ctl.wait(D_FULL + s, (c / kStages) & 1)) return false;
             // the products that read this buffer of Z^T two chunks ago
             if (!STATE_ONLY && c >= 2 && !ctl.wait(D_OFULL + (c & 1), ((c >> 1) - 1) & 1)) return false;
-            unsigned char *st = sm + s * kStageBytes;
-            int t0;
-            const int cw = sp.c0 + c, rows = chunk_rows(sp, w.rev, cw, t0);
-            if (w.cu_seqlens && rows < C) {                  // Y of the next sequence: out of the products
-                for (int i = tid - 128; i < (C - rows) * 2 * 8; i += 512) {
-                    const int r = rows + (i >> 4), tile = (i >> 3) & 1, ch = i & 7;
-                    *reinterpret_cast<uint4 *>(st + (2 + tile) * TILE + r * 128 + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
-                }
+            const bool sp_c = sp.c0 + c == special;
+            const int rows = sp_c ? tail : C;
+            if (w.cu_seqlens && rows < C) {
+                // rows of the next sequence out of the products: Y together, of Z the block read below
+                unsigned char *y = sm + s * kStageBytes + 2 * TILE;
+                for (int i = tid - 128; i < (C - rows) * 2 * 8; i += 256)
+                    *reinterpret_cast<uint4 *>(y + ((i >> 3) & 1) * TILE + (rows + (i >> 4)) * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                unsigned char *z = sm + s * kStageBytes + (4 + (q4 >> 1)) * TILE;
+                if (32 * part + lane >= rows)
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<uint4 *>(z + sw128_chunk(32 * part + lane, 4 * (q4 & 1) + k)) = make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
+                __syncwarp();
             }
-            // ldmatrix rows: lane i gives token 8 (i / 16) + i % 8 of an 8-column group (i / 8) % 2
-            const uint32_t zt = smem_u32(st + (4 + (q4 >> 1)) * TILE);
-            const float *wt = tab + TAB_W + (cw == special ? 64 : 0) + 16 * part + 2 * (lane & 3);
-            const int row0 = 16 * part + 8 * (lane >> 4) + (lane & 7), grp = 4 * (q4 & 1) + ((lane >> 3) & 1);
-            const float2 w0 = *reinterpret_cast<const float2 *>(wt), w1 = *reinterpret_cast<const float2 *>(wt + 8);
+            const float *wt = tab + TAB_W + (sp_c ? 64 : 0) + my_token;
+            const uint32_t at = z_at + s * kStageBytes;
 #pragma unroll
-            for (int l = 0; l < 2; ++l) {
-                uint32_t z[4];
-                ldmatrix_x4_trans(z, zt + sw128_chunk(row0, grp + 2 * l));
-                if (rows < C) {                              // rows past the end (a weight of zero would keep a NaN)
+            for (int k = 0; k < 2; ++k) {
+                const float2 w0 = *reinterpret_cast<const float2 *>(wt + 16 * k), w1 = *reinterpret_cast<const float2 *>(wt + 16 * k + 8);
+#pragma unroll
+                for (int l = 0; l < 2; ++l) {
+                    uint32_t z[4];
+                    ldmatrix_x4_trans(z, (at ^ (32 * l)) + 2048 * k);
+                    if (!STATE_ONLY)
+                        tmem_st16x128b_x2(t_lane + ((uint32_t)(16 * l) << 16) + T_ZR + 32 * (c & 1) + 16 * part + 8 * k, z);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int left = rows - (16 * part + 8 * (e >> 1) + 2 * (lane & 3));
-                        z[e] &= left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+                        const uint64_t ww = e < 2 ? pack2(w0.x, w0.y) : pack2(w1.x, w1.y);
+                        uint64_t v = mul2(ww, pack2(__uint_as_float(z[e] << 16), __uint_as_float(z[e] & 0xffff0000u)));
+                        const int x = 8 * l + 4 * k + e;
+                        zp[0][x] = split_pair(v);
+                        if (NZ == 3) zp[1][x] = split_pair(v);
+                        zp[NZ - 1][x] = NZ == 3 ? high_pair(v) : round_pair(v);
                     }
-                }
-                if (!STATE_ONLY) tmem_st16x128b_x2(t_lane + ((uint32_t)(16 * l) << 16) + T_ZR + 32 * (c & 1) + 8 * part, z);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint64_t ww = e < 2 ? pack2(w0.x, w0.y) : pack2(w1.x, w1.y);
-                    uint64_t v = mul2(ww, pack2(__uint_as_float(z[e] << 16), __uint_as_float(z[e] & 0xffff0000u)));
-                    zp[0][4 * l + e] = split_pair(v);
-                    if (NZ == 3) zp[1][4 * l + e] = split_pair(v);
-                    zp[NZ - 1][4 * l + e] = NZ == 3 ? high_pair(v) : round_pair(v);
                 }
             }
             return true;
@@ -462,7 +467,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             for (int pc = 0; pc < NZ; ++pc)
 #pragma unroll
                 for (int l = 0; l < 2; ++l)
-                    tmem_st16x128b_x2(t_lane + ((uint32_t)(16 * l) << 16) + T_Z + 32 * pc + 8 * part, zp[pc] + 4 * l);
+                    tmem_st16x128b_x4(t_lane + ((uint32_t)(16 * l) << 16) + T_Z + 32 * pc + 16 * part, zp[pc] + 8 * l);
         };
         auto announce_z = [&]() {
             tmem_wait_st();
@@ -485,9 +490,9 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             const float2 pf = *reinterpret_cast<const float2 *>(tab + TAB_L + (is_special ? 2 : 0));
             const uint64_t ph = pack2(pf.x, pf.x), pl = pack2(pf.y, pf.y);
 #pragma unroll
-            for (int e0 = 0; e0 < 16; e0 += 8) {
+            for (int e0 = 0; e0 < 32; e0 += 8) {
                 float d[16];
-                tmem_ld16(t_lane + T_D + 32 * part + 2 * e0, d);
+                tmem_ld16(t_lane + T_D + 64 * part + 2 * e0, d);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 8; ++e) H[e0 + e] = fma2(ph, H[e0 + e], fma2(pl, H[e0 + e], pack2(d[2 * e], d[2 * e + 1])));
@@ -506,73 +511,117 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
         else if (w.fin && sp.c1 == sp.nchunks) dst = w.fin + ((size_t)sp.b * w.Hv + h) * hstate;
         if (ok && dst) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < 32; ++e) {
                 float a, b;
                 unpack2(H[e], a, b);
-                float *at = dst + (size_t)(32 * part + 2 * e) * kHeadDim + dz;
+                float *at = dst + (size_t)(64 * part + 2 * e) * kHeadDim + dz;
                 at[0] = a;
                 at[kHeadDim] = b;
             }
         }
-    } else if (warp < 24) {
+    } else if (warp < 16) {
         // ======================================================== P
         regs_dec<kRegsP>();
         const int q4 = warp & 3;
         const uint32_t t_lane = tmem + ((uint32_t)(q4 * 32) << 16);
         const int g = lane >> 2, t = lane & 3, i0 = 16 * q4 + g;         // rows i0, i0 + 8
         unsigned char *pt = sm + DOFF_P + i0 * 128 + 4 * t;
-        for (int c = 0; c < n && !STATE_ONLY; ++c) {
-            const bool sp_c = sp.c0 + c == special;
-            const float *ct = tab + TAB_C + (sp_c ? 64 : 0), *ft = tab + TAB_F + (sp_c ? 64 : 0);
-            // M = 64 accumulators sit in lanes 0-15 of every quarter
-            if (!ctl.wait(D_GFULL, c & 1)) break;
-            tc_fence_after();
-            // the MMAs of the chunk before have read its P
-            if (c > 0 && !ctl.wait(D_OFULL + ((c - 1) & 1), ((c - 1) >> 1) & 1)) break;
-            auto make_p = [&](auto strong_tag) {
-                const float r0 = strong_tag ? 1.f / ft[i0] : 0.f, r1 = strong_tag ? 1.f / ft[i0 + 8] : 0.f;
-#pragma unroll 1
-                for (int hj = 0; hj < 2; ++hj) {             // 32 columns
-                    uint32_t r[16];
-                    tmem_ld16x256b_x4(t_lane + T_G + 32 * hj, r);
-                    tmem_wait_ld();
+        // Blocks of 8 columns past this warp's 16 rows are zeros for good; the two on the diagonal
+        // are multiplied by a mask.  sgn (i - j) = tokens from j to i in walking order.
+        const int sgn = w.rev ? -1 : 1;
+        uint64_t mask[2][2];                                 // [block][half of the rows]
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const int k = 4 * hj + kk, j = 8 * k + 2 * t;
-                        float2 sc = *reinterpret_cast<const float2 *>(ct + j);
+        for (int d = 0; d < 2; ++d)
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const int i = i0 + 8 * half;
-                            const int e = w.rev ? j - i : i - j, e1 = w.rev ? e + 1 : e - 1;
-                            if (strong_tag) {
-                                const float rr = half ? r1 : r0;
-                                sc.x = tab[TAB_PW + max(e, 0)] * rr;
-                                sc.y = tab[TAB_PW + max(e1, 0)] * rr;
-                            }
-                            const uint32_t *v2 = r + 4 * kk + 2 * half;
-                            uint64_t v = pack2(e >= 0 ? sc.x * __uint_as_float(v2[0]) : 0.f,
-                                               e1 >= 0 ? sc.y * __uint_as_float(v2[1]) : 0.f);
-                            unsigned char *at = pt + half * 1024 + ((k ^ g) << 4);   // (i0 + 8 half) & 7 = g
-                            *reinterpret_cast<uint32_t *>(at) = split_pair(v);
-                            *reinterpret_cast<uint32_t *>(at + TILE) = round_pair(v);
-                        }
-                    }
+            for (int half = 0; half < 2; ++half) {
+                const int e = sgn * (g + 8 * half - 8 * d - 2 * t);
+                mask[d][half] = pack2(e >= 0 ? 1.f : 0.f, e - sgn >= 0 ? 1.f : 0.f);
+            }
+        if (!STATE_ONLY) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    *reinterpret_cast<uint32_t *>(pt + half * 1024 + ((k ^ g) << 4)) = 0u;
+                    *reinterpret_cast<uint32_t *>(pt + half * 1024 + ((k ^ g) << 4) + TILE) = 0u;
                 }
-            };
-            if (strong) make_p(std::true_type{});
-            else make_p(std::false_type{});
+        }
+        auto wait_p = [&](int c) -> bool {
+            // M = 64 accumulators sit in lanes 0-15 of every quarter
+            if (!ctl.wait(D_GFULL, c & 1)) return false;
+            // the MMAs of the chunk before have read its P
+            if (c > 0 && !ctl.wait(D_OFULL + ((c - 1) & 1), ((c - 1) >> 1) & 1)) return false;
+            tc_fence_after();
+            return true;
+        };
+        auto store_p = [&](int k, int half, uint64_t v) {
+            unsigned char *at = pt + half * 1024 + ((k ^ g) << 4);       // (i0 + 8 half) & 7 = g
+            *reinterpret_cast<uint32_t *>(at) = split_pair(v);
+            *reinterpret_cast<uint32_t *>(at + TILE) = round_pair(v);
+        };
+        auto announce_p = [&]() {
             tc_fence_before();
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[D_PREADY]);      // and G is read
+            if (lane == 0) mbar_arrive(&bar[D_PREADY]);                  // and G is read
+        };
+        if (!strong) {
+            for (int c = 0; c < n && !STATE_ONLY; ++c) {
+                if (!wait_p(c)) break;
+                const float *ct = tab + TAB_C + (sp.c0 + c == special ? 64 : 0) + 2 * t;
+#pragma unroll 1
+                for (int b = w.rev ? q4 : 0, bn = w.rev ? 4 : q4 + 1; b < bn; ++b) {   // 16 columns
+                    uint32_t r[8];
+                    tmem_ld16x256b_x2(t_lane + T_G + 16 * b, r);
+                    uint64_t s2[2];
+#pragma unroll
+                    for (int d = 0; d < 2; ++d) {
+                        const float2 sc = *reinterpret_cast<const float2 *>(ct + 16 * b + 8 * d);
+                        s2[d] = pack2(sc.x, sc.y);
+                    }
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int d = 0; d < 2; ++d)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            uint64_t v = mul2(s2[d], pack2(__uint_as_float(r[4 * d + 2 * half]), __uint_as_float(r[4 * d + 2 * half + 1])));
+                            if (b == q4) v = mul2(v, mask[d][half]);
+                            store_p(2 * b + d, half, v);
+                        }
+                }
+                announce_p();
+            }
+        } else {
+            for (int c = 0; c < n && !STATE_ONLY; ++c) {
+                if (!wait_p(c)) break;
+                const float *ft = tab + TAB_F + (sp.c0 + c == special ? 64 : 0);
+#pragma unroll 1
+                for (int k = 0; k < 8; ++k) {
+                    uint32_t r[4];
+                    tmem_ld16x256b_x1(t_lane + T_G + 8 * k, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int e = sgn * (i0 + 8 * half - 8 * k - 2 * t), e1 = e - sgn;
+                        const float f = 1.f / ft[i0 + 8 * half];
+                        store_p(k, half, pack2(e >= 0 ? f * tab[TAB_PW + e] * __uint_as_float(r[2 * half]) : 0.f,
+                                               e1 >= 0 ? f * tab[TAB_PW + e1] * __uint_as_float(r[2 * half + 1]) : 0.f));
+                    }
+                }
+                announce_p();
+            }
         }
     } else {
         // ======================================================== O
         regs_dec<kRegsOut>();
         const int q4 = warp & 3;
         const uint32_t t_lane = tmem + ((uint32_t)(q4 * 32) << 16);
-        const bool leader = tid == 768;
+        const bool leader = tid == 512;
         const int t = lane & 3;
+        // stmatrix rows: lane i gives token 8 (i / 16) + i % 8 of the 8-column group (i / 8) % 2; the
+        // second 16 lanes' group differs in bit 1 of the chunk index, 32 in the address
+        const uint32_t o_at = sbase + DOFF_O + (q4 >> 1) * TILE +
+                              sw128_chunk(8 * (lane >> 4) + (lane & 7), 4 * (q4 & 1) + ((lane >> 3) & 1));
         const size_t stride = (size_t)w.Hv * kHeadDim;
         for (int c = 0; c < n && !STATE_ONLY; ++c) {
             const int cw = sp.c0 + c;
@@ -591,33 +640,32 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                 if (lane == 0) mbar_arrive(&bar[D_OFREE]);
                 continue;
             }
-            const uint32_t stage = smem_u32(sm + DOFF_O);
-            const int mt = lane >> 3, mi = lane & 7;         // stored row mi of matrix mt
 #pragma unroll 1
-            for (int it = 0; it < 4; ++it) {                 // 32-token block, 16-lane slab
-                const int cb = it >> 1, slab = it & 1;
-                uint32_t r[16];
-                tmem_ld16x256b_x4(t_lane + ((uint32_t)(16 * slab) << 16) + T_O + 32 * cb, r);
-                tmem_wait_ld();
-                if (it == 3) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar[D_OFREE]);
-                }
+            for (int cb = 0; cb < 2; ++cb) {                 // 32 tokens
+                float2 f[4];
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    uint32_t m[4];
+                for (int k = 0; k < 4; ++k) f[k] = *reinterpret_cast<const float2 *>(ft + 32 * cb + 8 * k + 2 * t);
 #pragma unroll
-                    for (int mm = 0; mm < 4; ++mm) {
-                        const int k = 2 * kk + (mm >> 1);
-                        const float2 f = *reinterpret_cast<const float2 *>(ft + 32 * cb + 8 * k + 2 * t);
-                        const uint32_t *v = r + 4 * k + 2 * (mm & 1);
-                        m[mm] = round_pair(mul2(pack2(f.x, f.y), pack2(__uint_as_float(v[0]), __uint_as_float(v[1]))));
+                for (int slab = 0; slab < 2; ++slab) {       // 16 lanes
+                    uint32_t r[16];
+                    tmem_ld16x256b_x4(t_lane + ((uint32_t)(16 * slab) << 16) + T_O + 32 * cb, r);
+                    tmem_wait_ld();
+                    if (cb == 1 && slab == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar[D_OFREE]);
                     }
-                    const int orow = 32 * cb + 8 * (2 * kk + (mt >> 1)) + mi;       // token
-                    const int jst = q4 * 32 + 16 * slab + 8 * (mt & 1);             // first z of the block
-                    stmatrix_x4_trans(stage + (jst >> 6) * TILE + sw128_chunk(orow, (jst & 63) >> 3),
-                                      m[0], m[1], m[2], m[3]);
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) {
+                        uint32_t m[4];
+#pragma unroll
+                        for (int mm = 0; mm < 4; ++mm) {
+                            const int k = 2 * kk + (mm >> 1);
+                            const uint32_t *v = r + 4 * k + 2 * (mm & 1);
+                            m[mm] = round_pair(mul2(pack2(f[k].x, f[k].y), pack2(__uint_as_float(v[0]), __uint_as_float(v[1]))));
+                        }
+                        stmatrix_x4_trans((o_at ^ (32 * slab)) + 4096 * cb + 2048 * kk, m[0], m[1], m[2], m[3]);
+                    }
                 }
             }
             fence_proxy_async_smem();
@@ -635,6 +683,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
     if (warp == 0) {
         tc_fence_after();
         tmem_dealloc(tmem, T_COLS);
+        if (lane == 0 && *abort_flag) atomicOr(&g_tc_error, 1u);
     }
 }
 

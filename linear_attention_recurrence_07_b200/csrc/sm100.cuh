@@ -186,7 +186,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
           "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
-// 16 consecutive columns, same lane mapping.
+// 8 and 16 consecutive columns, same lane mapping.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float *v) {
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float *v) {
     uint32_t *r = reinterpret_cast<uint32_t *>(v);
     asm volatile(
@@ -224,12 +230,27 @@ __device__ __forceinline__ void tmem_ld16x256b_x4(uint32_t taddr, uint32_t *r) {
           "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
-// 16 lanes x 128 bits, twice along the columns (8 columns), stored: thread t of the warp
-// gives, for k = 0, 1, r[2k] = lane (base + t/4), column col + 4k + t%4, and r[2k+1] = the same
+// The same twice and once along the columns (16, 8 columns).
+__device__ __forceinline__ void tmem_ld16x256b_x2(uint32_t taddr, uint32_t *r) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld16x256b_x1(uint32_t taddr, uint32_t *r) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr));
+}
+// 16 lanes x 128 bits, two (four) times along the columns (8, 16 columns), stored: thread t of the
+// warp gives, for k = 0, 1 (.. 3), r[2k] = lane (base + t/4), column col + 4k + t%4, and r[2k+1] = the same
 // column of lane (base + 8 + t/4): pairs as ldmatrix.trans delivers them.
 __device__ __forceinline__ void tmem_st16x128b_x2(uint32_t taddr, const uint32_t *r) {
     asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};"
                  ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+__device__ __forceinline__ void tmem_st16x128b_x4(uint32_t taddr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 // Four 8x8 bf16 matrices, loaded transposed: thread t gives the address of row t%8 of matrix
 // t/8 and gets, of matrix i, rows 2(t%4), +1 (low, high half) of column t/4.
