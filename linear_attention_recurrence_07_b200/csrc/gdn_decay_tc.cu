@@ -5,8 +5,8 @@
 // Per chunk of L <= 64 tokens, H the state at its start (decayed to its first token),
 // p_i = i forwards, L - 1 - i backwards:
 //   G    = X Y^T                                        M=64  N=64  K=128
-//   P_ij = lambda^{-p_j} G_ij, j at or before i         (two bf16 pieces)
-//   O^T  = (H^T X^T + Z^T P^T) diag(lambda^p)           M=128 N=64  K=128 + 2x64
+//   P_ij = lambda^{-p_j} G_ij, j at or before i         (NP bf16 pieces)
+//   O^T  = (H^T X^T + Z^T P^T) diag(lambda^p)           M=128 N=64  K=128 + NP x 64
 //   D^T  = Z'^T Y, Z' = diag(lambda^{L-p}) Z in NZ bf16 pieces
 //                                                       M=128 N=128 K=NZ x 64
 //   H^T <- lambda^L H^T + D^T                           (fp32 registers)
@@ -14,9 +14,10 @@
 // is one fused multiply-add per state element.  The state therefore lives in registers
 // (64 per thread over 256 threads), and only its bf16 rounding goes to the tensor core.
 //
-// Roundings: H is rounded to bf16 where it meets X, as every operand of a bf16 product: its
-// 128 terms average the rounding out to that of O itself.  P, of which a short sequence has
-// few terms, keeps 16 bits in two pieces.  Z' has three pieces, all 24 bits, where an end
+// Roundings: H and P are rounded to bf16 where they meet X and Z, as every operand of a bf16
+// product: the terms of a row average it out to about the rounding of O itself.  Sequences of
+// one chunk, whose first rows have few terms and no H, get 16 bits of P in two pieces (they
+// are bound by latency, and the pieces share the room of P's second buffer).  Z' has three pieces, all 24 bits, where an end
 // state is wanted, two where the state only feeds O; small pieces are accumulated first,
 // because the tensor core truncates.  lambda^{-p_j}
 // grows to lambda^{-63}: below lambda = 2^-(100/63) the scale is held at 2^100, which
@@ -26,7 +27,7 @@
 //   warp 0      TMA producer: X, Y, Z tiles, four stages of 48 KB
 //   warp 1      issues the D MMAs, warp 2 the G and O MMAs (one elected thread each, in order)
 //   warps 4-11  state: thread = TMEM lane (z dimension) and half of the 128 columns;
-//               copies Z^T and its decayed pieces to TMEM, adds D to the state, writes H
+//               writes the decayed pieces of Z^T to TMEM, adds D to the state, writes H
 //   warps 12-15 G -> P (shared memory)
 //   warps 16-19 O epilogue (stmatrix, TMA store)
 #include "tc_common.cuh"
@@ -43,12 +44,11 @@ constexpr uint32_t kStageBytes = 6 * TILE;            // [X0][X1][Y0][Y1][Z0][Z1
 constexpr uint32_t T_D = 0;        // D^T, 128 fp32 columns
 constexpr uint32_t T_H = 128;      // H^T rounded, 64 packed columns
 constexpr uint32_t T_Z = 192;      // Z'^T pieces, 32 packed columns each
-constexpr uint32_t T_ZR = 288;     // Z^T, 32 packed columns, two buffers
-constexpr uint32_t T_G = 352;
+constexpr uint32_t T_G = 288;      // two buffers of 64, chunk c uses c % 2
 constexpr uint32_t T_O = 416;
 constexpr uint32_t T_COLS = 512;
 
-constexpr uint32_t DOFF_P = kStages * kStageBytes;    // P pieces: high, low
+constexpr uint32_t DOFF_P = kStages * kStageBytes;    // two buffers, chunk c uses c % 2, or the two pieces
 constexpr uint32_t DOFF_O = DOFF_P + 2 * TILE;
 constexpr uint32_t DOFF_TAB = DOFF_O + 2 * TILE;      // powers; per token: Z weights, O scales, P scales
 constexpr uint32_t TAB_PW = 0, TAB_W = 66, TAB_F = 66 + 128, TAB_C = 66 + 256, TAB_L = 66 + 3 * 128,
@@ -57,26 +57,27 @@ constexpr uint32_t DOFF_BAR = DOFF_TAB + TAB_FLOATS * 4;
 enum : int {
     D_FULL = 0,                    // x4: tiles of a stage landed
     D_EMPTY = 4,                   // x4: stage no longer read (both issuers)
-    D_ZP = 8,                      // Z and Z' written, D of the chunk before read (8 warps)
+    D_ZP = 8,                      // Z' written, D of the chunk before read (8 warps)
     D_DFULL = 9,                   // D done
     D_HREADY = 10,                 // H written (8 warps)
     D_XFULL = 11,                  // H's share of O done
-    D_GFULL = 12,                  // G done
-    D_PREADY = 13,                 // P written (4 warps)
-    // x2, chunk c uses c % 2: O done.  (The state's warps wait for it up to two chunks late; on
-    // one barrier the phase after it could have completed by then.)
-    D_OFULL = 14,
-    D_OFREE = 16,                  // O read (4 warps)
-    D_DRAIN = 17,                  // x2: last MMAs of either issuer
-    D_NBAR = 19
+    D_OFREE = 12,                  // O read (4 warps)
+    D_DRAIN = 13,                  // last MMAs of both issuers
+    // x2, chunk c uses c % 2: P's warps run up to a chunk ahead of the MMAs, and on one barrier
+    // the phase after the awaited one could have completed by the time of the wait.
+    D_GFULL = 14,                  // G done
+    D_PREADY = 16,                 // P written, G read (4 warps)
+    D_OFULL = 18,                  // O done
+    D_NBAR = 20
 };
 constexpr uint32_t DOFF_MISC = DOFF_BAR + D_NBAR * 8;
-constexpr uint32_t D_SMEM = DOFF_MISC + 16 + 1024;
+constexpr uint32_t D_SMEM = DOFF_MISC + 8 + 1024;
 static_assert(D_SMEM <= 232448, "shared memory per CTA");
 static_assert(DOFF_TAB % 16 == 0 && DOFF_BAR % 8 == 0, "alignment");
 
 constexpr uint32_t IDD_G = idesc_bf16(64, 64, false, false);
-constexpr uint32_t IDD_O = idesc_bf16(128, 64, false, false);
+constexpr uint32_t IDD_OX = idesc_bf16(128, 64, false, false);
+constexpr uint32_t IDD_OI = idesc_bf16(128, 64, true, false);
 constexpr uint32_t IDD_D = idesc_bf16(128, 128, false, true);
 // Registers per thread: 640 x 96 at launch; the warpgroups without state give part of their
 // share to the two that hold it (a spilled register is an L2 round trip here, because the
@@ -170,7 +171,7 @@ __device__ __forceinline__ void store_rows(OT *dst, uint32_t t_lane, const float
     }
 }
 
-template <bool STATE_ONLY, int NZ>
+template <bool STATE_ONLY, int NZ, int NP>
 __global__ void __launch_bounds__(kDtThreads, 1)
 decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
                 const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_o,
@@ -203,8 +204,8 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
         prefetch_tensormap(&tm_y);
         prefetch_tensormap(&tm_z);
         for (int i = 0; i < (int)D_NBAR; ++i)
-            mbar_init(&bar[i], i == D_ZP || i == D_HREADY ? 8 : i == D_PREADY || i == D_OFREE ? 4
-                               : i >= D_EMPTY && i < D_EMPTY + kStages && !STATE_ONLY ? 2 : 1);
+            mbar_init(&bar[i], i == D_ZP || i == D_HREADY ? 8 : i == D_PREADY || i == D_PREADY + 1 || i == D_OFREE ? 4
+                               : ((i >= D_EMPTY && i < D_EMPTY + kStages) || i == D_DRAIN) && !STATE_ONLY ? 2 : 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -307,7 +308,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                 if (!ctl.wait(D_FULL + s, (c / kStages) & 1)) return false;
                 // rows past a packed sequence's end are zeroed before Z' is announced
                 if (w.cu_seqlens && sp.c0 + c == special && !ctl.wait(D_ZP, c & 1)) return false;
-                tc_fence_after();                            // G of the chunk before has been read
+                tc_fence_after();                            // G of two chunks before has been read
                 if (elect_one()) {
                     const uint64_t xd = smem_desc_sw128(sbase + s * kStageBytes, 16, 1024);
 #pragma unroll 1
@@ -315,9 +316,9 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const uint64_t at = xd + hk * (TILE >> 4) + k * 2;
-                            mma_bf16(tmem + T_G, at, at + (2 * TILE >> 4), IDD_G, hk > 0 || k > 0);
+                            mma_bf16(tmem + T_G + 64 * (c & 1), at, at + (2 * TILE >> 4), IDD_G, hk > 0 || k > 0);
                         }
-                    mma_commit(&bar[D_GFULL]);
+                    mma_commit(&bar[D_GFULL + (c & 1)]);
                 }
                 __syncwarp();
                 return true;
@@ -325,6 +326,8 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             bool ok = n > 0 && issue_g(0);
             for (int c = 0; c < n && ok; ++c) {
                 const int s = c % kStages;
+                // G one chunk ahead of P; its buffer was read before P of chunk c - 1 was written
+                if (c + 1 < n && !(ok = issue_g(c + 1))) break;
                 if (!ctl.wait(D_HREADY, c & 1)) break;
                 if (c > 0 && !ctl.wait(D_OFREE, (c - 1) & 1)) break;
                 tc_fence_after();
@@ -334,31 +337,29 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                     for (int hk = 0; hk < 2; ++hk)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_bf16_ts(tmem + T_O, tmem + T_H + hk * 32 + k * 8, xd + hk * (TILE >> 4) + k * 2, IDD_O,
+                            mma_bf16_ts(tmem + T_O, tmem + T_H + hk * 32 + k * 8, xd + hk * (TILE >> 4) + k * 2, IDD_OX,
                                         hk > 0 || k > 0);
                     mma_commit(&bar[D_XFULL]);
-                    mma_commit(&bar[D_EMPTY + s]);           // G was issued before
                 }
                 __syncwarp();
-                if (!ctl.wait(D_PREADY, c & 1)) break;
+                if (!ctl.wait(D_PREADY + (c & 1), (c >> 1) & 1)) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    // H written (above) implies Z written
-                    const uint64_t pd = smem_desc_sw128(sbase + DOFF_P, 16, 1024);
+                    const uint64_t zd = smem_desc_sw128(sbase + s * kStageBytes + 4 * TILE, TILE, 1024);
+                    const uint64_t pd = smem_desc_sw128(sbase + DOFF_P + (NP == 1 ? (c & 1) * TILE : 0), 16, 1024);
 #pragma unroll 1
-                    for (int pc = 1; pc >= 0; --pc)
+                    for (int pc = NP - 1; pc >= 0; --pc)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_bf16_ts(tmem + T_O, tmem + T_ZR + (c & 1) * 32 + k * 8, pd + pc * (TILE >> 4) + k * 2, IDD_O,
-                                        true);
+                            mma_bf16(tmem + T_O, zd + k * (2048 >> 4), pd + pc * (TILE >> 4) + k * 2, IDD_OI, true);
                     mma_commit(&bar[D_OFULL + (c & 1)]);
+                    mma_commit(&bar[D_EMPTY + s]);
                 }
                 __syncwarp();
-                if (c + 1 < n) ok = issue_g(c + 1);
             }
             if (elect_one()) {
-                mma_commit(&bar[D_DRAIN + 1]);
-                mbar_wait(&bar[D_DRAIN + 1], 0, 1ll << 30);
+                mma_commit(&bar[D_DRAIN]);
+                mbar_wait(&bar[D_DRAIN], 0, 1ll << 30);
             }
             __syncwarp();
         }
@@ -409,9 +410,9 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[D_HREADY]);
         };
-        // This warp's block of Z^T (32 lanes x 32 tokens): as it is to TMEM, its decayed pieces in
-        // registers (until D of the chunk before is done).  zp[.][8 l + 4 k + 2 m + r]: lanes
-        // 16 l + 8 r + lane / 4, tokens 16 k + 8 m + 2 (lane % 4), +1 of the block.
+        // The decayed pieces of this warp's block of Z^T (32 lanes x 32 tokens) in registers (until
+        // D of the chunk before is done).  zp[.][8 l + 4 k + 2 m + r]: lanes 16 l + 8 r + lane / 4,
+        // tokens 16 k + 8 m + 2 (lane % 4), +1 of the block.
         uint32_t zp[NZ][16];
         // ldmatrix rows: lane i gives token 8 (i / 16) + i % 8 of an 8-column group (i / 8) % 2;
         // the second 16 lanes' group differs in bit 1 of the chunk index, 32 in the address
@@ -421,8 +422,6 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
         auto make_z = [&](int c) -> bool {
             const int s = c % kStages;
             if (!ctl.wait(D_FULL + s, (c / kStages) & 1)) return false;
-            // the products that read this buffer of Z^T two chunks ago
-            if (!STATE_ONLY && c >= 2 && !ctl.wait(D_OFULL + (c & 1), ((c >> 1) - 1) & 1)) return false;
             const bool sp_c = sp.c0 + c == special;
             const int rows = sp_c ? tail : C;
             if (w.cu_seqlens && rows < C) {
@@ -447,8 +446,6 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                 for (int l = 0; l < 2; ++l) {
                     uint32_t z[4];
                     ldmatrix_x4_trans(z, (at ^ (32 * l)) + 2048 * k);
-                    if (!STATE_ONLY)
-                        tmem_st16x128b_x2(t_lane + ((uint32_t)(16 * l) << 16) + T_ZR + 32 * (c & 1) + 16 * part + 8 * k, z);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const uint64_t ww = e < 2 ? pack2(w0.x, w0.y) : pack2(w1.x, w1.y);
@@ -542,54 +539,60 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             for (int k = 0; k < 8; ++k)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    *reinterpret_cast<uint32_t *>(pt + half * 1024 + ((k ^ g) << 4)) = 0u;
-                    *reinterpret_cast<uint32_t *>(pt + half * 1024 + ((k ^ g) << 4) + TILE) = 0u;
+                    *reinterpret_cast<uint32_t *>(pt + half * 1024 + ((k ^ g) << 4)) = 0u;           // both buffers,
+                    *reinterpret_cast<uint32_t *>(pt + half * 1024 + ((k ^ g) << 4) + TILE) = 0u;    // or pieces
                 }
         }
         auto wait_p = [&](int c) -> bool {
             // M = 64 accumulators sit in lanes 0-15 of every quarter
-            if (!ctl.wait(D_GFULL, c & 1)) return false;
-            // the MMAs of the chunk before have read its P
-            if (c > 0 && !ctl.wait(D_OFULL + ((c - 1) & 1), ((c - 1) >> 1) & 1)) return false;
+            if (!ctl.wait(D_GFULL + (c & 1), (c >> 1) & 1)) return false;
+            // the MMAs of two chunks before have read this buffer
+            if (c > 1 && !ctl.wait(D_OFULL + (c & 1), ((c >> 1) - 1) & 1)) return false;
             tc_fence_after();
             return true;
         };
-        auto store_p = [&](int k, int half, uint64_t v) {
+        auto store_p = [&](int c, int k, int half, uint64_t v) {
             unsigned char *at = pt + half * 1024 + ((k ^ g) << 4);       // (i0 + 8 half) & 7 = g
-            *reinterpret_cast<uint32_t *>(at) = split_pair(v);
-            *reinterpret_cast<uint32_t *>(at + TILE) = round_pair(v);
+            if (NP == 2) {
+                *reinterpret_cast<uint32_t *>(at) = split_pair(v);
+                *reinterpret_cast<uint32_t *>(at + TILE) = round_pair(v);
+            } else {
+                *reinterpret_cast<uint32_t *>(at + (c & 1) * TILE) = round_pair(v);
+            }
         };
-        auto announce_p = [&]() {
+        auto announce_p = [&](int c) {
             tc_fence_before();
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[D_PREADY]);                  // and G is read
+            if (lane == 0) mbar_arrive(&bar[D_PREADY + (c & 1)]);                  // and G is read
         };
         if (!strong) {
             for (int c = 0; c < n && !STATE_ONLY; ++c) {
                 if (!wait_p(c)) break;
                 const float *ct = tab + TAB_C + (sp.c0 + c == special ? 64 : 0) + 2 * t;
+                const int bn = w.rev ? 4 : q4 + 1;
+                int b = w.rev ? q4 : 0;                      // 16 columns
+                uint32_t next[8];
+                tmem_ld16x256b_x2(t_lane + T_G + 64 * (c & 1) + 16 * b, next);
 #pragma unroll 1
-                for (int b = w.rev ? q4 : 0, bn = w.rev ? 4 : q4 + 1; b < bn; ++b) {   // 16 columns
+                for (; b < bn; ++b) {
                     uint32_t r[8];
-                    tmem_ld16x256b_x2(t_lane + T_G + 16 * b, r);
-                    uint64_t s2[2];
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) r[x] = next[x];
+                    if (b + 1 < bn) tmem_ld16x256b_x2(t_lane + T_G + 64 * (c & 1) + 16 * (b + 1), next);
 #pragma unroll
                     for (int d = 0; d < 2; ++d) {
                         const float2 sc = *reinterpret_cast<const float2 *>(ct + 16 * b + 8 * d);
-                        s2[d] = pack2(sc.x, sc.y);
-                    }
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int d = 0; d < 2; ++d)
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
-                            uint64_t v = mul2(s2[d], pack2(__uint_as_float(r[4 * d + 2 * half]), __uint_as_float(r[4 * d + 2 * half + 1])));
+                            uint64_t v = mul2(pack2(sc.x, sc.y), pack2(__uint_as_float(r[4 * d + 2 * half]), __uint_as_float(r[4 * d + 2 * half + 1])));
                             if (b == q4) v = mul2(v, mask[d][half]);
-                            store_p(2 * b + d, half, v);
+                            store_p(c, 2 * b + d, half, v);
                         }
+                    }
                 }
-                announce_p();
+                announce_p(c);
             }
         } else {
             for (int c = 0; c < n && !STATE_ONLY; ++c) {
@@ -598,17 +601,17 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
 #pragma unroll 1
                 for (int k = 0; k < 8; ++k) {
                     uint32_t r[4];
-                    tmem_ld16x256b_x1(t_lane + T_G + 8 * k, r);
+                    tmem_ld16x256b_x1(t_lane + T_G + 64 * (c & 1) + 8 * k, r);
                     tmem_wait_ld();
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int e = sgn * (i0 + 8 * half - 8 * k - 2 * t), e1 = e - sgn;
                         const float f = 1.f / ft[i0 + 8 * half];
-                        store_p(k, half, pack2(e >= 0 ? f * tab[TAB_PW + e] * __uint_as_float(r[2 * half]) : 0.f,
+                        store_p(c, k, half, pack2(e >= 0 ? f * tab[TAB_PW + e] * __uint_as_float(r[2 * half]) : 0.f,
                                                e1 >= 0 ? f * tab[TAB_PW + e1] * __uint_as_float(r[2 * half + 1]) : 0.f));
                     }
                 }
-                announce_p();
+                announce_p(c);
             }
         }
     } else {
@@ -687,14 +690,14 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
     }
 }
 
-template <bool STATE_ONLY, int NZ>
+template <bool STATE_ONLY, int NZ, int NP>
 cudaError_t launch_tc(const CUtensorMap &tx, const CUtensorMap &ty, const CUtensorMap &tz, const CUtensorMap &to,
                       const DecayWalk &w, cudaStream_t stream)
 {
-    cudaError_t err = cudaFuncSetAttribute(decay_tc_kernel<STATE_ONLY, NZ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t err = cudaFuncSetAttribute(decay_tc_kernel<STATE_ONLY, NZ, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            (int)D_SMEM);
     if (err != cudaSuccess) return err;
-    decay_tc_kernel<STATE_ONLY, NZ><<<dim3((unsigned)w.Hv, (unsigned)(w.B * w.nseg)), kDtThreads, D_SMEM, stream>>>(
+    decay_tc_kernel<STATE_ONLY, NZ, NP><<<dim3((unsigned)w.Hv, (unsigned)(w.B * w.nseg)), kDtThreads, D_SMEM, stream>>>(
         tx, ty, tz, to, w);
     return cudaGetLastError();
 }
@@ -720,10 +723,12 @@ cudaError_t launch_decay_walk_tc(const DecayWalk &w, cudaStream_t stream)
     if (w.o_f32) to = tx;                        // not used
     else if (!make_map(&to, w.o, rows_b, w.T, w.Hv)) return cudaErrorInvalidValue;
     const bool ends = w.fin != nullptr;          // an end state is wanted: its increments with all 24 bits
+    const bool one_chunk = w.T <= C;
     cudaError_t err = cudaSuccess;
-    if (w.nseg > 1) err = ends ? launch_tc<true, 3>(tx, ty, tz, to, w, stream) : launch_tc<true, 2>(tx, ty, tz, to, w, stream);
+    if (w.nseg > 1) err = ends ? launch_tc<true, 3, 1>(tx, ty, tz, to, w, stream) : launch_tc<true, 2, 1>(tx, ty, tz, to, w, stream);
     if (err != cudaSuccess) return err;
-    return ends ? launch_tc<false, 3>(tx, ty, tz, to, w, stream) : launch_tc<false, 2>(tx, ty, tz, to, w, stream);
+    if (one_chunk) return ends ? launch_tc<false, 3, 2>(tx, ty, tz, to, w, stream) : launch_tc<false, 2, 2>(tx, ty, tz, to, w, stream);
+    return ends ? launch_tc<false, 3, 1>(tx, ty, tz, to, w, stream) : launch_tc<false, 2, 1>(tx, ty, tz, to, w, stream);
 }
 
 }  // namespace gdn
