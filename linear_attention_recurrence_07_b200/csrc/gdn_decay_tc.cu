@@ -136,24 +136,17 @@ struct DecayCtl {
     }
 };
 
-// Upper 16 bits of two floats as a bf16 pair, and their exact remainders.
-__device__ __forceinline__ uint32_t split_pair(uint64_t &v) {
-    float a, b;
-    unpack2(v, a, b);
-    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-    v = sub2(v, pack2(__uint_as_float(ua & 0xffff0000u), __uint_as_float(ub & 0xffff0000u)));
-    return __byte_perm(ua, ub, 0x7632);
-}
-// Upper 16 bits (the last of exact pieces), and rounded to bf16.
-__device__ __forceinline__ uint32_t high_pair(uint64_t v) {
-    float a, b;
-    unpack2(v, a, b);
-    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-}
+// Two floats rounded to a bf16 pair.
 __device__ __forceinline__ uint32_t round_pair(uint64_t v) {
     float a, b;
     unpack2(v, a, b);
     return pack_bf16x2(a, b);
+}
+// The rounded pair, and in v what it leaves over (exact: at most 16 bits of an fp32).
+__device__ __forceinline__ uint32_t split_pair(uint64_t &v) {
+    const uint32_t p = round_pair(v);
+    v = sub2(v, pack2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u)));
+    return p;
 }
 
 // Rows of O from the accumulators one column (token) at a time: ragged chunks of packed
@@ -453,7 +446,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                         const int x = 8 * l + 4 * k + e;
                         zp[0][x] = split_pair(v);
                         if (NZ == 3) zp[1][x] = split_pair(v);
-                        zp[NZ - 1][x] = NZ == 3 ? high_pair(v) : round_pair(v);
+                        zp[NZ - 1][x] = round_pair(v);
                     }
                 }
             }
@@ -486,13 +479,13 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             const bool is_special = sp.c0 + c == special;
             const float2 pf = *reinterpret_cast<const float2 *>(tab + TAB_L + (is_special ? 2 : 0));
             const uint64_t ph = pack2(pf.x, pf.x), pl = pack2(pf.y, pf.y);
-#pragma unroll
-            for (int e0 = 0; e0 < 32; e0 += 8) {
-                float d[16];
-                tmem_ld16(t_lane + T_D + 64 * part + 2 * e0, d);
+            {
+                float d[64];
+                tmem_ld32(t_lane + T_D + 64 * part, d);
+                tmem_ld32(t_lane + T_D + 64 * part + 32, d + 32);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) H[e0 + e] = fma2(ph, H[e0 + e], fma2(pl, H[e0 + e], pack2(d[2 * e], d[2 * e + 1])));
+                for (int e = 0; e < 32; ++e) H[e] = fma2(ph, H[e], fma2(pl, H[e], pack2(d[2 * e], d[2 * e + 1])));
             }
             if (c + 1 < n) {
                 announce_z();
