@@ -508,11 +508,10 @@ gdn_status gdn_decay_decode_step_slots(const void *q, const void *k, const void 
  *      S0, dS_final [B, Hv, dk, dv] fp32 or NULL (zeros).
  * Out (overwritten): dq, dk [B, T, Hqk, dk] and dv [B, T, Hv, dv] of dtype (the
  *      inputs' type, rounded once from fp32); dS0 [B, Hv, dk, dv] fp32 or NULL
- *      (skipped).  Outputs must not overlap inputs or each other, except that
- *      dS0 may be dS_final.
+ *      (skipped).  Outputs must not overlap inputs or each other.
  * workspace: gdn_decay_bwd_workspace(...) bytes for the current device, rules as
  *      for gdn_decay_fwd.  It holds the segments' states and, where QK heads are
- *      shared, one fp32 row per token and V head.
+ *      shared, two fp32 rows per token and V head.
  * Sizes, dtypes and errors as gdn_decay_fwd.  No atomics: repeated calls return
  * the same bits.
  */

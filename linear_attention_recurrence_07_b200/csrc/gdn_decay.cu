@@ -49,8 +49,9 @@ template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bf
 
 template <typename T>
 __global__ void __launch_bounds__(kSimtThreads)
-decay_walk_kernel(const DecayWalk w, bool state_only)
+decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
 {
+    const DecayWalk &w = d.w[blockIdx.z];
     extern __shared__ __align__(16) unsigned char raw[];
     SimtSmem &sm = *reinterpret_cast<SimtSmem *>(raw);
     const int tid = threadIdx.x;
@@ -216,17 +217,18 @@ decay_walk_kernel(const DecayWalk w, bool state_only)
 }
 
 template <typename T>
-cudaError_t launch_typed(const DecayWalk &w, cudaStream_t stream)
+cudaError_t launch_typed(const DecayWalks &d, cudaStream_t stream)
 {
     cudaError_t err = cudaFuncSetAttribute(decay_walk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            (int)sizeof(SimtSmem));
     if (err != cudaSuccess) return err;
-    const dim3 grid((unsigned)w.Hv * kZSlices, (unsigned)(w.B * w.nseg));
+    const DecayWalk &w = d.w[0];
+    const dim3 grid((unsigned)w.Hv * kZSlices, (unsigned)(w.B * w.nseg), (unsigned)d.n);
     if (w.nseg > 1) {
-        decay_walk_kernel<T><<<grid, kSimtThreads, sizeof(SimtSmem), stream>>>(w, true);
+        decay_walk_kernel<T><<<grid, kSimtThreads, sizeof(SimtSmem), stream>>>(d, true);
         if ((err = cudaGetLastError()) != cudaSuccess) return err;
     }
-    decay_walk_kernel<T><<<grid, kSimtThreads, sizeof(SimtSmem), stream>>>(w, false);
+    decay_walk_kernel<T><<<grid, kSimtThreads, sizeof(SimtSmem), stream>>>(d, false);
     return cudaGetLastError();
 }
 
@@ -252,9 +254,9 @@ head_sum_kernel(const float *__restrict__ part, T *__restrict__ out, long long n
 
 }  // namespace
 
-cudaError_t launch_decay_walk_simt(const DecayWalk &w, gdn_dtype dtype, cudaStream_t stream)
+cudaError_t launch_decay_walks_simt(const DecayWalks &d, gdn_dtype dtype, cudaStream_t stream)
 {
-    return dtype == GDN_BF16 ? launch_typed<__nv_bfloat16>(w, stream) : launch_typed<float>(w, stream);
+    return dtype == GDN_BF16 ? launch_typed<__nv_bfloat16>(d, stream) : launch_typed<float>(d, stream);
 }
 
 cudaError_t launch_head_sum(const float *part, void *out, long long rows, int Hqk, int Hv, gdn_dtype dtype,

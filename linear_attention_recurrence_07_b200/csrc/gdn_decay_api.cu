@@ -32,13 +32,13 @@ constexpr size_t kStateBytes = (size_t)gdn::kHeadDim * gdn::kHeadDim * sizeof(fl
 constexpr int kMaxDecaySegments = 16;
 constexpr int kMinSegmentChunks = 4;
 
-// Segments of a dense walk: as many as fill the device with one CTA (fp32: one head's
-// four half-SM CTAs) per head and segment, of at least four chunks, because the launch
-// that computes their start states reads y and z once more.
-void choose_segments(DecayWalk &w, gdn_dtype dtype)
+// Segments of `walks` dense walks that run side by side: as many as fill the device with
+// one CTA (fp32: one head's four half-SM CTAs) per walk, head and segment, of at least four
+// chunks, because the launch that computes their start states reads y and z once more.
+void choose_segments(DecayWalk &w, int walks, gdn_dtype dtype)
 {
     const int nchunks = (w.T + gdn::kChunk - 1) / gdn::kChunk;
-    const long long units = (long long)w.B * w.Hv * (dtype == GDN_F32 ? 2 : 1);
+    const long long units = (long long)w.B * w.Hv * walks * (dtype == GDN_F32 ? 2 : 1);
     long long n = sm_count() / units;
     if (n > kMaxDecaySegments) n = kMaxDecaySegments;
     if (n < 1) n = 1;
@@ -53,10 +53,10 @@ size_t segment_bytes(const DecayWalk &w)
     return w.nseg > 1 ? (size_t)w.B * w.nseg * w.Hv * kStateBytes : 0;
 }
 
-cudaError_t launch_walk(const DecayWalk &w, gdn_dtype dtype, cudaStream_t s)
+cudaError_t launch_walks(const gdn::DecayWalks &d, gdn_dtype dtype, cudaStream_t s)
 {
-    if (dtype == GDN_BF16 && gdn::chunk_tc_available()) return gdn::launch_decay_walk_tc(w, s);
-    return gdn::launch_decay_walk_simt(w, dtype, s);
+    if (dtype == GDN_BF16 && gdn::chunk_tc_available()) return gdn::launch_decay_walks_tc(d, s);
+    return gdn::launch_decay_walks_simt(d, dtype, s);
 }
 
 // T == 0: the state passes through.
@@ -83,7 +83,9 @@ gdn_status fwd_common(const void *q, const void *k, const void *v, const float *
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (T == 0) return pass_state(S_final, S0, B, Hv, s);
     if (!q || !k || !v || !decay || !o) return GDN_ERR_INVALID_ARG;
-    DecayWalk w{};
+    gdn::DecayWalks d{};
+    d.n = 1;
+    DecayWalk &w = d.w[0];
     w.x = q; w.y = k; w.z = v;
     w.hx = w.hy = Hqk; w.hz = Hv;
     w.o = o;
@@ -97,14 +99,14 @@ gdn_status fwd_common(const void *q, const void *k, const void *v, const float *
     w.nseg = 1;
     w.seg_chunks = (T + gdn::kChunk - 1) / gdn::kChunk;
     if (!cu) {
-        choose_segments(w, dtype);
+        choose_segments(w, 1, dtype);
         const size_t need = segment_bytes(w);
         if (need > 0) {
             if (!workspace || workspace_bytes < need || misaligned(workspace, 256)) return GDN_ERR_INVALID_ARG;
             w.seg = static_cast<float *>(workspace);
         }
     }
-    return launch_status(launch_walk(w, dtype, s));
+    return launch_status(launch_walks(d, dtype, s));
 }
 
 gdn_status check_token_op(int B, int Hqk, int Hv, int dk, int dv, gdn_dtype dtype, long long ctas_per_head)
@@ -175,7 +177,7 @@ size_t gdn_decay_fwd_workspace(int B, int T, int Hv, int dk, int dv, gdn_dtype d
     if (B <= 0 || T <= 0 || Hv <= 0 || dk != gdn::kHeadDim || dv != gdn::kHeadDim || !is_dtype(dtype)) return 0;
     DecayWalk w{};
     w.B = B; w.T = T; w.Hv = Hv;
-    choose_segments(w, dtype);
+    choose_segments(w, 1, dtype);
     return segment_bytes(w);
 }
 
@@ -215,8 +217,11 @@ size_t gdn_decay_bwd_workspace(int B, int T, int Hqk, int Hv, int dk, int dv, gd
     if (B <= 0 || T <= 0 || Hqk <= 0 || Hv <= 0 || Hv % Hqk || dk != gdn::kHeadDim || dv != gdn::kHeadDim ||
         !is_dtype(dtype))
         return 0;
+    DecayWalk w{};
+    w.B = B; w.T = T; w.Hv = Hv;
+    choose_segments(w, 3, dtype);
     const size_t rows = Hv == Hqk ? 0 : (size_t)B * T * Hv * gdn::kHeadDim * sizeof(float);
-    return gdn_decay_fwd_workspace(B, T, Hv, dk, dv, dtype) + rows;
+    return 3 * segment_bytes(w) + 2 * rows;
 }
 
 gdn_status gdn_decay_bwd(const void *q, const void *k, const void *v, const float *decay, const float *S0,
@@ -239,44 +244,49 @@ gdn_status gdn_decay_bwd(const void *q, const void *k, const void *v, const floa
     DecayWalk w{};
     w.decay = decay;
     w.B = B; w.T = T; w.Hv = Hv;
-    choose_segments(w, dtype);
+    choose_segments(w, 3, dtype);
     const size_t seg = segment_bytes(w);
     const bool shared = Hv != Hqk;
     const size_t need = gdn_decay_bwd_workspace(B, T, Hqk, Hv, dk_, dv_, dtype);
     if (need > 0 && (!workspace || workspace_bytes < need || misaligned(workspace, 256))) return GDN_ERR_INVALID_ARG;
-    w.seg = static_cast<float *>(workspace);
-    float *rows = shared ? reinterpret_cast<float *>(static_cast<char *>(workspace) + seg) : nullptr;
+    char *ws = static_cast<char *>(workspace);
+    // shared QK heads: one fp32 row per token and V head for each of dq and dk, summed afterwards
     const long long tokens = (long long)B * T;
-    cudaError_t err;
+    float *rows_q = shared ? reinterpret_cast<float *>(ws + 3 * seg) : nullptr;
+    float *rows_k = shared ? rows_q + (size_t)tokens * Hv * gdn::kHeadDim : nullptr;
 
+    gdn::DecayWalks d{};
+    d.n = 3;
+    for (int i = 0; i < 3; ++i) {
+        d.w[i] = w;
+        d.w[i].seg = seg ? reinterpret_cast<float *>(ws + i * seg) : nullptr;
+    }
     // dq_t = S_t dO_t: the walk of S^T (row = v's dimension)
-    DecayWalk wq = w;
+    DecayWalk &wq = d.w[0];
     wq.x = dO; wq.y = v; wq.z = k;
     wq.hx = wq.hy = Hv; wq.hz = Hqk;
     wq.init = S0; wq.init_trans = true; wq.init_decays = true;
-    wq.o = shared ? static_cast<void *>(rows) : dq;
+    wq.o = shared ? static_cast<void *>(rows_q) : dq;
     wq.o_f32 = shared;
-    err = launch_walk(wq, dtype, s);
-    if (err == cudaSuccess && shared) err = gdn::launch_head_sum(rows, dq, tokens, Hqk, Hv, dtype, s);
-    // dk_t = G_t v_t: backwards, the walk of G^T; before dv's, whose end state may replace dS_final
-    DecayWalk wk = w;
+    // dk_t = G_t v_t: backwards, the walk of G^T
+    DecayWalk &wk = d.w[1];
     wk.rev = true;
     wk.x = v; wk.y = dO; wk.z = q;
     wk.hx = wk.hy = Hv; wk.hz = Hqk;
     wk.init = dS_final; wk.init_trans = true;
-    wk.o = shared ? static_cast<void *>(rows) : dk;
+    wk.o = shared ? static_cast<void *>(rows_k) : dk;
     wk.o_f32 = shared;
-    if (err == cudaSuccess) err = launch_walk(wk, dtype, s);
-    if (err == cudaSuccess && shared) err = gdn::launch_head_sum(rows, dk, tokens, Hqk, Hv, dtype, s);
     // dv_t = G_t^T k_t, and dS0 = lambda G_0
-    DecayWalk wv = w;
+    DecayWalk &wv = d.w[2];
     wv.rev = true;
     wv.x = k; wv.y = q; wv.z = dO;
     wv.hx = wv.hy = Hqk; wv.hz = Hv;
     wv.init = dS_final;
     wv.fin = dS0;
     wv.o = dv;
-    if (err == cudaSuccess) err = launch_walk(wv, dtype, s);
+    cudaError_t err = launch_walks(d, dtype, s);
+    if (err == cudaSuccess && shared) err = gdn::launch_head_sum(rows_q, dq, tokens, Hqk, Hv, dtype, s);
+    if (err == cudaSuccess && shared) err = gdn::launch_head_sum(rows_k, dk, tokens, Hqk, Hv, dtype, s);
     return launch_status(err);
 }
 

@@ -149,6 +149,12 @@ __device__ __forceinline__ uint32_t split_pair(uint64_t &v) {
     return p;
 }
 
+// Kernel argument: the walks and their tensor maps (x, y, z, o).
+struct TcWalks {
+    CUtensorMap maps[kMaxWalks][4];
+    DecayWalks d;
+};
+
 // Rows of O from the accumulators one column (token) at a time: ragged chunks of packed
 // sequences, and fp32 partial rows (a warp writes 32 consecutive values of a row).
 template <typename OT>
@@ -166,10 +172,11 @@ __device__ __forceinline__ void store_rows(OT *dst, uint32_t t_lane, const float
 
 template <bool STATE_ONLY, int NZ, int NP>
 __global__ void __launch_bounds__(kDtThreads, 1)
-decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
-                const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_o,
-                const DecayWalk w)
+decay_tc_kernel(const __grid_constant__ TcWalks p)
 {
+    const DecayWalk &w = p.d.w[blockIdx.z];
+    const CUtensorMap &tm_x = p.maps[blockIdx.z][0], &tm_y = p.maps[blockIdx.z][1], &tm_z = p.maps[blockIdx.z][2],
+                      &tm_o = p.maps[blockIdx.z][3];
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + DOFF_BAR);
@@ -684,14 +691,14 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
 }
 
 template <bool STATE_ONLY, int NZ, int NP>
-cudaError_t launch_tc(const CUtensorMap &tx, const CUtensorMap &ty, const CUtensorMap &tz, const CUtensorMap &to,
-                      const DecayWalk &w, cudaStream_t stream)
+cudaError_t launch_tc(const TcWalks &p, cudaStream_t stream)
 {
     cudaError_t err = cudaFuncSetAttribute(decay_tc_kernel<STATE_ONLY, NZ, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            (int)D_SMEM);
     if (err != cudaSuccess) return err;
-    decay_tc_kernel<STATE_ONLY, NZ, NP><<<dim3((unsigned)w.Hv, (unsigned)(w.B * w.nseg)), kDtThreads, D_SMEM, stream>>>(
-        tx, ty, tz, to, w);
+    const DecayWalk &w = p.d.w[0];
+    decay_tc_kernel<STATE_ONLY, NZ, NP>
+        <<<dim3((unsigned)w.Hv, (unsigned)(w.B * w.nseg), (unsigned)p.d.n), kDtThreads, D_SMEM, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -706,22 +713,27 @@ cudaError_t decay_tc_take_error(unsigned *out)
     return err;
 }
 
-cudaError_t launch_decay_walk_tc(const DecayWalk &w, cudaStream_t stream)
+cudaError_t launch_decay_walks_tc(const DecayWalks &d, cudaStream_t stream)
 {
-    CUtensorMap tx, ty, tz, to;
-    const int rows_b = w.cu_seqlens ? 1 : w.B;   // batch rows of the token arrays
-    if (!make_map(&tx, w.x, rows_b, w.T, w.hx) || !make_map(&ty, w.y, rows_b, w.T, w.hy) ||
-        !make_map(&tz, w.z, rows_b, w.T, w.hz))
-        return cudaErrorInvalidValue;
-    if (w.o_f32) to = tx;                        // not used
-    else if (!make_map(&to, w.o, rows_b, w.T, w.Hv)) return cudaErrorInvalidValue;
-    const bool ends = w.fin != nullptr;          // an end state is wanted: its increments with all 24 bits
-    const bool one_chunk = w.T <= C;
+    TcWalks p;
+    p.d = d;
+    bool ends = false;                           // an end state is wanted: its increments with all 24 bits
+    for (int i = 0; i < d.n; ++i) {
+        const DecayWalk &w = d.w[i];
+        const int rows_b = w.cu_seqlens ? 1 : w.B;   // batch rows of the token arrays
+        if (!make_map(&p.maps[i][0], w.x, rows_b, w.T, w.hx) || !make_map(&p.maps[i][1], w.y, rows_b, w.T, w.hy) ||
+            !make_map(&p.maps[i][2], w.z, rows_b, w.T, w.hz))
+            return cudaErrorInvalidValue;
+        if (w.o_f32) p.maps[i][3] = p.maps[i][0];    // not used
+        else if (!make_map(&p.maps[i][3], w.o, rows_b, w.T, w.Hv)) return cudaErrorInvalidValue;
+        ends = ends || w.fin;
+    }
+    const DecayWalk &w = d.w[0];
     cudaError_t err = cudaSuccess;
-    if (w.nseg > 1) err = ends ? launch_tc<true, 3, 1>(tx, ty, tz, to, w, stream) : launch_tc<true, 2, 1>(tx, ty, tz, to, w, stream);
+    if (w.nseg > 1) err = ends ? launch_tc<true, 3, 1>(p, stream) : launch_tc<true, 2, 1>(p, stream);
     if (err != cudaSuccess) return err;
-    if (one_chunk) return ends ? launch_tc<false, 3, 2>(tx, ty, tz, to, w, stream) : launch_tc<false, 2, 2>(tx, ty, tz, to, w, stream);
-    return ends ? launch_tc<false, 3, 1>(tx, ty, tz, to, w, stream) : launch_tc<false, 2, 1>(tx, ty, tz, to, w, stream);
+    if (w.T <= C) return ends ? launch_tc<false, 3, 2>(p, stream) : launch_tc<false, 2, 2>(p, stream);
+    return ends ? launch_tc<false, 3, 1>(p, stream) : launch_tc<false, 2, 1>(p, stream);
 }
 
 }  // namespace gdn

@@ -102,8 +102,15 @@ struct DecayWalk {
     int nseg = 1, seg_chunks = 0;
     float *seg = nullptr;
 };
-cudaError_t launch_decay_walk_simt(const DecayWalk &w, gdn_dtype dtype, cudaStream_t stream);
-cudaError_t launch_decay_walk_tc(const DecayWalk &w, cudaStream_t stream);   // bf16 operands
+// Up to three walks of the same B, T, Hv and segments, side by side in one launch (two with
+// segments): a gradient's three walks fill the device where one would not.
+constexpr int kMaxWalks = 3;
+struct DecayWalks {
+    DecayWalk w[kMaxWalks];
+    int n;
+};
+cudaError_t launch_decay_walks_simt(const DecayWalks &d, gdn_dtype dtype, cudaStream_t stream);
+cudaError_t launch_decay_walks_tc(const DecayWalks &d, cudaStream_t stream);   // bf16 operands
 cudaError_t decay_tc_take_error(unsigned *out);
 // out [rows, Hqk, 128] = sum over each QK head's V heads of part [rows, Hv, 128]
 cudaError_t launch_head_sum(const float *part, void *out, long long rows, int Hqk, int Hv,
