@@ -226,7 +226,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
             const int p = w.rev ? L - 1 - t : t;                         // tokens since the chunk's start
             e = which < 2 ? max(L - p - bk, 0) : which < 4 ? p : -p;
             at = TAB_W + (i - 65);
-            if (which >= 2 && which < 4) e = fmin(e, kScaleFloor / loglam);   // loglam < 0 or 0: +-inf
+            if (strong && which >= 2 && which < 4) e = fmin(e, kScaleFloor / loglam);
         }
         tab[at] = (float)decay_pow(loglam, e);
     }

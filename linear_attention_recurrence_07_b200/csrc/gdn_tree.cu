@@ -350,7 +350,7 @@ commit_kernel(const T *__restrict__ k, const T *__restrict__ v, const float *__r
     __shared__ int path_len;
     __shared__ float sk[kGroup][kHeadDim];
     __shared__ float4 part[8][kGroup][32];
-    __shared__ float su[kGroup][kHeadDim];
+    __shared__ __align__(16) float su[kGroup][kHeadDim];     // read as float4
     __shared__ float skk[kGroup][kGroup];
     const unsigned bh = blockIdx.x;
     const int b = (int)(bh / (unsigned)Hv), h = (int)(bh - (unsigned)b * Hv), hq = h / (Hv / Hqk);

@@ -13,8 +13,12 @@ no code with the CUDA path.
   recurrence), for the backward pass.
 * ``chunk_backward``: the same gradients through the chunkwise WY form (the
   blocked algebra of a chunked backward kernel), required to agree with it.
+* ``decay``: the constant-decay linear attention and its gradients, draft trees
+  (delta and decay rule) and the 8-bit rows of the state cache, with majorants
+  from which the GPU tests' tolerances are computed.
 """
 from .oracle import decode_step, default_threads, forward  # noqa: F401
 from .chunk_form import chunk_forward  # noqa: F401
 from .backward import backward  # noqa: F401
 from .chunk_backward import chunk_backward  # noqa: F401
+from . import decay  # noqa: F401
