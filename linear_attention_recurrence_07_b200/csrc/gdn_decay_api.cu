@@ -30,13 +30,15 @@ int sm_count()
 
 constexpr size_t kStateBytes = (size_t)gdn::kHeadDim * gdn::kHeadDim * sizeof(float);
 constexpr int kMaxDecaySegments = 16;
-constexpr int kMinSegmentChunks = 4;
 
 // Segments of `walks` dense walks that run side by side: as many as fill the device with
-// one CTA (fp32: one head's four half-SM CTAs) per walk, head and segment, of at least four
-// chunks, because the launch that computes their start states reads y and z once more.
+// one CTA (fp32: one head's four half-SM CTAs) per walk, head and segment.  bf16: of at
+// least four chunks, because the launch that computes their start states reads y and z
+// once more and starts anew; the fp32 kernel is bound by its arithmetic, of which that
+// launch has a fifth, so one chunk is enough.
 void choose_segments(DecayWalk &w, int walks, gdn_dtype dtype)
 {
+    const int kMinSegmentChunks = dtype == GDN_F32 ? 1 : 4;
     const int nchunks = (w.T + gdn::kChunk - 1) / gdn::kChunk;
     const long long units = (long long)w.B * w.Hv * walks * (dtype == GDN_F32 ? 2 : 1);
     long long n = sm_count() / units;
@@ -137,7 +139,7 @@ gdn_status decode_common(const void *q, const void *k, const void *v, const floa
 // q, o null for the commit, accepted null for the verification; alpha and beta, or decay.
 gdn_status tree_common(gdn::TreeArgs a, bool commit, int dk, int dv, gdn_dtype dtype, void *stream)
 {
-    gdn_status st = check_token_op(a.B, a.Hqk, a.Hv, dk, dv, dtype, 1);
+    gdn_status st = check_token_op(a.B, a.Hqk, a.Hv, dk, dv, dtype, 4);
     if (st != GDN_OK) return st;
     if (a.n < 1 || a.n_slots < 0) return GDN_ERR_INVALID_ARG;
     if (a.n > gdn::kMaxTreeNodes) return GDN_ERR_UNSUPPORTED;

@@ -8,20 +8,28 @@
 // token" replaced by "ancestor":
 //   u_i = beta_i (v_i - root_i S^T k_i - sum_{j strict ancestor} Gam_ij (k_i . k_j) u_j)
 //   o_i = root_i S^T q_i + sum_{j on path(i)} Gam_ij (q_i . k_j) u_j
-// K S and Q S are warp MMAs on bf16 pieces of S (two pieces for bf16 inputs: 16 bits,
-// against the 8 of the output; three, all 24 bits, for fp32 inputs, whose rows are
+// K S and Q S are warp MMAs on bf16 pieces of S (two pieces for bf16 inputs: 14 to 16
+// bits, against the 8 of the output; three, all 24 bits, for fp32 inputs, whose rows are
 // cut in three as well).  A state is 64 KiB and n is at most 64 rows, so the products
 // are short next to the state's load, and M = 2n rows do not fill a 128-row tcgen05
 // tile: fragments come straight from the fp32 state in shared memory, which saves
-// the pass that would lay the pieces out for it.  The sums over ancestors run over
-// each node's path list, not over all earlier nodes: a bushy tree costs its depths.
+// the pass that would lay the pieces out for it.
+//
+// A CTA owns 64 columns of one head's state (two to five CTAs per SM, so that one's load
+// runs under another's sums).  The sums over ancestors go level by level: a node has one
+// ancestor on every level above it, so at level L every deeper node takes one term from
+// the row its ancestor has just finished, into registers, and the nodes of the next level
+// are finished.  A bushy tree costs its depth, not its size; non-ancestors are never read,
+// so that what is not finite stays below its node.
 #include "gdn_internal.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kTreeThreads = 256;
-constexpr int kLdS = kHeadDim + 4;       // floats per row of S, U, QS in shared memory
+constexpr int kTreeThreads = 128;
+constexpr int kTreeCols = 64;            // columns of the state per CTA
+constexpr int kTreeSlices = kHeadDim / kTreeCols;
+constexpr int kLdS = kTreeCols + 4;      // floats per row of S, U, QS in shared memory
 constexpr int kLdK = kHeadDim + 8;       // bf16 per row of K and Q
 constexpr float kLog2Clamp = -87.0f * 1.4426950408889634f;
 
@@ -50,6 +58,20 @@ __device__ __forceinline__ uint32_t take_piece(float &a, float &b) {
     return __byte_perm(ua, ub, 0x7632);
 }
 
+__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
+    const uint4 a = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        x[2 * e] = __uint_as_float(w[e] << 16);
+        x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+}
+
 template <typename T> struct TreeTypes;
 template <> struct TreeTypes<__nv_bfloat16> { static constexpr int kPlanes = 1, kPieces = 2; };
 template <> struct TreeTypes<float> { static constexpr int kPlanes = 3, kPieces = 3; };
@@ -62,13 +84,14 @@ struct TreeSmem {
         struct { float U[N][kLdS], QS[N][kLdS]; } r;     // after the products with S
     };
     __nv_bfloat16 kq[kPlanes][2][N][kLdK];               // k rows, q rows
-    float A[N][N + 4], P[N][N + 4];                      // by position in the node's path list
+    float A[N][N + 4], P[N][N + 4];                      // [node][level of its ancestor]
     double b[N];                                         // log2 of root_i
     unsigned long long mask[N];                          // path(i), bit j; 0 for padding
     float beta[N], root[N];
     int jump[N];
-    unsigned char list[N][N];                            // path(i) in node order
+    unsigned char list[N][N];                            // path(i) in node order: [node][level]
     unsigned char len[N];
+    int levels;
 };
 
 template <typename T, bool DELTA, int N>
@@ -82,20 +105,24 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
     constexpr int kPlanes = Sm::kPlanes, kPieces = TreeTypes<T>::kPieces, MT = N / 16;
     extern __shared__ __align__(16) unsigned char raw[];
     Sm &sm = *reinterpret_cast<Sm *>(raw);
-    const unsigned bh = blockIdx.x;
+    const unsigned bh = blockIdx.x / kTreeSlices;
+    const int c0 = (int)(blockIdx.x - bh * kTreeSlices) * kTreeCols;
     const int b = (int)(bh / (unsigned)Hv), h = (int)(bh - (unsigned)b * Hv), hq = h / (Hv / Hqk);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slot = slots ? slots[b] : b;
     if (slot < 0 || slot >= n_slots) return;
 
-    const float *S = pool + ((size_t)slot * Hv + h) * (kHeadDim * kHeadDim);
+    const float *S = pool + ((size_t)slot * Hv + h) * (kHeadDim * kHeadDim) + c0;
 #pragma unroll
-    for (int m = 0; m < 16; ++m)
-        cp_async16(&sm.S[warp + 8 * m][4 * lane], S + (warp + 8 * m) * kHeadDim + 4 * lane);
+    for (int m = 0; m < 16; ++m) {
+        const int row = (tid >> 4) + 8 * m, c = (tid & 15) * 4;
+        cp_async16(&sm.S[row][c], S + row * kHeadDim + c);
+    }
 
     if (warp == 0) {
         // ---- paths and gates by pointer jumping: after round r, mask and b cover 2^r steps.
         //      jump: next node up, -1 past the root, -2 padding.
+        constexpr int kPer = (N + 31) / 32;
         for (int i = lane; i < N; i += 32) {
             int p = i < n ? parents[(size_t)b * n + i] : -2;
             if (p < -1 || p >= i) p = -2;
@@ -112,7 +139,6 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
             sm.beta[i] = be;
         }
         __syncwarp();
-        constexpr int kPer = (N + 31) / 32;
 #pragma unroll 1
         for (int step = 1; step < N; step <<= 1) {
             unsigned long long m2[kPer];
@@ -136,6 +162,7 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
             }
             __syncwarp();
         }
+        int most = 0;
         for (int i = lane; i < N; i += 32) {
             unsigned long long m = sm.jump[i] == -1 ? sm.mask[i] : 0ull;   // -2 reached: padding
             sm.mask[i] = m;
@@ -146,7 +173,10 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
                 m &= m - 1;
             }
             sm.len[i] = (unsigned char)c;
+            most = max(most, c);
         }
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) sm.levels = most;
     } else {
         // ---- k and q rows as bf16 planes; rows past n are zeros
         for (int i = tid - 32; i < 2 * N * (kHeadDim / 4); i += kTreeThreads - 32) {
@@ -171,14 +201,15 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
     cp_async_wait_all();
     __syncthreads();
 
-    const int role = warp >> 2, cb = warp & 3;           // role 0: k rows, 1: q rows
+    const int role = warp >> 1, cb = warp & 1;           // role 0: k rows, 1: q rows
     const int g = lane >> 2, t = lane & 3;
     const int lrow = lane & 15, lcol = (lane >> 4) * 8;  // ldmatrix addresses
-    // ---- grams with k -> coefficients of the path sums
+    // ---- grams with k -> coefficients of the path sums, j <= i only
     if (DELTA || role == 1) {
-        for (int nt = cb; nt < N / 8; nt += 4) {
 #pragma unroll 1
-            for (int mt = nt / 2; mt < MT; ++mt) {       // j <= i only
+        for (int nt = cb; nt < N / 8; nt += 2) {
+#pragma unroll 1
+            for (int mt = nt / 2; mt < MT; ++mt) {
                 float acc[4] = {};
 #pragma unroll
                 for (int pa = 0; pa < kPlanes; ++pa)
@@ -206,7 +237,9 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
             }
         }
     }
-    // ---- rows times S: this warp's 32 columns, thread (g, t) the columns 4g .. 4g+3 of B
+    // ---- rows times S: this warp's 32 columns, thread (g, t) the columns 4g .. 4g+3 of B.
+    //      fp32 inputs: the tensor core truncates as it accumulates, so each 16 columns of K are
+    //      summed from zero, small pieces first, and added in fp32.
     float acc[MT][4][4];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -230,18 +263,31 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
                 bp[p][3][0] = take_piece(s0.w, s1.w); bp[p][3][1] = take_piece(s2.w, s3.w);
             }
 #pragma unroll
-            for (int pa = 0; pa < kPlanes; ++pa)
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
+            for (int mt = 0; mt < MT; ++mt) {
+                if constexpr (kPlanes == 1) {
                     uint32_t a[4];
-                    ldmatrix_x4(a, &sm.kq[pa][role][mt * 16 + lrow][ks * 16 + lcol]);
+                    ldmatrix_x4(a, &sm.kq[0][role][mt * 16 + lrow][ks * 16 + lcol]);
 #pragma unroll
-                    for (int p = 0; p < kPieces; ++p)
-                        if (pa + p < kPieces) {
+                    for (int p = kPieces - 1; p >= 0; --p)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) mma16816(acc[mt][j], a, bp[p][j][0], bp[p][j][1]);
+                        for (int j = 0; j < 4; ++j) mma16816(acc[mt][j], a, bp[p][j][0], bp[p][j][1]);
+                } else {
+                    float d[4][4] = {};
+#pragma unroll
+                    for (int sum = kPieces - 1; sum >= 0; --sum)         // orders of size, small first
+#pragma unroll
+                        for (int pa = sum; pa >= 0; --pa) {
+                            uint32_t a[4];
+                            ldmatrix_x4(a, &sm.kq[pa][role][mt * 16 + lrow][ks * 16 + lcol]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) mma16816(d[j], a, bp[sum - pa][j][0], bp[sum - pa][j][1]);
                         }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[mt][j][e] += d[j][e];
                 }
+            }
         }
     }
     __syncthreads();                                     // S read; A and P written
@@ -259,55 +305,61 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
             }
             if (role == 0) {
                 const bool on = i < n && sm.mask[i] != 0;
-                const T *vr = v + (((size_t)b * n + i) * Hv + h) * kHeadDim + c;
                 const float f = sm.root[i], be = sm.beta[i];
+                float vv[8] = {};
+                if (on) load8(v + (((size_t)b * n + i) * Hv + h) * kHeadDim + c0 + c, vv);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float vv = on ? to_f32(vr[j]) : 0.f;
-                    x[j] = DELTA ? be * (vv - f * x[j]) : vv;
-                }
+                for (int j = 0; j < 8; ++j) x[j] = DELTA ? be * (vv[j] - f * x[j]) : vv[j];
             }
             float *dst = role == 0 ? &sm.r.U[i][c] : &sm.r.QS[i][c];
             *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
             *reinterpret_cast<float4 *>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
         }
     __syncthreads();
-    // ---- u_i down the tree, one column per thread
-    if (DELTA) {
-        if (tid < kHeadDim) {
-#pragma unroll 1
-            for (int i = 1; i < n; ++i) {
-                const int strict = (int)sm.len[i] - 1;
-                if (strict <= 0) continue;
-                float s = 0.f;
-                for (int d = 0; d < strict; ++d) s = fmaf(sm.A[i][d], sm.r.U[sm.list[i][d]][tid], s);
-                sm.r.U[i][tid] -= s;
-            }
-        }
-        __syncthreads();
+    // ---- levels: warp w owns nodes w, w + 4, ..., lane l columns 2l, 2l + 1
+    constexpr int kOwn = N / 4;
+    float2 u[kOwn], out[kOwn];
+    int len[kOwn];
+#pragma unroll
+    for (int x = 0; x < kOwn; ++x) {
+        const int i = warp + 4 * x;
+        len[x] = sm.len[i];
+        const float2 r = *reinterpret_cast<const float2 *>(&sm.r.QS[i][2 * lane]);
+        out[x] = make_float2(sm.root[i] * r.x, sm.root[i] * r.y);
+        u[x] = *reinterpret_cast<const float2 *>(&sm.r.U[i][2 * lane]);
     }
-    // ---- outputs: two columns per thread, every fourth node
-    {
-        const int c = 2 * (tid & 63);
+    const int levels = sm.levels;
 #pragma unroll 1
-        for (int i = tid >> 6; i < n; i += 4) {
-            const int len = sm.len[i];
-            if (len == 0) continue;                      // padding: the row stays as it was
-            const float2 r = *reinterpret_cast<const float2 *>(&sm.r.QS[i][c]);
-            float s0 = sm.root[i] * r.x, s1 = sm.root[i] * r.y;
-            for (int d = 0; d < len; ++d) {
-                const float p = sm.P[i][d];
-                const float2 u = *reinterpret_cast<const float2 *>(&sm.r.U[sm.list[i][d]][c]);
-                s0 = fmaf(p, u.x, s0);
-                s1 = fmaf(p, u.y, s1);
-            }
-            T *dst = o + (((size_t)b * n + i) * Hv + h) * kHeadDim + c;
-            if constexpr (kPlanes == 1) {
-                *reinterpret_cast<__nv_bfloat162 *>(dst) = __floats2bfloat162_rn(s0, s1);
-            } else {
-                *reinterpret_cast<float2 *>(dst) = make_float2(s0, s1);
+    for (int L = 0; L < levels; ++L) {
+        if (DELTA && L > 0) {                            // the nodes of this level are finished
+#pragma unroll
+            for (int x = 0; x < kOwn; ++x)
+                if (len[x] == L + 1) *reinterpret_cast<float2 *>(&sm.r.U[warp + 4 * x][2 * lane]) = u[x];
+            __syncthreads();
+        }
+#pragma unroll
+        for (int x = 0; x < kOwn; ++x) {
+            if (len[x] > L) {
+                const int i = warp + 4 * x;
+                const float2 w = *reinterpret_cast<const float2 *>(&sm.r.U[sm.list[i][L]][2 * lane]);
+                const float p = sm.P[i][L];
+                out[x].x = fmaf(p, w.x, out[x].x);
+                out[x].y = fmaf(p, w.y, out[x].y);
+                if (DELTA && len[x] > L + 1) {
+                    const float a = sm.A[i][L];
+                    u[x].x = fmaf(-a, w.x, u[x].x);
+                    u[x].y = fmaf(-a, w.y, u[x].y);
+                }
             }
         }
+    }
+#pragma unroll
+    for (int x = 0; x < kOwn; ++x) {
+        const int i = warp + 4 * x;
+        if (len[x] == 0) continue;                       // padding: the row stays as it was
+        T *dst = o + (((size_t)b * n + i) * Hv + h) * kHeadDim + c0 + 2 * lane;
+        if constexpr (kPlanes == 1) *reinterpret_cast<__nv_bfloat162 *>(dst) = __floats2bfloat162_rn(out[x].x, out[x].y);
+        else *reinterpret_cast<float2 *>(dst) = out[x];
     }
 }
 
@@ -317,7 +369,7 @@ cudaError_t launch_tree_n(const TreeArgs &a, cudaStream_t stream)
     const int smem = (int)sizeof(TreeSmem<T, N>);
     cudaError_t err = cudaFuncSetAttribute(tree_kernel<T, DELTA, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
-    tree_kernel<T, DELTA, N><<<(unsigned)((size_t)a.B * a.Hv), kTreeThreads, smem, stream>>>(
+    tree_kernel<T, DELTA, N><<<(unsigned)((size_t)a.B * a.Hv * kTreeSlices), kTreeThreads, smem, stream>>>(
         (const T *)a.q, (const T *)a.k, (const T *)a.v, a.alpha, a.beta, a.decay, a.parents, a.pool, a.slots, (T *)a.o,
         a.n, a.n_slots, a.Hqk, a.Hv);
     return cudaGetLastError();
@@ -328,19 +380,25 @@ cudaError_t launch_tree_typed(const TreeArgs &a, cudaStream_t stream)
 {
     if (a.n <= 16) return launch_tree_n<T, DELTA, 16>(a, stream);
     if (a.n <= 32) return launch_tree_n<T, DELTA, 32>(a, stream);
+    if (a.n <= 48) return launch_tree_n<T, DELTA, 48>(a, stream);
     return launch_tree_n<T, DELTA, 64>(a, stream);
 }
 
 // ------------------------------------------------------------------ commit
-// One CTA per (sequence, V head): the state in registers as in the decode kernel
-// (warp w rows w, w + 8, ..., lane l columns 4l .. 4l + 3), read and written once.  The
-// path's nodes are taken four at a time: their products with the state share one
-// pass over the registers and one reduction, the delta rule inside the four is a
-// 4 x 4 substitution per column, and one pass applies the four writes.
+// One CTA owns 32 columns of one state (a row's piece is one 128-byte line), in registers,
+// read and written once: thread (row group, lane of 8) holds eight float4, as in the decay
+// decode.  The path's nodes are taken four at a time: their products with the state share
+// one pass over the registers and one reduction, the delta rule inside the four is a 4 x 4
+// substitution per column, and one pass applies the four writes.
 constexpr int kGroup = 4;
+constexpr int kComCols = 32;
+constexpr int kComSlices = kHeadDim / kComCols;
+constexpr int kComThreads = 128;
+constexpr int kComGroups = kComThreads / (kComCols / 4);     // 16 row groups
+constexpr int kComRows = kHeadDim / kComGroups;              // 8
 
 template <typename T, bool DELTA>
-__global__ void __launch_bounds__(kTreeThreads, 2)
+__global__ void __launch_bounds__(kComThreads)
 commit_kernel(const T *__restrict__ k, const T *__restrict__ v, const float *__restrict__ alpha,
               const float *__restrict__ beta, const float *__restrict__ decay, const int *__restrict__ parents,
               const int *__restrict__ accepted, float *pool, const int *__restrict__ slots, int n, int n_slots,
@@ -349,19 +407,20 @@ commit_kernel(const T *__restrict__ k, const T *__restrict__ v, const float *__r
     __shared__ int path[kMaxTreeNodes], par[kMaxTreeNodes];
     __shared__ int path_len;
     __shared__ float sk[kGroup][kHeadDim];
-    __shared__ float4 part[8][kGroup][32];
-    __shared__ __align__(16) float su[kGroup][kHeadDim];     // read as float4
+    __shared__ float4 part[kComThreads / 32][kGroup][kComCols / 4];
+    __shared__ __align__(16) float su[kGroup][kComCols];     // read as float4
     __shared__ float skk[kGroup][kGroup];
-    const unsigned bh = blockIdx.x;
+    const unsigned bh = blockIdx.x / kComSlices;
+    const int c0 = (int)(blockIdx.x - bh * kComSlices) * kComCols;
     const int b = (int)(bh / (unsigned)Hv), h = (int)(bh - (unsigned)b * Hv), hq = h / (Hv / Hqk);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l8 = tid & 7, rg = tid >> 3;
     const int slot = slots ? slots[b] : b, leaf = accepted[b];
     if (slot < 0 || slot >= n_slots || leaf < 0 || leaf >= n) return;
     if (tid < n) par[tid] = parents[(size_t)b * n + tid];
-    float4 *S4 = reinterpret_cast<float4 *>(pool + ((size_t)slot * Hv + h) * (kHeadDim * kHeadDim));
-    float4 s[16];
+    float4 *S4 = reinterpret_cast<float4 *>(pool + ((size_t)slot * Hv + h) * (kHeadDim * kHeadDim) + c0) + l8;
+    float4 s[kComRows];
 #pragma unroll
-    for (int m = 0; m < 16; ++m) s[m] = __ldcs(S4 + (warp + 8 * m) * 32 + lane);
+    for (int m = 0; m < kComRows; ++m) s[m] = __ldcs(S4 + (rg + kComGroups * m) * (kHeadDim / 4));
     __syncthreads();
     if (tid == 0) {
         int len = 0, i = leaf;
@@ -378,12 +437,9 @@ commit_kernel(const T *__restrict__ k, const T *__restrict__ v, const float *__r
     for (int d0 = 0; d0 < len; d0 += kGroup) {
         const int m = min(kGroup, len - d0);
         // rows of the group (root first); missing nodes get k = 0 and no write
-        for (int i = tid; i < kGroup * kHeadDim; i += kTreeThreads) {
-            const int j = i / kHeadDim, d = i % kHeadDim;
-            float x = 0.f;
-            if (j < m) x = to_f32(k[(((size_t)b * n + path[len - 1 - d0 - j]) * Hqk + hq) * kHeadDim + d]);
-            sk[j][d] = x;
-        }
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j)
+            sk[j][tid] = j < m ? to_f32(k[(((size_t)b * n + path[len - 1 - d0 - j]) * Hqk + hq) * kHeadDim + tid]) : 0.f;
         float a[kGroup];                                 // gates; 1 for missing nodes
 #pragma unroll
         for (int j = 0; j < kGroup; ++j) {
@@ -391,10 +447,20 @@ commit_kernel(const T *__restrict__ k, const T *__restrict__ v, const float *__r
             if (j < m)
                 a[j] = fmaxf(DELTA ? alpha[((size_t)b * n + path[len - 1 - d0 - j]) * Hv + h] : decay[h], 1.6458114e-38f);
         }
+        // what the substitution of this thread's column needs, on its way during the products
+        float vv[kGroup], be[kGroup];
+        if (tid < kComCols) {
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) {
+                const size_t at = ((size_t)b * n + path[len - 1 - d0 - min(j, m - 1)]) * Hv + h;
+                vv[j] = to_f32(v[at * kHeadDim + c0 + tid]);
+                be[j] = DELTA ? beta[at] : 1.f;
+            }
+        }
         __syncthreads();
         if (DELTA) {
-            if (warp < 6) {                              // k_i . k_j, i > j, one pair per warp
-                const int i = warp < 1 ? 1 : warp < 3 ? 2 : 3, j = warp - (i * (i - 1)) / 2;
+            for (int pr = warp; pr < 6; pr += kComThreads / 32) {        // k_i . k_j, i > j
+                const int i = pr < 1 ? 1 : pr < 3 ? 2 : 3, j = pr - (i * (i - 1)) / 2;
                 float x = 0.f;
 #pragma unroll
                 for (int d = 0; d < 4; ++d) x = fmaf(sk[i][lane + 32 * d], sk[j][lane + 32 * d], x);
@@ -406,33 +472,41 @@ commit_kernel(const T *__restrict__ k, const T *__restrict__ v, const float *__r
 #pragma unroll
             for (int j = 0; j < kGroup; ++j) pp[j] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
+            for (int r = 0; r < kComRows; ++r) {
 #pragma unroll
                 for (int j = 0; j < kGroup; ++j) {
-                    const float ki = sk[j][warp + 8 * r];
+                    const float ki = sk[j][rg + kComGroups * r];
                     pp[j].x = fmaf(s[r].x, ki, pp[j].x); pp[j].y = fmaf(s[r].y, ki, pp[j].y);
                     pp[j].z = fmaf(s[r].z, ki, pp[j].z); pp[j].w = fmaf(s[r].w, ki, pp[j].w);
                 }
             }
 #pragma unroll
-            for (int j = 0; j < kGroup; ++j) part[warp][j][lane] = pp[j];
+            for (int j = 0; j < kGroup; ++j) {
+#pragma unroll
+                for (int off = 8; off < 32; off <<= 1) {                 // the four row groups of a warp
+                    pp[j].x += __shfl_xor_sync(0xffffffffu, pp[j].x, off);
+                    pp[j].y += __shfl_xor_sync(0xffffffffu, pp[j].y, off);
+                    pp[j].z += __shfl_xor_sync(0xffffffffu, pp[j].z, off);
+                    pp[j].w += __shfl_xor_sync(0xffffffffu, pp[j].w, off);
+                }
+                if (lane < 8) part[warp][j][l8] = pp[j];
+            }
             __syncthreads();
         }
-        if (tid < kHeadDim) {
+        if (tid < kComCols) {
             float u[kGroup];
 #pragma unroll
             for (int j = 0; j < kGroup; ++j) {
                 u[j] = 0.f;
                 if (j < m) {
-                    const size_t at = ((size_t)b * n + path[len - 1 - d0 - j]) * Hv + h;
-                    u[j] = to_f32(v[at * kHeadDim + tid]);
+                    u[j] = vv[j];
                     if (DELTA) {
                         float p = 0.f;
 #pragma unroll
-                        for (int w = 0; w < 8; ++w) p += reinterpret_cast<const float *>(&part[w][j][0])[tid];
+                        for (int w = 0; w < kComThreads / 32; ++w) p += reinterpret_cast<const float *>(&part[w][j][0])[tid];
 #pragma unroll
                         for (int i = 0; i < j; ++i) p = fmaf(a[i], p, skk[j][i] * u[i]);   // S after node i, times k_j
-                        u[j] = beta[at] * (u[j] - a[j] * p);
+                        u[j] = be[j] * (u[j] - a[j] * p);
                     }
                 }
                 su[j][tid] = u[j];
@@ -441,12 +515,12 @@ commit_kernel(const T *__restrict__ k, const T *__restrict__ v, const float *__r
         __syncthreads();
         float4 u4[kGroup];
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) u4[j] = *reinterpret_cast<const float4 *>(&su[j][4 * lane]);
+        for (int j = 0; j < kGroup; ++j) u4[j] = *reinterpret_cast<const float4 *>(&su[j][4 * l8]);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
+        for (int r = 0; r < kComRows; ++r) {
 #pragma unroll
             for (int j = 0; j < kGroup; ++j) {
-                const float ki = sk[j][warp + 8 * r];
+                const float ki = sk[j][rg + kComGroups * r];
                 s[r].x = fmaf(a[j], s[r].x, ki * u4[j].x); s[r].y = fmaf(a[j], s[r].y, ki * u4[j].y);
                 s[r].z = fmaf(a[j], s[r].z, ki * u4[j].z); s[r].w = fmaf(a[j], s[r].w, ki * u4[j].w);
             }
@@ -454,13 +528,13 @@ commit_kernel(const T *__restrict__ k, const T *__restrict__ v, const float *__r
         __syncthreads();                                 // sk, su, part are written again
     }
 #pragma unroll
-    for (int m = 0; m < 16; ++m) __stcs(S4 + (warp + 8 * m) * 32 + lane, s[m]);
+    for (int m = 0; m < kComRows; ++m) __stcs(S4 + (rg + kComGroups * m) * (kHeadDim / 4), s[m]);
 }
 
 template <typename T, bool DELTA>
 cudaError_t launch_commit_typed(const TreeArgs &a, cudaStream_t stream)
 {
-    commit_kernel<T, DELTA><<<(unsigned)((size_t)a.B * a.Hv), kTreeThreads, 0, stream>>>(
+    commit_kernel<T, DELTA><<<(unsigned)((size_t)a.B * a.Hv * kComSlices), kComThreads, 0, stream>>>(
         (const T *)a.k, (const T *)a.v, a.alpha, a.beta, a.decay, a.parents, a.accepted, a.pool_out, a.slots, a.n,
         a.n_slots, a.Hqk, a.Hv);
     return cudaGetLastError();
