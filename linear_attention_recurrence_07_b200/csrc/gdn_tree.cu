@@ -86,6 +86,7 @@ struct TreeSmem {
     __nv_bfloat16 kq[kPlanes][2][N][kLdK];               // k rows, q rows
     float A[N][N + 4], P[N][N + 4];                      // [node][level of its ancestor]
     double b[N];                                         // log2 of root_i
+    float2 b2[N];                                        // the same as a sum of two floats
     unsigned long long mask[N];                          // path(i), bit j; 0 for padding
     float beta[N], root[N];
     int jump[N];
@@ -119,24 +120,41 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
         cp_async16(&sm.S[row][c], S + row * kHeadDim + c);
     }
 
+    // ---- k and q rows as bf16 planes; rows past n are zeros
+    if constexpr (kPlanes == 1) {
+        for (int i = tid; i < 2 * N * 16; i += kTreeThreads) {
+            const int which = i / (N * 16), r = (i / 16) % N, d = (i % 16) * 8;
+            void *dst = &sm.kq[0][which][r][d];
+            if (r < n) cp_async16(dst, (which ? q : k) + (((size_t)b * n + r) * Hqk + hq) * kHeadDim + d);
+            else *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
     if (warp == 0) {
         // ---- paths and gates by pointer jumping: after round r, mask and b cover 2^r steps.
         //      jump: next node up, -1 past the root, -2 padding.
         constexpr int kPer = (N + 31) / 32;
-        for (int i = lane; i < N; i += 32) {
-            int p = i < n ? parents[(size_t)b * n + i] : -2;
-            if (p < -1 || p >= i) p = -2;
-            sm.jump[i] = p;
-            sm.mask[i] = 1ull << i;
-            double g = 0.0;
-            float be = 0.f;
+        int p[kPer];
+        float ga[kPer], be[kPer];
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+            const int i = lane + 32 * x;
+            p[x] = -2; ga[x] = 1.f; be[x] = 0.f;
             if (i < n) {
                 const size_t at = ((size_t)b * n + i) * Hv + h;
-                g = (double)fmaxf(log2f(DELTA ? alpha[at] : decay[h]), kLog2Clamp);
-                if (DELTA) be = beta[at];
+                p[x] = parents[(size_t)b * n + i];
+                ga[x] = DELTA ? alpha[at] : decay[h];
+                if (DELTA) be[x] = beta[at];
             }
-            sm.b[i] = g;
-            sm.beta[i] = be;
+        }
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+            const int i = lane + 32 * x;
+            if (i < N) {
+                sm.jump[i] = p[x] < -1 || p[x] >= i ? -2 : p[x];
+                sm.mask[i] = 1ull << i;
+                sm.b[i] = (double)fmaxf(log2f(ga[x]), kLog2Clamp);
+                sm.beta[i] = be[x];
+            }
         }
         __syncwarp();
 #pragma unroll 1
@@ -160,36 +178,34 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
                 const int i = lane + 32 * x;
                 if (i < N) { sm.mask[i] |= m2[x]; sm.b[i] += b2[x]; sm.jump[i] = j2[x]; }
             }
+            if (!__any_sync(0xffffffffu, j2[0] >= 0 || j2[kPer - 1] >= 0)) step = N;    // every path has ended
             __syncwarp();
         }
         int most = 0;
-        for (int i = lane; i < N; i += 32) {
-            unsigned long long m = sm.jump[i] == -1 ? sm.mask[i] : 0ull;   // -2 reached: padding
-            sm.mask[i] = m;
-            sm.root[i] = exp2f((float)sm.b[i]);
-            int c = 0;
-            while (m) {
-                sm.list[i][c++] = (unsigned char)(__ffsll((long long)m) - 1);
-                m &= m - 1;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+            const int i = lane + 32 * x;
+            if (i < N) {
+                const unsigned long long m = sm.jump[i] == -1 ? sm.mask[i] : 0ull;   // -2 reached: padding
+                const double bi = sm.b[i];
+                const float hi = (float)bi;
+                sm.mask[i] = m;
+                sm.b2[i] = make_float2(hi, (float)(bi - (double)hi));
+                sm.root[i] = exp2f(hi);
+                const int c = __popcll(m);
+                sm.len[i] = (unsigned char)c;
+                most = max(most, c);
             }
-            sm.len[i] = (unsigned char)c;
-            most = max(most, c);
         }
         most = __reduce_max_sync(0xffffffffu, most);
         if (lane == 0) sm.levels = most;
     } else {
-        // ---- k and q rows as bf16 planes; rows past n are zeros
-        for (int i = tid - 32; i < 2 * N * (kHeadDim / 4); i += kTreeThreads - 32) {
-            const int which = i / (N * (kHeadDim / 4)), r = (i / (kHeadDim / 4)) % N, d = (i % (kHeadDim / 4)) * 4;
-            const T *src = which ? q : k;
-            const size_t at = (((size_t)b * n + r) * Hqk + hq) * kHeadDim + d;
-            if constexpr (kPlanes == 1) {
-                uint2 u = make_uint2(0u, 0u);
-                if (r < n) u = *reinterpret_cast<const uint2 *>(src + at);
-                *reinterpret_cast<uint2 *>(&sm.kq[0][which][r][d]) = u;
-            } else {
+        for (int i = tid - 32; i < N * N / 4; i += kTreeThreads - 32) reinterpret_cast<uint32_t *>(&sm.list[0][0])[i] = 0u;
+        if constexpr (kPlanes > 1) {
+            for (int i = tid - 32; i < 2 * N * (kHeadDim / 4); i += kTreeThreads - 32) {
+                const int which = i / (N * (kHeadDim / 4)), r = (i / (kHeadDim / 4)) % N, d = (i % (kHeadDim / 4)) * 4;
                 float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (r < n) f = *reinterpret_cast<const float4 *>(src + at);
+                if (r < n) f = *reinterpret_cast<const float4 *>((which ? q : k) + (((size_t)b * n + r) * Hqk + hq) * kHeadDim + d);
 #pragma unroll
                 for (int pl = 0; pl < kPlanes; ++pl) {
                     const uint32_t lo = take_piece(f.x, f.y), hi = take_piece(f.z, f.w);
@@ -208,30 +224,42 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
     if (DELTA || role == 1) {
 #pragma unroll 1
         for (int nt = cb; nt < N / 8; nt += 2) {
+            uint32_t kb[kPlanes][kHeadDim / 16][2];          // this tile's 8 rows of k
+#pragma unroll
+            for (int pb = 0; pb < kPlanes; ++pb)
+#pragma unroll
+                for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+                    const __nv_bfloat16 *kr = &sm.kq[pb][0][nt * 8 + g][ks * 16 + 2 * t];
+                    kb[pb][ks][0] = *reinterpret_cast<const uint32_t *>(kr);
+                    kb[pb][ks][1] = *reinterpret_cast<const uint32_t *>(kr + 8);
+                }
 #pragma unroll 1
             for (int mt = nt / 2; mt < MT; ++mt) {
-                float acc[4] = {};
+                float acc[2][4] = {};                        // even and odd ks: half the chain
 #pragma unroll
-                for (int pa = 0; pa < kPlanes; ++pa)
+                for (int sum = kPlanes - 1; sum >= 0; --sum)
 #pragma unroll
-                    for (int pb = 0; pa + pb < kPlanes; ++pb)
+                    for (int pa = sum; pa >= 0; --pa)
 #pragma unroll
                         for (int ks = 0; ks < kHeadDim / 16; ++ks) {
                             uint32_t a[4];
                             ldmatrix_x4(a, &sm.kq[pa][role][mt * 16 + lrow][ks * 16 + lcol]);
-                            const __nv_bfloat16 *kr = &sm.kq[pb][0][nt * 8 + g][ks * 16 + 2 * t];
-                            mma16816(acc, a, *reinterpret_cast<const uint32_t *>(kr),
-                                     *reinterpret_cast<const uint32_t *>(kr + 8));
+                            mma16816(acc[ks & 1], a, kb[sum - pa][ks][0], kb[sum - pa][ks][1]);
                         }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int i = mt * 16 + g + (e >> 1) * 8, j = nt * 8 + 2 * t + (e & 1);
                     const unsigned long long m = sm.mask[i];
-                    if (((m >> j) & 1ull) && (role == 1 || j < i)) {
-                        const int at = __popcll(m & ((1ull << j) - 1ull));
-                        const float x = exp2f((float)(sm.b[i] - sm.b[j])) * acc[e];
-                        if (role == 0) sm.A[i][at] = sm.beta[i] * x;
-                        else sm.P[i][at] = x;
+                    const float2 bi = sm.b2[i], bj = sm.b2[j];
+                    const float x = exp2f((bi.x - bj.x) + (bi.y - bj.y)) * (acc[0][e] + acc[1][e]);
+                    const int at = __popcll(m & ((1ull << j) - 1ull));
+                    if ((m >> j) & 1ull) {
+                        if (role == 0) {
+                            if (j < i) sm.A[i][at] = sm.beta[i] * x;
+                        } else {
+                            sm.P[i][at] = x;
+                            sm.list[i][at] = (unsigned char)j;
+                        }
                     }
                 }
             }
@@ -337,19 +365,20 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
                 if (len[x] == L + 1) *reinterpret_cast<float2 *>(&sm.r.U[warp + 4 * x][2 * lane]) = u[x];
             __syncthreads();
         }
+        // selected, not branched over, so that all rows are on their way at once
 #pragma unroll
         for (int x = 0; x < kOwn; ++x) {
-            if (len[x] > L) {
-                const int i = warp + 4 * x;
-                const float2 w = *reinterpret_cast<const float2 *>(&sm.r.U[sm.list[i][L]][2 * lane]);
-                const float p = sm.P[i][L];
-                out[x].x = fmaf(p, w.x, out[x].x);
-                out[x].y = fmaf(p, w.y, out[x].y);
-                if (DELTA && len[x] > L + 1) {
-                    const float a = sm.A[i][L];
-                    u[x].x = fmaf(-a, w.x, u[x].x);
-                    u[x].y = fmaf(-a, w.y, u[x].y);
-                }
+            const int i = warp + 4 * x;
+            const float2 w = *reinterpret_cast<const float2 *>(&sm.r.U[sm.list[i][L]][2 * lane]);
+            const float p = sm.P[i][L];
+            const bool on = len[x] > L;
+            out[x].x = on ? fmaf(p, w.x, out[x].x) : out[x].x;
+            out[x].y = on ? fmaf(p, w.y, out[x].y) : out[x].y;
+            if (DELTA) {
+                const float a = sm.A[i][L];
+                const bool deeper = len[x] > L + 1;
+                u[x].x = deeper ? fmaf(-a, w.x, u[x].x) : u[x].x;
+                u[x].y = deeper ? fmaf(-a, w.y, u[x].y) : u[x].y;
             }
         }
     }
