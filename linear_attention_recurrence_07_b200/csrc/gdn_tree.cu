@@ -22,9 +22,12 @@
 // are finished.  A bushy tree costs its depth, not its size; non-ancestors are never read,
 // so that what is not finite stays below its node.
 #include "gdn_internal.cuh"
+#include "sm100.cuh"
 
 namespace gdn {
 namespace {
+
+using namespace sm100;
 
 constexpr int kTreeThreads = 128;
 constexpr int kTreeCols = 64;            // columns of the state per CTA
@@ -427,7 +430,7 @@ constexpr int kComGroups = kComThreads / (kComCols / 4);     // 16 row groups
 constexpr int kComRows = kHeadDim / kComGroups;              // 8
 
 template <typename T, bool DELTA>
-__global__ void __launch_bounds__(kComThreads)
+__global__ void __launch_bounds__(kComThreads, 8)
 commit_kernel(const T *__restrict__ k, const T *__restrict__ v, const float *__restrict__ alpha,
               const float *__restrict__ beta, const float *__restrict__ decay, const int *__restrict__ parents,
               const int *__restrict__ accepted, float *pool, const int *__restrict__ slots, int n, int n_slots,
@@ -443,13 +446,18 @@ commit_kernel(const T *__restrict__ k, const T *__restrict__ v, const float *__r
     const int c0 = (int)(blockIdx.x - bh * kComSlices) * kComCols;
     const int b = (int)(bh / (unsigned)Hv), h = (int)(bh - (unsigned)b * Hv), hq = h / (Hv / Hqk);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l8 = tid & 7, rg = tid >> 3;
+    const int my_parent = tid < n ? parents[(size_t)b * n + tid] : 0;
     const int slot = slots ? slots[b] : b, leaf = accepted[b];
     if (slot < 0 || slot >= n_slots || leaf < 0 || leaf >= n) return;
-    if (tid < n) par[tid] = parents[(size_t)b * n + tid];
+    if (tid < n) par[tid] = my_parent;
     float4 *S4 = reinterpret_cast<float4 *>(pool + ((size_t)slot * Hv + h) * (kHeadDim * kHeadDim) + c0) + l8;
-    float4 s[kComRows];
+    uint64_t s[kComRows][2];                             // pairs of columns
 #pragma unroll
-    for (int m = 0; m < kComRows; ++m) s[m] = __ldcs(S4 + (rg + kComGroups * m) * (kHeadDim / 4));
+    for (int m = 0; m < kComRows; ++m) {
+        const float4 x = __ldcs(S4 + (rg + kComGroups * m) * (kHeadDim / 4));
+        s[m][0] = pack2(x.x, x.y);
+        s[m][1] = pack2(x.z, x.w);
+    }
     __syncthreads();
     if (tid == 0) {
         int len = 0, i = leaf;
@@ -463,29 +471,33 @@ commit_kernel(const T *__restrict__ k, const T *__restrict__ v, const float *__r
     __syncthreads();
     const int len = path_len;
     if (len == 0) return;
-    for (int d0 = 0; d0 < len; d0 += kGroup) {
+    // one group's inputs: element tid of each k, the gates, and what the substitution of this
+    // thread's column needs (root first; missing nodes get k = 0, gate 1 and no write)
+    float nk[kGroup], na[kGroup], nv[kGroup], nb[kGroup];
+    auto fetch = [&](int d0) {
         const int m = min(kGroup, len - d0);
-        // rows of the group (root first); missing nodes get k = 0 and no write
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j)
-            sk[j][tid] = j < m ? to_f32(k[(((size_t)b * n + path[len - 1 - d0 - j]) * Hqk + hq) * kHeadDim + tid]) : 0.f;
-        float a[kGroup];                                 // gates; 1 for missing nodes
 #pragma unroll
         for (int j = 0; j < kGroup; ++j) {
-            a[j] = 1.f;
-            if (j < m)
-                a[j] = fmaxf(DELTA ? alpha[((size_t)b * n + path[len - 1 - d0 - j]) * Hv + h] : decay[h], 1.6458114e-38f);
-        }
-        // what the substitution of this thread's column needs, on its way during the products
-        float vv[kGroup], be[kGroup];
-        if (tid < kComCols) {
-#pragma unroll
-            for (int j = 0; j < kGroup; ++j) {
-                const size_t at = ((size_t)b * n + path[len - 1 - d0 - min(j, m - 1)]) * Hv + h;
-                vv[j] = to_f32(v[at * kHeadDim + c0 + tid]);
-                be[j] = DELTA ? beta[at] : 1.f;
+            const size_t node = (size_t)b * n + path[len - 1 - d0 - min(j, m - 1)];
+            nk[j] = j < m ? to_f32(k[(node * Hqk + hq) * kHeadDim + tid]) : 0.f;
+            na[j] = j < m ? fmaxf(DELTA ? alpha[node * Hv + h] : decay[h], 1.6458114e-38f) : 1.f;
+            nv[j] = nb[j] = 0.f;
+            if (tid < kComCols) {
+                nv[j] = to_f32(v[(node * Hv + h) * kHeadDim + c0 + tid]);
+                if (DELTA) nb[j] = beta[node * Hv + h];
             }
         }
+    };
+    fetch(0);
+    for (int d0 = 0; d0 < len; d0 += kGroup) {
+        const int m = min(kGroup, len - d0);
+        float a[kGroup], vv[kGroup], be[kGroup];
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) {
+            sk[j][tid] = nk[j];
+            a[j] = na[j]; vv[j] = nv[j]; be[j] = nb[j];
+        }
+        if (d0 + kGroup < len) fetch(d0 + kGroup);       // while this group is worked on
         __syncthreads();
         if (DELTA) {
             for (int pr = warp; pr < 6; pr += kComThreads / 32) {        // k_i . k_j, i > j
@@ -497,28 +509,27 @@ commit_kernel(const T *__restrict__ k, const T *__restrict__ v, const float *__r
                 for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
                 if (lane == 0) skk[i][j] = x;
             }
-            float4 pp[kGroup];
-#pragma unroll
-            for (int j = 0; j < kGroup; ++j) pp[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int r = 0; r < kComRows; ++r) {
-#pragma unroll
-                for (int j = 0; j < kGroup; ++j) {
-                    const float ki = sk[j][rg + kComGroups * r];
-                    pp[j].x = fmaf(s[r].x, ki, pp[j].x); pp[j].y = fmaf(s[r].y, ki, pp[j].y);
-                    pp[j].z = fmaf(s[r].z, ki, pp[j].z); pp[j].w = fmaf(s[r].w, ki, pp[j].w);
-                }
-            }
 #pragma unroll
             for (int j = 0; j < kGroup; ++j) {
+                if (j >= m) break;
+                uint64_t p0 = 0, p1 = 0;
+#pragma unroll
+                for (int r = 0; r < kComRows; ++r) {
+                    const float ki = sk[j][rg + kComGroups * r];
+                    p0 = fma2(s[r][0], pack2(ki, ki), p0);
+                    p1 = fma2(s[r][1], pack2(ki, ki), p1);
+                }
+                float4 pp;
+                unpack2(p0, pp.x, pp.y);
+                unpack2(p1, pp.z, pp.w);
 #pragma unroll
                 for (int off = 8; off < 32; off <<= 1) {                 // the four row groups of a warp
-                    pp[j].x += __shfl_xor_sync(0xffffffffu, pp[j].x, off);
-                    pp[j].y += __shfl_xor_sync(0xffffffffu, pp[j].y, off);
-                    pp[j].z += __shfl_xor_sync(0xffffffffu, pp[j].z, off);
-                    pp[j].w += __shfl_xor_sync(0xffffffffu, pp[j].w, off);
+                    pp.x += __shfl_xor_sync(0xffffffffu, pp.x, off);
+                    pp.y += __shfl_xor_sync(0xffffffffu, pp.y, off);
+                    pp.z += __shfl_xor_sync(0xffffffffu, pp.z, off);
+                    pp.w += __shfl_xor_sync(0xffffffffu, pp.w, off);
                 }
-                if (lane < 8) part[warp][j][l8] = pp[j];
+                if (lane < 8) part[warp][j][l8] = pp;
             }
             __syncthreads();
         }
@@ -538,26 +549,42 @@ commit_kernel(const T *__restrict__ k, const T *__restrict__ v, const float *__r
                         u[j] = be[j] * (u[j] - a[j] * p);
                     }
                 }
-                su[j][tid] = u[j];
+            }
+            // the writes as they stand after the group: each decayed by the gates behind it
+            float behind = 1.f;
+#pragma unroll
+            for (int j = kGroup - 1; j >= 0; --j) {
+                su[j][tid] = behind * u[j];
+                behind *= a[j];
             }
         }
+        const float all = (a[0] * a[1]) * (a[2] * a[3]);
         __syncthreads();
-        float4 u4[kGroup];
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j) u4[j] = *reinterpret_cast<const float4 *>(&su[j][4 * l8]);
 #pragma unroll
         for (int r = 0; r < kComRows; ++r) {
+            s[r][0] = mul2(pack2(all, all), s[r][0]);
+            s[r][1] = mul2(pack2(all, all), s[r][1]);
+        }
 #pragma unroll
-            for (int j = 0; j < kGroup; ++j) {
+        for (int j = 0; j < kGroup; ++j) {
+            if (j >= m) break;
+            const float4 u4 = *reinterpret_cast<const float4 *>(&su[j][4 * l8]);
+#pragma unroll
+            for (int r = 0; r < kComRows; ++r) {
                 const float ki = sk[j][rg + kComGroups * r];
-                s[r].x = fmaf(a[j], s[r].x, ki * u4[j].x); s[r].y = fmaf(a[j], s[r].y, ki * u4[j].y);
-                s[r].z = fmaf(a[j], s[r].z, ki * u4[j].z); s[r].w = fmaf(a[j], s[r].w, ki * u4[j].w);
+                s[r][0] = fma2(pack2(ki, ki), pack2(u4.x, u4.y), s[r][0]);
+                s[r][1] = fma2(pack2(ki, ki), pack2(u4.z, u4.w), s[r][1]);
             }
         }
         __syncthreads();                                 // sk, su, part are written again
     }
 #pragma unroll
-    for (int m = 0; m < kComRows; ++m) __stcs(S4 + (rg + kComGroups * m) * (kHeadDim / 4), s[m]);
+    for (int m = 0; m < kComRows; ++m) {
+        float4 x;
+        unpack2(s[m][0], x.x, x.y);
+        unpack2(s[m][1], x.z, x.w);
+        __stcs(S4 + (rg + kComGroups * m) * (kHeadDim / 4), x);
+    }
 }
 
 template <typename T, bool DELTA>
