@@ -61,18 +61,16 @@ __device__ __forceinline__ uint32_t take_piece(float &a, float &b) {
     return __byte_perm(ua, ub, 0x7632);
 }
 
-__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+__device__ __forceinline__ void load4(const float *p, float (&x)[4]) {
+    const float4 a = *reinterpret_cast<const float4 *>(p);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        x[2 * e] = __uint_as_float(w[e] << 16);
-        x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    }
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&x)[4]) {
+    const uint2 a = *reinterpret_cast<const uint2 *>(p);
+    x[0] = __uint_as_float(a.x << 16);
+    x[1] = __uint_as_float(a.x & 0xffff0000u);
+    x[2] = __uint_as_float(a.y << 16);
+    x[3] = __uint_as_float(a.y & 0xffff0000u);
 }
 
 template <typename T> struct TreeTypes;
@@ -268,83 +266,87 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
             }
         }
     }
-    // ---- rows times S: this warp's 32 columns, thread (g, t) the columns 4g .. 4g+3 of B.
-    //      fp32 inputs: the tensor core truncates as it accumulates, so each 16 columns of K are
-    //      summed from zero, small pieces first, and added in fp32.
-    float acc[MT][4][4];
+    // ---- rows of k and of q times S: this warp's 16 columns (each piece of S is cut once), thread
+    //      (g, t) the columns 2g, 2g+1 of B.  fp32 inputs: the tensor core truncates as it accumulates,
+    //      so each 16 rows of S are summed from zero, small pieces first, and added in fp32.
+    constexpr int R0 = DELTA ? 0 : 1;                    // the decay rule needs no k S
+    const int cw = 16 * warp;
+    float acc[2][MT][2][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int r = R0; r < 2; ++r)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[mt][j][e] = 0.f;
-    if (DELTA || role == 1) {
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[r][mt][j][e] = 0.f;
 #pragma unroll 1
-        for (int ks = 0; ks < kHeadDim / 16; ++ks) {
-            float4 s0 = *reinterpret_cast<const float4 *>(&sm.S[ks * 16 + 2 * t][32 * cb + 4 * g]);
-            float4 s1 = *reinterpret_cast<const float4 *>(&sm.S[ks * 16 + 2 * t + 1][32 * cb + 4 * g]);
-            float4 s2 = *reinterpret_cast<const float4 *>(&sm.S[ks * 16 + 2 * t + 8][32 * cb + 4 * g]);
-            float4 s3 = *reinterpret_cast<const float4 *>(&sm.S[ks * 16 + 2 * t + 9][32 * cb + 4 * g]);
-            uint32_t bp[kPieces][4][2];
+    for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+        const float *sr = &sm.S[ks * 16 + 2 * t][cw + 2 * g];
+        float2 s0 = *reinterpret_cast<const float2 *>(sr), s1 = *reinterpret_cast<const float2 *>(sr + kLdS);
+        float2 s2 = *reinterpret_cast<const float2 *>(sr + 8 * kLdS), s3 = *reinterpret_cast<const float2 *>(sr + 9 * kLdS);
+        uint32_t bp[kPieces][2][2];
 #pragma unroll
-            for (int p = 0; p < kPieces; ++p) {
-                bp[p][0][0] = take_piece(s0.x, s1.x); bp[p][0][1] = take_piece(s2.x, s3.x);
-                bp[p][1][0] = take_piece(s0.y, s1.y); bp[p][1][1] = take_piece(s2.y, s3.y);
-                bp[p][2][0] = take_piece(s0.z, s1.z); bp[p][2][1] = take_piece(s2.z, s3.z);
-                bp[p][3][0] = take_piece(s0.w, s1.w); bp[p][3][1] = take_piece(s2.w, s3.w);
-            }
+        for (int p = 0; p < kPieces; ++p) {
+            bp[p][0][0] = take_piece(s0.x, s1.x); bp[p][0][1] = take_piece(s2.x, s3.x);
+            bp[p][1][0] = take_piece(s0.y, s1.y); bp[p][1][1] = take_piece(s2.y, s3.y);
+        }
+#pragma unroll
+        for (int r = R0; r < 2; ++r)
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 if constexpr (kPlanes == 1) {
                     uint32_t a[4];
-                    ldmatrix_x4(a, &sm.kq[0][role][mt * 16 + lrow][ks * 16 + lcol]);
+                    ldmatrix_x4(a, &sm.kq[0][r][mt * 16 + lrow][ks * 16 + lcol]);
 #pragma unroll
                     for (int p = kPieces - 1; p >= 0; --p)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) mma16816(acc[mt][j], a, bp[p][j][0], bp[p][j][1]);
+                        for (int j = 0; j < 2; ++j) mma16816(acc[r][mt][j], a, bp[p][j][0], bp[p][j][1]);
                 } else {
-                    float d[4][4] = {};
+                    float d[2][4] = {};
 #pragma unroll
                     for (int sum = kPieces - 1; sum >= 0; --sum)         // orders of size, small first
 #pragma unroll
                         for (int pa = sum; pa >= 0; --pa) {
                             uint32_t a[4];
-                            ldmatrix_x4(a, &sm.kq[pa][role][mt * 16 + lrow][ks * 16 + lcol]);
+                            ldmatrix_x4(a, &sm.kq[pa][r][mt * 16 + lrow][ks * 16 + lcol]);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) mma16816(d[j], a, bp[sum - pa][j][0], bp[sum - pa][j][1]);
+                            for (int j = 0; j < 2; ++j) mma16816(d[j], a, bp[sum - pa][j][0], bp[sum - pa][j][1]);
                         }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 2; ++j)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[mt][j][e] += d[j][e];
+                        for (int e = 0; e < 4; ++e) acc[r][mt][j][e] += d[j][e];
                 }
             }
-        }
     }
-    __syncthreads();                                     // S read; A and P written
-    // ---- accumulators: rows g, g + 8 of each tile, columns 32 cb + 8t .. + 7
+    // v of this thread's rows and columns, on its way over the barrier
+    float vv[MT][2][4];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int i = mt * 16 + g + 8 * half, c = 32 * cb + 8 * t;
-            float x[8];
+            const int i = mt * 16 + g + 8 * half;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[j] = acc[mt][j][2 * half];
-                x[4 + j] = acc[mt][j][2 * half + 1];
-            }
-            if (role == 0) {
-                const bool on = i < n && sm.mask[i] != 0;
-                const float f = sm.root[i], be = sm.beta[i];
-                float vv[8] = {};
-                if (on) load8(v + (((size_t)b * n + i) * Hv + h) * kHeadDim + c0 + c, vv);
+            for (int e = 0; e < 4; ++e) vv[mt][half][e] = 0.f;
+            if (i < n && sm.mask[i] != 0)
+                load4(v + (((size_t)b * n + i) * Hv + h) * kHeadDim + c0 + cw + 4 * t, vv[mt][half]);
+        }
+    __syncthreads();                                     // S read; A and P written
+    // ---- accumulators: rows g, g + 8 of each tile, columns cw + 4t .. + 3
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = DELTA ? be * (vv[j] - f * x[j]) : vv[j];
-            }
-            float *dst = role == 0 ? &sm.r.U[i][c] : &sm.r.QS[i][c];
-            *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<float4 *>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int i = mt * 16 + g + 8 * half, c = cw + 4 * t;
+            const float f = sm.root[i], be = sm.beta[i];
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[e] = DELTA ? be * (vv[mt][half][e] - f * acc[0][mt][e & 1][2 * half + (e >> 1)]) : vv[mt][half][e];
+            *reinterpret_cast<float4 *>(&sm.r.U[i][c]) = make_float4(x[0], x[1], x[2], x[3]);
+            const float(&y)[2][4] = acc[1][mt];
+            *reinterpret_cast<float4 *>(&sm.r.QS[i][c]) = make_float4(y[0][2 * half], y[1][2 * half], y[0][2 * half + 1], y[1][2 * half + 1]);
         }
     __syncthreads();
     // ---- levels: warp w owns nodes w, w + 4, ..., lane l columns 2l, 2l + 1
