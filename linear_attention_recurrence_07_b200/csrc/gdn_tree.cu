@@ -29,7 +29,6 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTreeThreads = 128;
 constexpr int kTreeCols = 64;            // columns of the state per CTA
 constexpr int kTreeSlices = kHeadDim / kTreeCols;
 constexpr int kLdS = kTreeCols + 4;      // floats per row of S, U, QS in shared memory
@@ -96,8 +95,11 @@ struct TreeSmem {
     int levels;
 };
 
+// Warps per CTA: four for small trees (of which more CTAs fit on an SM), eight for large ones.
+template <int N> struct TreeWarps { static constexpr int kWarps = N <= 16 ? 4 : 8; };
+
 template <typename T, bool DELTA, int N>
-__global__ void __launch_bounds__(kTreeThreads)
+__global__ void __launch_bounds__(TreeWarps<N>::kWarps * 32)
 tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
             const float *__restrict__ alpha, const float *__restrict__ beta, const float *__restrict__ decay,
             const int *__restrict__ parents, const float *__restrict__ pool, const int *__restrict__ slots,
@@ -105,23 +107,15 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
 {
     using Sm = TreeSmem<T, N>;
     constexpr int kPlanes = Sm::kPlanes, kPieces = TreeTypes<T>::kPieces, MT = N / 16;
+    constexpr int W = TreeWarps<N>::kWarps, kTreeThreads = W * 32;
     extern __shared__ __align__(16) unsigned char raw[];
     Sm &sm = *reinterpret_cast<Sm *>(raw);
     const unsigned bh = blockIdx.x / kTreeSlices;
     const int c0 = (int)(blockIdx.x - bh * kTreeSlices) * kTreeCols;
     const int b = (int)(bh / (unsigned)Hv), h = (int)(bh - (unsigned)b * Hv), hq = h / (Hv / Hqk);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int slot = slots ? slots[b] : b;
-    if (slot < 0 || slot >= n_slots) return;
-
-    const float *S = pool + ((size_t)slot * Hv + h) * (kHeadDim * kHeadDim) + c0;
-#pragma unroll
-    for (int m = 0; m < 16; ++m) {
-        const int row = (tid >> 4) + 8 * m, c = (tid & 15) * 4;
-        cp_async16(&sm.S[row][c], S + row * kHeadDim + c);
-    }
-
-    // ---- k and q rows as bf16 planes; rows past n are zeros
+    // ---- what does not wait for the slot: k and q rows (bf16: straight to shared memory; rows
+    //      past n are zeros), the tree and its gates, v of this thread's rows and columns
     if constexpr (kPlanes == 1) {
         for (int i = tid; i < 2 * N * 16; i += kTreeThreads) {
             const int which = i / (N * 16), r = (i / 16) % N, d = (i % 16) * 8;
@@ -130,12 +124,10 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
             else *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
         }
     }
+    constexpr int kPer = (N + 31) / 32;
+    int p[kPer];
+    float ga[kPer], be[kPer];
     if (warp == 0) {
-        // ---- paths and gates by pointer jumping: after round r, mask and b cover 2^r steps.
-        //      jump: next node up, -1 past the root, -2 padding.
-        constexpr int kPer = (N + 31) / 32;
-        int p[kPer];
-        float ga[kPer], be[kPer];
 #pragma unroll
         for (int x = 0; x < kPer; ++x) {
             const int i = lane + 32 * x;
@@ -147,6 +139,35 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
                 if (DELTA) be[x] = beta[at];
             }
         }
+    }
+    const int slot = slots ? slots[b] : b;
+    if (slot < 0 || slot >= n_slots) {
+        cp_async_wait_all();
+        return;
+    }
+    const float *S = pool + ((size_t)slot * Hv + h) * (kHeadDim * kHeadDim) + c0;
+#pragma unroll
+    for (int m = 0; m < 2048 / kTreeThreads; ++m) {
+        const int row = (tid >> 4) + (kTreeThreads / 16) * m, c = (tid & 15) * 4;
+        cp_async16(&sm.S[row][c], S + row * kHeadDim + c);
+    }
+    // warps by columns of S, and with eight of them by row set (0: k, 1: q)
+    constexpr int RW = W == 8 ? 1 : 2;                   // row sets per warp
+    const int role = W == 8 ? warp >> 2 : 0, cw = 16 * (warp & 3);
+    const int g = lane >> 2, t = lane & 3;
+    float vv[MT][2][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int i = mt * 16 + g + 8 * half;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) vv[mt][half][e] = 0.f;
+            if (i < n && (W == 4 || role == 0)) load4(v + (((size_t)b * n + i) * Hv + h) * kHeadDim + c0 + cw + 4 * t, vv[mt][half]);
+        }
+    if (warp == 0) {
+        // ---- paths and gates by pointer jumping: after round r, mask and b cover 2^r steps.
+        //      jump: next node up, -1 past the root, -2 padding.
 #pragma unroll
         for (int x = 0; x < kPer; ++x) {
             const int i = lane + 32 * x;
@@ -218,13 +239,12 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
     cp_async_wait_all();
     __syncthreads();
 
-    const int role = warp >> 1, cb = warp & 1;           // role 0: k rows, 1: q rows
-    const int g = lane >> 2, t = lane & 3;
     const int lrow = lane & 15, lcol = (lane >> 4) * 8;  // ldmatrix addresses
     // ---- grams with k -> coefficients of the path sums, j <= i only
-    if (DELTA || role == 1) {
+    const int gr = warp / (W / 2), gc = warp % (W / 2);  // row set and share of the columns
+    if (DELTA || gr == 1) {
 #pragma unroll 1
-        for (int nt = cb; nt < N / 8; nt += 2) {
+        for (int nt = gc; nt < N / 8; nt += W / 2) {
             uint32_t kb[kPlanes][kHeadDim / 16][2];          // this tile's 8 rows of k
 #pragma unroll
             for (int pb = 0; pb < kPlanes; ++pb)
@@ -234,8 +254,9 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
                     kb[pb][ks][0] = *reinterpret_cast<const uint32_t *>(kr);
                     kb[pb][ks][1] = *reinterpret_cast<const uint32_t *>(kr + 8);
                 }
-#pragma unroll 1
-            for (int mt = nt / 2; mt < MT; ++mt) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                if (mt < nt / 2) continue;
                 float acc[2][4] = {};                        // even and odd ks: half the chain
 #pragma unroll
                 for (int sum = kPlanes - 1; sum >= 0; --sum)
@@ -244,7 +265,7 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
 #pragma unroll
                         for (int ks = 0; ks < kHeadDim / 16; ++ks) {
                             uint32_t a[4];
-                            ldmatrix_x4(a, &sm.kq[pa][role][mt * 16 + lrow][ks * 16 + lcol]);
+                            ldmatrix_x4(a, &sm.kq[pa][gr][mt * 16 + lrow][ks * 16 + lcol]);
                             mma16816(acc[ks & 1], a, kb[sum - pa][ks][0], kb[sum - pa][ks][1]);
                         }
 #pragma unroll
@@ -255,7 +276,7 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
                     const float x = exp2f((bi.x - bj.x) + (bi.y - bj.y)) * (acc[0][e] + acc[1][e]);
                     const int at = __popcll(m & ((1ull << j) - 1ull));
                     if ((m >> j) & 1ull) {
-                        if (role == 0) {
+                        if (gr == 0) {
                             if (j < i) sm.A[i][at] = sm.beta[i] * x;
                         } else {
                             sm.P[i][at] = x;
@@ -269,17 +290,17 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
     // ---- rows of k and of q times S: this warp's 16 columns (each piece of S is cut once), thread
     //      (g, t) the columns 2g, 2g+1 of B.  fp32 inputs: the tensor core truncates as it accumulates,
     //      so each 16 rows of S are summed from zero, small pieces first, and added in fp32.
-    constexpr int R0 = DELTA ? 0 : 1;                    // the decay rule needs no k S
-    const int cw = 16 * warp;
-    float acc[2][MT][2][4];
+    float acc[RW][MT][2][4];
 #pragma unroll
-    for (int r = R0; r < 2; ++r)
+    for (int r = 0; r < RW; ++r)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[r][mt][j][e] = 0.f;
+    // the decay rule needs no k S
+    if (DELTA || W == 4 || role == 1)
 #pragma unroll 1
     for (int ks = 0; ks < kHeadDim / 16; ++ks) {
         const float *sr = &sm.S[ks * 16 + 2 * t][cw + 2 * g];
@@ -292,12 +313,12 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
             bp[p][1][0] = take_piece(s0.y, s1.y); bp[p][1][1] = take_piece(s2.y, s3.y);
         }
 #pragma unroll
-        for (int r = R0; r < 2; ++r)
+        for (int r = DELTA || RW == 1 ? 0 : 1; r < RW; ++r)
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 if constexpr (kPlanes == 1) {
                     uint32_t a[4];
-                    ldmatrix_x4(a, &sm.kq[0][r][mt * 16 + lrow][ks * 16 + lcol]);
+                    ldmatrix_x4(a, &sm.kq[0][role + r][mt * 16 + lrow][ks * 16 + lcol]);
 #pragma unroll
                     for (int p = kPieces - 1; p >= 0; --p)
 #pragma unroll
@@ -309,7 +330,7 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
 #pragma unroll
                         for (int pa = sum; pa >= 0; --pa) {
                             uint32_t a[4];
-                            ldmatrix_x4(a, &sm.kq[pa][r][mt * 16 + lrow][ks * 16 + lcol]);
+                            ldmatrix_x4(a, &sm.kq[pa][role + r][mt * 16 + lrow][ks * 16 + lcol]);
 #pragma unroll
                             for (int j = 0; j < 2; ++j) mma16816(d[j], a, bp[sum - pa][j][0], bp[sum - pa][j][1]);
                         }
@@ -320,18 +341,6 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
                 }
             }
     }
-    // v of this thread's rows and columns, on its way over the barrier
-    float vv[MT][2][4];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int i = mt * 16 + g + 8 * half;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) vv[mt][half][e] = 0.f;
-            if (i < n && sm.mask[i] != 0)
-                load4(v + (((size_t)b * n + i) * Hv + h) * kHeadDim + c0 + cw + 4 * t, vv[mt][half]);
-        }
     __syncthreads();                                     // S read; A and P written
     // ---- accumulators: rows g, g + 8 of each tile, columns cw + 4t .. + 3
 #pragma unroll
@@ -339,23 +348,27 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int i = mt * 16 + g + 8 * half, c = cw + 4 * t;
-            const float f = sm.root[i], be = sm.beta[i];
-            float x[4];
+            if (W == 4 || role == 0) {
+                const float f = sm.root[i], be_i = sm.beta[i];
+                float x[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                x[e] = DELTA ? be * (vv[mt][half][e] - f * acc[0][mt][e & 1][2 * half + (e >> 1)]) : vv[mt][half][e];
-            *reinterpret_cast<float4 *>(&sm.r.U[i][c]) = make_float4(x[0], x[1], x[2], x[3]);
-            const float(&y)[2][4] = acc[1][mt];
-            *reinterpret_cast<float4 *>(&sm.r.QS[i][c]) = make_float4(y[0][2 * half], y[1][2 * half], y[0][2 * half + 1], y[1][2 * half + 1]);
+                for (int e = 0; e < 4; ++e)
+                    x[e] = DELTA ? be_i * (vv[mt][half][e] - f * acc[0][mt][e & 1][2 * half + (e >> 1)]) : vv[mt][half][e];
+                *reinterpret_cast<float4 *>(&sm.r.U[i][c]) = make_float4(x[0], x[1], x[2], x[3]);
+            }
+            if (W == 4 || role == 1) {
+                const float(&y)[2][4] = acc[RW - 1][mt];
+                *reinterpret_cast<float4 *>(&sm.r.QS[i][c]) = make_float4(y[0][2 * half], y[1][2 * half], y[0][2 * half + 1], y[1][2 * half + 1]);
+            }
         }
     __syncthreads();
-    // ---- levels: warp w owns nodes w, w + 4, ..., lane l columns 2l, 2l + 1
-    constexpr int kOwn = N / 4;
+    // ---- levels: warp w of W owns nodes w, w + W, ..., lane l columns 2l, 2l + 1
+    constexpr int kOwn = N / W;
     float2 u[kOwn], out[kOwn];
     int len[kOwn];
 #pragma unroll
     for (int x = 0; x < kOwn; ++x) {
-        const int i = warp + 4 * x;
+        const int i = warp + W * x;
         len[x] = sm.len[i];
         const float2 r = *reinterpret_cast<const float2 *>(&sm.r.QS[i][2 * lane]);
         out[x] = make_float2(sm.root[i] * r.x, sm.root[i] * r.y);
@@ -367,13 +380,13 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
         if (DELTA && L > 0) {                            // the nodes of this level are finished
 #pragma unroll
             for (int x = 0; x < kOwn; ++x)
-                if (len[x] == L + 1) *reinterpret_cast<float2 *>(&sm.r.U[warp + 4 * x][2 * lane]) = u[x];
+                if (len[x] == L + 1) *reinterpret_cast<float2 *>(&sm.r.U[warp + W * x][2 * lane]) = u[x];
             __syncthreads();
         }
         // selected, not branched over, so that all rows are on their way at once
 #pragma unroll
         for (int x = 0; x < kOwn; ++x) {
-            const int i = warp + 4 * x;
+            const int i = warp + W * x;
             const float2 w = *reinterpret_cast<const float2 *>(&sm.r.U[sm.list[i][L]][2 * lane]);
             const float p = sm.P[i][L];
             const bool on = len[x] > L;
@@ -389,7 +402,7 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
     }
 #pragma unroll
     for (int x = 0; x < kOwn; ++x) {
-        const int i = warp + 4 * x;
+        const int i = warp + W * x;
         if (len[x] == 0) continue;                       // padding: the row stays as it was
         T *dst = o + (((size_t)b * n + i) * Hv + h) * kHeadDim + c0 + 2 * lane;
         if constexpr (kPlanes == 1) *reinterpret_cast<__nv_bfloat162 *>(dst) = __floats2bfloat162_rn(out[x].x, out[x].y);
@@ -403,7 +416,7 @@ cudaError_t launch_tree_n(const TreeArgs &a, cudaStream_t stream)
     const int smem = (int)sizeof(TreeSmem<T, N>);
     cudaError_t err = cudaFuncSetAttribute(tree_kernel<T, DELTA, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
-    tree_kernel<T, DELTA, N><<<(unsigned)((size_t)a.B * a.Hv * kTreeSlices), kTreeThreads, smem, stream>>>(
+    tree_kernel<T, DELTA, N><<<(unsigned)((size_t)a.B * a.Hv * kTreeSlices), TreeWarps<N>::kWarps * 32, smem, stream>>>(
         (const T *)a.q, (const T *)a.k, (const T *)a.v, a.alpha, a.beta, a.decay, a.parents, a.pool, a.slots, (T *)a.o,
         a.n, a.n_slots, a.Hqk, a.Hv);
     return cudaGetLastError();
