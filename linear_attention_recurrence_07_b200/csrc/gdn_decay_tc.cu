@@ -84,6 +84,7 @@ constexpr uint32_t IDD_D = idesc_bf16(128, 128, false, true);
 // shared memory leaves no L1): 40 + 2 x 160 + 2 x 56 <= 5 x 96.
 constexpr int kRegsIssue = 40, kRegsState = 160, kRegsP = 56, kRegsOut = 56;
 constexpr double kScaleFloor = -69.31471805599453;    // log of 2^-100
+constexpr float kScaleMin = 7.8886091e-31f;           // 2^-100
 
 template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -171,78 +172,89 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
     const int special = w.rev ? 0 : sp.nchunks - 1;
     const int tail = sp.L - (sp.nchunks - 1) * C;
     const int back = (w.fin_back && !STATE_ONLY) ? 1 : 0;
-    const double loglam = decay_log(w.decay[h]);
-    const bool strong = 63.0 * loglam < kScaleFloor;         // lambda^63 below the scales' floor
 
+    // The first stages' tiles, in flight while the rest is set up (only this thread waits on D_EMPTY).
+    auto load_stage = [&](int c) {
+        const int s = c % kStages;
+        int t0;
+        chunk_rows(sp, w.rev, sp.c0 + c, t0);
+        unsigned char *st = sm + s * kStageBytes;
+        uint64_t *full = &bar[D_FULL + s];
+        const int hx = h / (w.Hv / w.hx), hy = h / (w.Hv / w.hy), hz = h / (w.Hv / w.hz);
+        mbar_arrive_expect_tx(full, STATE_ONLY ? 4 * TILE : kStageBytes);
+        tma_load_4d(st + 2 * TILE, &tm_y, full, 0, hy, t0, sp.bt);
+        tma_load_4d(st + 3 * TILE, &tm_y, full, 64, hy, t0, sp.bt);
+        tma_load_4d(st + 4 * TILE, &tm_z, full, 0, hz, t0, sp.bt);
+        tma_load_4d(st + 5 * TILE, &tm_z, full, 64, hz, t0, sp.bt);
+        if (!STATE_ONLY) {
+            tma_load_4d(st + 0 * TILE, &tm_x, full, 0, hx, t0, sp.bt);
+            tma_load_4d(st + 1 * TILE, &tm_x, full, 64, hx, t0, sp.bt);
+        }
+    };
     if (tid == 0) {
-        if (!STATE_ONLY) { prefetch_tensormap(&tm_x); prefetch_tensormap(&tm_o); }
-        prefetch_tensormap(&tm_y);
-        prefetch_tensormap(&tm_z);
         for (int i = 0; i < (int)D_NBAR; ++i)
             mbar_init(&bar[i], i == D_ZP || i == D_HREADY ? 8 : i == D_PREADY || i == D_PREADY + 1 || i == D_OFREE ? 4
                                : ((i >= D_EMPTY && i < D_EMPTY + kStages) || i == D_DRAIN) && !STATE_ONLY ? 2 : 1);
         *abort_flag = 0;
         fence_mbar_init();
+#pragma unroll 1
+        for (int c = 0; c < min(n, kStages); ++c) load_stage(c);
+        if (!STATE_ONLY) prefetch_tensormap(&tm_o);
     }
-    if (warp == 0) {
+    if (warp == 1) {
         tmem_alloc(tmem_slot, T_COLS);
         tmem_relinquish();
     }
-    // tables: [0] of each pair for full chunks, [1] for the special one
-    for (int i = tid - 32; i >= 0 && i < 65 + 3 * 128; i += kDtThreads - 32) {
-        double e;
-        uint32_t at;
-        if (i < 65) {
-            e = i;
-            at = TAB_PW + i;
-        } else {
-            const int t = (i - 65) & 63, which = (i - 65) >> 6;          // w, w', f, f', c, c'
-            const int L = (which & 1) ? tail : C, bk = (which & 1) ? back : 0;
-            const int p = w.rev ? L - 1 - t : t;                         // tokens since the chunk's start
-            e = which < 2 ? max(L - p - bk, 0) : which < 4 ? p : -p;
-            at = TAB_W + (i - 65);
-            if (strong && which >= 2 && which < 4) e = fmin(e, kScaleFloor / loglam);
+    if (warp == 2 || warp == 3 || warp >= 12) {
+        // tables: [0] of each pair for full chunks, [1] for the special one
+        const double loglam = decay_log(w.decay[h]);
+        const bool strong = 63.0 * loglam < kScaleFloor;     // lambda^63 below the scales' floor
+        const int ti = warp < 4 ? tid - 64 : tid - 320;      // 0 .. 319
+        for (int i = ti; i < 65 + 3 * 128; i += 320) {
+            double e;
+            uint32_t at;
+            if (i < 65) {
+                e = i;
+                at = TAB_PW + i;
+            } else {
+                const int t = (i - 65) & 63, which = (i - 65) >> 6;      // w, w', f, f', c, c'
+                const int L = (which & 1) ? tail : C, bk = (which & 1) ? back : 0;
+                const int p = w.rev ? L - 1 - t : t;                     // tokens since the chunk's start
+                e = which < 2 ? max(L - p - bk, 0) : which < 4 ? p : -p;
+                at = TAB_W + (i - 65);
+                if (strong && which >= 2 && which < 4) e = fmin(e, kScaleFloor / loglam);
+            }
+            tab[at] = (float)decay_pow(loglam, e);
         }
-        tab[at] = (float)decay_pow(loglam, e);
-    }
-    if (tid < 18 && tid >= 2) {      // decay of segment tid - 2's start state up to this segment
-        const int g = tid - 2, here = tokens_before(sp, w.rev, sp.c0);
-        if (w.nseg > 1 && g <= sp.seg)
-            tab[TAB_SEG + g] = (float)decay_pow(loglam, here - tokens_before(sp, w.rev, g * w.seg_chunks));
-    } else if (tid < 2) {            // lambda^L of full chunks and of the special one, in two floats
-        const double p = decay_pow(loglam, tid ? tail - back : C);
-        tab[TAB_L + 2 * tid] = (float)p;
-        tab[TAB_L + 2 * tid + 1] = (float)(p - (double)(float)p);
+        if (ti < 18 && ti >= 2) {    // decay of segment ti - 2's start state up to this segment
+            const int g = ti - 2, here = tokens_before(sp, w.rev, sp.c0);
+            if (w.nseg > 1 && g <= sp.seg)
+                tab[TAB_SEG + g] = (float)decay_pow(loglam, here - tokens_before(sp, w.rev, g * w.seg_chunks));
+        } else if (ti < 2) {         // lambda^L of full chunks and of the special one, in two floats
+            const double p = decay_pow(loglam, ti ? tail - back : C);
+            tab[TAB_L + 2 * ti] = (float)p;
+            tab[TAB_L + 2 * ti + 1] = (float)(p - (double)(float)p);
+        }
     }
     tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    // Every role meets the others at this barrier once, after its register count is set (every
+    // warpgroup changes it, whether or not it has work below: the state's increase waits for the
+    // others' decrease) and, for the state, after its loads are issued.
+    auto all_set = [&]() -> uint32_t {
+        named_sync(3, kDtThreads);
+        tc_fence_after();
+        return *tmem_slot;
+    };
 
-    // Every warpgroup changes its share, whether or not it has work below: the state's increase
-    // waits for the others' decrease.
     if (warp < 4) {
         regs_dec<kRegsIssue>();
+        const uint32_t tmem = all_set();
         if (warp == 0 && lane == 0) {
             // ==================================================== TMA producer
-            const int hx = h / (w.Hv / w.hx), hy = h / (w.Hv / w.hy), hz = h / (w.Hv / w.hz);
-            int c = 0;
+            int c = min(n, kStages);
             for (; c < n; ++c) {
-                const int s = c % kStages;
-                if (c >= kStages && !ctl.wait_one(D_EMPTY + s, ((c / kStages) - 1) & 1)) break;
-                int t0;
-                chunk_rows(sp, w.rev, sp.c0 + c, t0);
-                unsigned char *st = sm + s * kStageBytes;
-                uint64_t *full = &bar[D_FULL + s];
-                mbar_arrive_expect_tx(full, STATE_ONLY ? 4 * TILE : kStageBytes);
-                tma_load_4d(st + 2 * TILE, &tm_y, full, 0, hy, t0, sp.bt);
-                tma_load_4d(st + 3 * TILE, &tm_y, full, 64, hy, t0, sp.bt);
-                tma_load_4d(st + 4 * TILE, &tm_z, full, 0, hz, t0, sp.bt);
-                tma_load_4d(st + 5 * TILE, &tm_z, full, 64, hz, t0, sp.bt);
-                if (!STATE_ONLY) {
-                    tma_load_4d(st + 0 * TILE, &tm_x, full, 0, hx, t0, sp.bt);
-                    tma_load_4d(st + 1 * TILE, &tm_x, full, 64, hx, t0, sp.bt);
-                }
+                if (!ctl.wait_one(D_EMPTY + c % kStages, ((c / kStages) - 1) & 1)) break;
+                load_stage(c);
             }
             // On an abort, copies still in flight land before the CTA's memory goes away.
             if (*abort_flag)
@@ -343,10 +355,34 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
         regs_inc<kRegsState>();
         const int q4 = warp & 3, part = (warp - 4) >> 2;
         const int dz = q4 * 32 + lane;
-        const uint32_t t_lane = tmem + ((uint32_t)(q4 * 32) << 16);
         uint64_t H[32];                                      // H^T[dz][64 part + 2 e], +1
 #pragma unroll
         for (int e = 0; e < 32; ++e) H[e] = 0;
+        const bool has_init = w.init && (STATE_ONLY ? sp.copy_init : w.nseg == 1);
+        if (has_init) {
+            const float *src = w.init + ((size_t)sp.b * w.Hv + h) * hstate;
+            if (w.init_trans) {
+                const float4 *row = reinterpret_cast<const float4 *>(src + (size_t)dz * kHeadDim + 64 * part);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float4 v = row[e];
+                    H[2 * e] = pack2(v.x, v.y);
+                    H[2 * e + 1] = pack2(v.z, v.w);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const float *at = src + (size_t)(64 * part + 2 * e) * kHeadDim + dz;
+                    H[e] = pack2(at[0], at[kHeadDim]);
+                }
+            }
+        }
+        const uint32_t tmem = all_set(), t_lane = tmem + ((uint32_t)(q4 * 32) << 16);
+        if (has_init && w.init_decays && sp.L > 0) {
+            const float f = tab[TAB_PW + 1];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) H[e] = mul2(pack2(f, f), H[e]);
+        }
         if (w.nseg > 1 && !STATE_ONLY) {
 #pragma unroll 1
             for (int g = 0; g <= sp.seg; ++g) {
@@ -355,24 +391,6 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
                     H[e] = fma2(pack2(f, f), pack2(src[(size_t)(2 * e) * kHeadDim], src[(size_t)(2 * e + 1) * kHeadDim]), H[e]);
-            }
-        } else if (w.init && (!STATE_ONLY || sp.copy_init)) {
-            const float f = (w.init_decays && sp.L > 0) ? tab[TAB_PW + 1] : 1.f;
-            const float *src = w.init + ((size_t)sp.b * w.Hv + h) * hstate;
-            if (w.init_trans) {
-                const float4 *row = reinterpret_cast<const float4 *>(src + (size_t)dz * kHeadDim + 64 * part);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float4 v = row[e];
-                    H[2 * e] = pack2(f * v.x, f * v.y);
-                    H[2 * e + 1] = pack2(f * v.z, f * v.w);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float *at = src + (size_t)(64 * part + 2 * e) * kHeadDim + dz;
-                    H[e] = pack2(f * at[0], f * at[kHeadDim]);
-                }
             }
         }
         auto write_h = [&]() {
@@ -495,6 +513,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
         // ======================================================== P
         regs_dec<kRegsP>();
         const int q4 = warp & 3;
+        const uint32_t tmem = all_set();
         const uint32_t t_lane = tmem + ((uint32_t)(q4 * 32) << 16);
         const int g = lane >> 2, t = lane & 3, i0 = 16 * q4 + g;         // rows i0, i0 + 8
         unsigned char *pt = sm + DOFF_P + i0 * 128 + 4 * t;
@@ -541,7 +560,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[D_PREADY + (c & 1)]);                  // and G is read
         };
-        if (!strong) {
+        if (tab[TAB_PW + 63] >= kScaleMin) {
             for (int c = 0; c < n && !STATE_ONLY; ++c) {
                 if (!wait_p(c)) break;
                 const float *ct = tab + TAB_C + (sp.c0 + c == special ? 64 : 0) + 2 * t;
@@ -593,6 +612,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
         // ======================================================== O
         regs_dec<kRegsOut>();
         const int q4 = warp & 3;
+        const uint32_t tmem = all_set();
         const uint32_t t_lane = tmem + ((uint32_t)(q4 * 32) << 16);
         const bool leader = tid == 512;
         const int t = lane & 3;
@@ -658,9 +678,9 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, T_COLS);
+        tmem_dealloc(*tmem_slot, T_COLS);
         if (lane == 0 && *abort_flag) atomicOr(&g_tc_error, 1u);
     }
 }
