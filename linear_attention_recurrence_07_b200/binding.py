@@ -495,7 +495,9 @@ def _workspace(workspace, nbytes, dev, stream):
     """The caller's workspace checked, or one for this call, kept by the allocator until the
     work on ``stream`` is done."""
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        if nbytes == 0:
+            return None
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         if stream is not None:
             workspace.record_stream(stream)
     elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
@@ -546,7 +548,7 @@ def gdn_decay_fwd(q, k, v, decay, S0, o, S_final, workspace=None, stream=None):
     workspace = _workspace(workspace, need, dev, stream)
     _check(_call(dev, library().gdn_decay_fwd, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0), _ptr(o),
                  _ptr(S_final), B, T, Hqk, Hv, dk, dv, _DTYPES[q.dtype], _ptr(workspace),
-                 workspace.numel(), _stream_handle(stream, dev)),
+                 0 if workspace is None else workspace.numel(), _stream_handle(stream, dev)),
            "gdn_decay_fwd")
 
 
@@ -635,7 +637,8 @@ def gdn_decay_bwd(q, k, v, decay, S0, dO, dS_final, dq, dk, dv, dS0, workspace=N
     workspace = _workspace(workspace, need, dev, stream)
     _check(_call(dev, library().gdn_decay_bwd, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0), _ptr(dO),
                  _ptr(dS_final), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dS0), B, T, Hqk, Hv, dkk, dvv,
-                 _DTYPES[q.dtype], _ptr(workspace), workspace.numel(), _stream_handle(stream, dev)),
+                 _DTYPES[q.dtype], _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                 _stream_handle(stream, dev)),
            "gdn_decay_bwd")
 
 

@@ -232,11 +232,14 @@ cudaError_t launch_typed(const DecayWalks &d, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-// One thread per four columns of an output row.
+// One thread per four columns of an output row; blockIdx.y picks the array.
 template <typename T>
 __global__ void __launch_bounds__(256)
-head_sum_kernel(const float *__restrict__ part, T *__restrict__ out, long long n4, int Hqk, int G)
+head_sum_kernel(const float *__restrict__ part_a, const float *__restrict__ part_b, T *__restrict__ out_a,
+                T *__restrict__ out_b, long long n4, int G)
 {
+    const float *part = blockIdx.y ? part_b : part_a;
+    T *out = blockIdx.y ? out_b : out_a;
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n4; i += (long long)gridDim.x * 256) {
         const long long row = i >> 5;                    // token * Hqk + head
         const int d = (int)(i & 31) * 4;
@@ -247,8 +250,12 @@ head_sum_kernel(const float *__restrict__ part, T *__restrict__ out, long long n
             a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
         }
         T *dst = out + row * kHeadDim + d;
-        dst[0] = from_f32<T>(a.x); dst[1] = from_f32<T>(a.y);
-        dst[2] = from_f32<T>(a.z); dst[3] = from_f32<T>(a.w);
+        if constexpr (sizeof(T) == 2) {
+            __nv_bfloat162 v[2] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(a.z, a.w)};
+            *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(v);
+        } else {
+            *reinterpret_cast<float4 *>(dst) = a;
+        }
     }
 }
 
@@ -259,15 +266,15 @@ cudaError_t launch_decay_walks_simt(const DecayWalks &d, gdn_dtype dtype, cudaSt
     return dtype == GDN_BF16 ? launch_typed<__nv_bfloat16>(d, stream) : launch_typed<float>(d, stream);
 }
 
-cudaError_t launch_head_sum(const float *part, void *out, long long rows, int Hqk, int Hv, gdn_dtype dtype,
-                            cudaStream_t stream)
+cudaError_t launch_head_sums(const float *part_a, const float *part_b, void *out_a, void *out_b, long long rows,
+                             int Hqk, int Hv, gdn_dtype dtype, cudaStream_t stream)
 {
     const long long n4 = rows * Hqk * (kHeadDim / 4);
-    const unsigned grid = (unsigned)((n4 + 255) / 256 < 148 * 16 ? (n4 + 255) / 256 : 148 * 16);
+    const dim3 grid((unsigned)((n4 + 255) / 256 < 148 * 8 ? (n4 + 255) / 256 : 148 * 8), 2);
     if (dtype == GDN_BF16)
-        head_sum_kernel<<<grid, 256, 0, stream>>>(part, (__nv_bfloat16 *)out, n4, Hqk, Hv / Hqk);
+        head_sum_kernel<<<grid, 256, 0, stream>>>(part_a, part_b, (__nv_bfloat16 *)out_a, (__nv_bfloat16 *)out_b, n4, Hv / Hqk);
     else
-        head_sum_kernel<<<grid, 256, 0, stream>>>(part, (float *)out, n4, Hqk, Hv / Hqk);
+        head_sum_kernel<<<grid, 256, 0, stream>>>(part_a, part_b, (float *)out_a, (float *)out_b, n4, Hv / Hqk);
     return cudaGetLastError();
 }
 

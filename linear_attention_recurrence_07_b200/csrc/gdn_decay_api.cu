@@ -287,8 +287,7 @@ gdn_status gdn_decay_bwd(const void *q, const void *k, const void *v, const floa
     wv.fin = dS0;
     wv.o = dv;
     cudaError_t err = launch_walks(d, dtype, s);
-    if (err == cudaSuccess && shared) err = gdn::launch_head_sum(rows_q, dq, tokens, Hqk, Hv, dtype, s);
-    if (err == cudaSuccess && shared) err = gdn::launch_head_sum(rows_k, dk, tokens, Hqk, Hv, dtype, s);
+    if (err == cudaSuccess && shared) err = gdn::launch_head_sums(rows_q, rows_k, dq, dk, tokens, Hqk, Hv, dtype, s);
     return launch_status(err);
 }
 

@@ -132,9 +132,8 @@ struct TcWalks {
 };
 
 // Rows of O from the accumulators one column (token) at a time: ragged chunks of packed
-// sequences, and fp32 partial rows (a warp writes 32 consecutive values of a row).
-template <typename OT>
-__device__ __forceinline__ void store_rows(OT *dst, uint32_t t_lane, const float *gt, int rows, size_t stride) {
+// sequences, whose rows past the end belong to others.
+__device__ __forceinline__ void store_rows(__nv_bfloat16 *dst, uint32_t t_lane, const float *gt, int rows, size_t stride) {
 #pragma unroll 1
     for (int r0 = 0; r0 < rows; r0 += 8) {
         float x[8];
@@ -142,7 +141,7 @@ __device__ __forceinline__ void store_rows(OT *dst, uint32_t t_lane, const float
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (r0 + e < rows) dst[(size_t)(r0 + e) * stride] = from_f32<OT>(gt[r0 + e] * x[e]);
+            if (r0 + e < rows) dst[(size_t)(r0 + e) * stride] = __float2bfloat16_rn(gt[r0 + e] * x[e]);
     }
 }
 
@@ -629,13 +628,43 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
             if (leader) bulk_wait_group_read0();             // the store before has read the staging tile
             if (!named_and(2, 128, ctl.wait(D_OFULL + (c & 1), (c >> 1) & 1))) break;
             tc_fence_after();
-            if (w.o_f32 || (rows < C && w.cu_seqlens)) {
-                const size_t at = ((size_t)sp.bt * w.T + t0) * stride + (size_t)h * kHeadDim + q4 * 32 + lane;
-                if (w.o_f32) store_rows(static_cast<float *>(w.o) + at, t_lane, ft, rows, stride);
-                else store_rows(static_cast<__nv_bfloat16 *>(w.o) + at, t_lane, ft, rows, stride);
+            if (rows < C && w.cu_seqlens) {
+                store_rows(static_cast<__nv_bfloat16 *>(w.o) + ((size_t)sp.bt * w.T + t0) * stride + (size_t)h * kHeadDim +
+                               q4 * 32 + lane, t_lane, ft, rows, stride);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[D_OFREE]);
+                continue;
+            }
+            if (w.o_f32) {
+                // fp32 rows (dense): 32 tokens x 128 values fill the staging tile; the second half is
+                // out of TMEM before it waits for the store of the first
+                float *tile = reinterpret_cast<float *>(sm + DOFF_O) + q4 * 32 + lane;
+#pragma unroll 1
+                for (int cb = 0; cb < 2; ++cb) {
+                    float x[32];
+                    tmem_ld32(t_lane + T_O + 32 * cb, x);
+                    tmem_wait_ld();
+                    if (cb == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar[D_OFREE]);
+                        if (leader) bulk_wait_group_read0();
+                        named_sync(2, 128);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 f = *reinterpret_cast<const float2 *>(ft + 32 * cb + e);
+                        tile[e * kHeadDim] = f.x * x[e];
+                        tile[(e + 1) * kHeadDim] = f.y * x[e + 1];
+                    }
+                    fence_proxy_async_smem();
+                    named_sync(2, 128);
+                    if (leader) {
+                        tma_store_4d(&tm_o, sm + DOFF_O, 0, h, t0 + 32 * cb, sp.bt);
+                        bulk_commit_group();
+                    }
+                }
                 continue;
             }
 #pragma unroll 1
@@ -685,6 +714,20 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
     }
 }
 
+// Map over a [B, T, H, 128] fp32 tensor; box = 128 x 1 head x 32 tokens x 1, rows as they are.
+bool make_map_f32(CUtensorMap *map, const void *base, int B, int T, int H)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)kHeadDim, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
+    const cuuint64_t strides[3] = {(cuuint64_t)kHeadDim * 4, (cuuint64_t)H * kHeadDim * 4, (cuuint64_t)T * H * kHeadDim * 4};
+    const cuuint32_t box[4] = {(cuuint32_t)kHeadDim, 1, 32, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool STATE_ONLY, int NZ, int NP>
 cudaError_t launch_tc(const TcWalks &p, cudaStream_t stream)
 {
@@ -719,8 +762,8 @@ cudaError_t launch_decay_walks_tc(const DecayWalks &d, cudaStream_t stream)
         if (!make_map(&p.maps[i][0], w.x, rows_b, w.T, w.hx) || !make_map(&p.maps[i][1], w.y, rows_b, w.T, w.hy) ||
             !make_map(&p.maps[i][2], w.z, rows_b, w.T, w.hz))
             return cudaErrorInvalidValue;
-        if (w.o_f32) p.maps[i][3] = p.maps[i][0];    // not used
-        else if (!make_map(&p.maps[i][3], w.o, rows_b, w.T, w.Hv)) return cudaErrorInvalidValue;
+        if (!(w.o_f32 ? make_map_f32(&p.maps[i][3], w.o, rows_b, w.T, w.Hv) : make_map(&p.maps[i][3], w.o, rows_b, w.T, w.Hv)))
+            return cudaErrorInvalidValue;
         ends = ends || w.fin;
     }
     const DecayWalk &w = d.w[0];

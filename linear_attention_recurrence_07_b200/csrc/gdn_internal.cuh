@@ -112,9 +112,9 @@ struct DecayWalks {
 cudaError_t launch_decay_walks_simt(const DecayWalks &d, gdn_dtype dtype, cudaStream_t stream);
 cudaError_t launch_decay_walks_tc(const DecayWalks &d, cudaStream_t stream);   // bf16 operands
 cudaError_t decay_tc_take_error(unsigned *out);
-// out [rows, Hqk, 128] = sum over each QK head's V heads of part [rows, Hv, 128]
-cudaError_t launch_head_sum(const float *part, void *out, long long rows, int Hqk, int Hv,
-                            gdn_dtype dtype, cudaStream_t stream);
+// out_a, out_b [rows, Hqk, 128] = sums over each QK head's V heads of part_a, part_b [rows, Hv, 128]
+cudaError_t launch_head_sums(const float *part_a, const float *part_b, void *out_a, void *out_b, long long rows,
+                             int Hqk, int Hv, gdn_dtype dtype, cudaStream_t stream);
 
 struct DecayDecodeArgs {
     const void *q, *k, *v;
