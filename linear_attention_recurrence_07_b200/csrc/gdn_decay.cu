@@ -34,6 +34,8 @@ struct SimtSmem {
     float H[kHeadDim][kLdZ];
     float P[kChunk][kLdP];
     float pw[kChunk + 1];                    // lambda^0 .. lambda^64
+    float seg[16];                           // decay of each segment's state up to this one
+    float2 step[2];                          // lambda^L as two floats: full chunks, the sequence's last
 };
 
 template <typename T>
@@ -58,17 +60,31 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
     const int h = blockIdx.x / kZSlices, z0 = (blockIdx.x - h * kZSlices) * kDz;
     const WalkSpan sp = walk_span(w, blockIdx.y, state_only);
     const size_t st = (size_t)kHeadDim * kHeadDim;
-    const double loglam = decay_log(w.decay[h]);
+    const int tail = sp.L - (sp.nchunks - 1) * kChunk, special = w.rev ? 0 : sp.nchunks - 1;
+    const int last_back = w.fin_back && !state_only;     // the end state is wanted undecayed
 
-    if (tid <= kChunk) sm.pw[tid] = (float)decay_pow(loglam, tid);
+    if (tid < kChunk + 1 + 16 + 2) {
+        const double loglam = decay_log(w.decay[h]);
+        if (tid <= kChunk) {
+            sm.pw[tid] = (float)decay_pow(loglam, tid);
+        } else if (tid <= kChunk + 16) {
+            const int g = tid - kChunk - 1, here = tokens_before(sp, w.rev, sp.c0);
+            if (w.nseg > 1 && !state_only && g <= sp.seg)
+                sm.seg[g] = (float)decay_pow(loglam, here - tokens_before(sp, w.rev, g * w.seg_chunks));
+        } else {
+            const int last = tid - kChunk - 17;
+            const double p = decay_pow(loglam, last ? tail - last_back : kChunk);
+            sm.step[last] = make_float2((float)p, (float)(p - (double)(float)p));
+        }
+    }
+    __syncthreads();
     // ---- start state
     if (w.nseg > 1 && !state_only) {
-        const int here = tokens_before(sp, w.rev, sp.c0);
         for (int i = tid; i < kHeadDim * (kDz / 4); i += kSimtThreads) {
             const int d = i >> 3, c = (i & 7) * 4;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int g = 0; g <= sp.seg; ++g) {          // entry g holds the walk up to segment g's start
-                const float f = (float)decay_pow(loglam, here - tokens_before(sp, w.rev, g * w.seg_chunks));
+                const float f = sm.seg[g];
                 const float4 v = *reinterpret_cast<const float4 *>(
                     w.seg + (((size_t)sp.b * w.nseg + g) * w.Hv + h) * st + (size_t)d * kHeadDim + z0 + c);
                 a.x = fmaf(f, v.x, a.x); a.y = fmaf(f, v.y, a.y);
@@ -78,7 +94,7 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
         }
     } else {
         const float *src = (w.init && (!state_only || sp.copy_init)) ? w.init + ((size_t)sp.b * w.Hv + h) * st : nullptr;
-        const float f = (w.init_decays && sp.L > 0) ? (float)decay_pow(loglam, 1.0) : 1.f;
+        const float f = (w.init_decays && sp.L > 0) ? sm.pw[1] : 1.f;
         for (int i = tid; i < kHeadDim * kDz; i += kSimtThreads) {
             const int d = w.init_trans ? (i & (kHeadDim - 1)) : i / kDz;
             const int c = w.init_trans ? i / kHeadDim : i % kDz;
@@ -140,47 +156,72 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
                     sm.P[i][j] = e >= 0 ? sm.pw[max(e, 0)] * p[a][b] : 0.f;
                 }
             __syncthreads();
-            // ---- o: rows r, r + 32, four columns
-            const int r = tid >> 3, cc = (tid & 7) * 4;
-            float acc[2][4] = {}, dia[2][4] = {};
-            for (int d = 0; d < kHeadDim; ++d) {
-                const float4 hv = *reinterpret_cast<const float4 *>(&sm.H[d][cc]);
+            // ---- o: rows 4 r .., four columns; the two halves of the block take half of d and of j
+            const int part = tid >> 7, r = (tid & 127) >> 3, cc = (tid & 7) * 4;
+            float acc[4][4] = {}, dia[4][4] = {};
+            for (int d = 64 * part; d < 64 * part + 64; d += 4) {
+                float4 hv[4];
 #pragma unroll
-                for (int a = 0; a < 2; ++a) {
-                    const float xv = sm.x[r + 32 * a][d];
-                    acc[a][0] = fmaf(xv, hv.x, acc[a][0]); acc[a][1] = fmaf(xv, hv.y, acc[a][1]);
-                    acc[a][2] = fmaf(xv, hv.z, acc[a][2]); acc[a][3] = fmaf(xv, hv.w, acc[a][3]);
+                for (int e = 0; e < 4; ++e) hv[e] = *reinterpret_cast<const float4 *>(&sm.H[d + e][cc]);
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    const float4 xv = *reinterpret_cast<const float4 *>(&sm.x[4 * r + a][d]);
+                    const float xx[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        acc[a][0] = fmaf(xx[e], hv[e].x, acc[a][0]); acc[a][1] = fmaf(xx[e], hv[e].y, acc[a][1]);
+                        acc[a][2] = fmaf(xx[e], hv[e].z, acc[a][2]); acc[a][3] = fmaf(xx[e], hv[e].w, acc[a][3]);
+                    }
                 }
             }
-            for (int j = 0; j < L; ++j) {
-                const float4 zv = *reinterpret_cast<const float4 *>(&sm.z[j][cc]);
+            for (int j = 4 * part; j < L; j += 8) {              // rows past L of z are zeros
+                float4 zv[4];
 #pragma unroll
-                for (int a = 0; a < 2; ++a) {
-                    const float pv = sm.P[r + 32 * a][j];
-                    dia[a][0] = fmaf(pv, zv.x, dia[a][0]); dia[a][1] = fmaf(pv, zv.y, dia[a][1]);
-                    dia[a][2] = fmaf(pv, zv.z, dia[a][2]); dia[a][3] = fmaf(pv, zv.w, dia[a][3]);
+                for (int e = 0; e < 4; ++e) zv[e] = *reinterpret_cast<const float4 *>(&sm.z[j + e][cc]);
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    const float4 pv = *reinterpret_cast<const float4 *>(&sm.P[4 * r + a][j]);
+                    const float pp[4] = {pv.x, pv.y, pv.z, pv.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        dia[a][0] = fmaf(pp[e], zv[e].x, dia[a][0]); dia[a][1] = fmaf(pp[e], zv[e].y, dia[a][1]);
+                        dia[a][2] = fmaf(pp[e], zv[e].z, dia[a][2]); dia[a][3] = fmaf(pp[e], zv[e].w, dia[a][3]);
+                    }
                 }
             }
+            __syncthreads();                                     // P and x have been read
+            float *half = &sm.P[0][0] + (tid & 127) * 16;        // 128 x 16 floats of P's room
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                const int i = r + 32 * a;
-                if (i >= L) continue;
-                const float f = sm.pw[w.rev ? L - 1 - i : i];
-                const size_t at = ((tok + i) * w.Hv + h) * kHeadDim + z0 + cc;
+            for (int a = 0; a < 4; ++a) {
+                const int i = 4 * r + a;
+                const float f = sm.pw[w.rev ? max(L - 1 - i, 0) : i];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float v = fmaf(f, acc[a][e], dia[a][e]);
-                    if (w.o_f32) static_cast<float *>(w.o)[at + e] = v;
-                    else static_cast<T *>(w.o)[at + e] = from_f32<T>(v);
+                for (int e = 0; e < 4; ++e) acc[a][e] = fmaf(f, acc[a][e], dia[a][e]);
+                if (part) *reinterpret_cast<float4 *>(half + 4 * a) = make_float4(acc[a][0], acc[a][1], acc[a][2], acc[a][3]);
+            }
+            __syncthreads();
+            if (!part) {
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    const int i = 4 * r + a;
+                    if (i >= L) continue;
+                    const float4 o4 = *reinterpret_cast<const float4 *>(half + 4 * a);
+                    const float v[4] = {acc[a][0] + o4.x, acc[a][1] + o4.y, acc[a][2] + o4.z, acc[a][3] + o4.w};
+                    const size_t at = ((tok + i) * w.Hv + h) * kHeadDim + z0 + cc;
+                    if (w.o_f32 || sizeof(T) == 4) {
+                        *reinterpret_cast<float4 *>(static_cast<float *>(w.o) + at) = make_float4(v[0], v[1], v[2], v[3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) static_cast<T *>(w.o)[at + e] = from_f32<T>(v[e]);
+                    }
                 }
             }
             __syncthreads();
         }
         // ---- H: rows d0 .. d0 + 3, columns 4 (tid & 7) ..
         {
-            const int back = (w.fin_back && !state_only && c == sp.nchunks - 1) ? 1 : 0;
-            const double pl = decay_pow(loglam, L - back);
-            const float hi = (float)pl, lo = (float)(pl - (double)hi);
+            const int back = last_back && c == special ? 1 : 0;
+            const float2 step = sm.step[c == special];
             const int d0 = (tid >> 3) * 4, cc = (tid & 7) * 4;
             float acc[4][4] = {};
             for (int j = 0; j < L; ++j) {
@@ -199,7 +240,7 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float &hv = sm.H[d0 + a][cc + e];
-                    hv = fmaf(hi, hv, fmaf(lo, hv, acc[a][e]));
+                    hv = fmaf(step.x, hv, fmaf(step.y, hv, acc[a][e]));
                 }
         }
         __syncthreads();
