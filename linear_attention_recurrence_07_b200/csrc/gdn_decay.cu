@@ -12,23 +12,22 @@
 // and lambda^L enters the state as a sum of two floats: its rounding would add up
 // over hundreds of chunks of a slowly decaying head.
 //
-// A CTA owns 32 columns of one head's state and output: with four CTAs per head the
-// score tile is computed four times (it is a quarter of the work), and short
-// prompts of few heads still spread over the device.  Everything sits in shared
-// memory, 4 x 4 register tiles per thread.
+// Two forms.  Wide: a CTA owns a whole head (128 columns of the state and output), 8 x 4
+// and 8 x 8 register tiles, the next chunk's rows on their way into registers during the
+// sums.  Narrow: 32 columns, two CTAs per SM; the score tile is computed four times, but
+// short prompts of few heads still spread over the device.
 #include "decay_common.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int kSimtThreads = 256;
-constexpr int kDz = 32;                      // columns of the state per CTA
-constexpr int kZSlices = kHeadDim / kDz;
 constexpr int kLdX = kHeadDim + 4;           // padded rows
 constexpr int kLdP = kChunk + 4;
-constexpr int kLdZ = kDz + 4;
 
+template <int DZ>                            // columns of the state per CTA
 struct SimtSmem {
+    static constexpr int kLdZ = DZ + 4;
     float x[kChunk][kLdX], y[kChunk][kLdX];
     float z[kChunk][kLdZ];
     float H[kHeadDim][kLdZ];
@@ -50,14 +49,25 @@ template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bf
 }
 
 template <typename T>
+__device__ __forceinline__ void store4(const DecayWalk &w, size_t at, const float (&v)[4]) {
+    if (w.o_f32 || sizeof(T) == 4) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(w.o) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) static_cast<T *>(w.o)[at + e] = from_f32<T>(v[e]);
+    }
+}
+
+template <typename T, int DZ>
 __global__ void __launch_bounds__(kSimtThreads)
 decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
 {
+    constexpr int kZSlices = kHeadDim / DZ;
     const DecayWalk &w = d.w[blockIdx.z];
     extern __shared__ __align__(16) unsigned char raw[];
-    SimtSmem &sm = *reinterpret_cast<SimtSmem *>(raw);
+    SimtSmem<DZ> &sm = *reinterpret_cast<SimtSmem<DZ> *>(raw);
     const int tid = threadIdx.x;
-    const int h = blockIdx.x / kZSlices, z0 = (blockIdx.x - h * kZSlices) * kDz;
+    const int h = blockIdx.x / kZSlices, z0 = (blockIdx.x - h * kZSlices) * DZ;
     const WalkSpan sp = walk_span(w, blockIdx.y, state_only);
     const size_t st = (size_t)kHeadDim * kHeadDim;
     const int tail = sp.L - (sp.nchunks - 1) * kChunk, special = w.rev ? 0 : sp.nchunks - 1;
@@ -80,8 +90,8 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
     __syncthreads();
     // ---- start state
     if (w.nseg > 1 && !state_only) {
-        for (int i = tid; i < kHeadDim * (kDz / 4); i += kSimtThreads) {
-            const int d = i >> 3, c = (i & 7) * 4;
+        for (int i = tid; i < kHeadDim * (DZ / 4); i += kSimtThreads) {
+            const int d = i / (DZ / 4), c = (i % (DZ / 4)) * 4;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int g = 0; g <= sp.seg; ++g) {          // entry g holds the walk up to segment g's start
                 const float f = sm.seg[g];
@@ -95,9 +105,9 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
     } else {
         const float *src = (w.init && (!state_only || sp.copy_init)) ? w.init + ((size_t)sp.b * w.Hv + h) * st : nullptr;
         const float f = (w.init_decays && sp.L > 0) ? sm.pw[1] : 1.f;
-        for (int i = tid; i < kHeadDim * kDz; i += kSimtThreads) {
-            const int d = w.init_trans ? (i & (kHeadDim - 1)) : i / kDz;
-            const int c = w.init_trans ? i / kHeadDim : i % kDz;
+        for (int i = tid; i < kHeadDim * DZ; i += kSimtThreads) {
+            const int d = w.init_trans ? (i & (kHeadDim - 1)) : i / DZ;
+            const int c = w.init_trans ? i / kHeadDim : i % DZ;
             const size_t at = w.init_trans ? (size_t)(z0 + c) * kHeadDim + d : (size_t)d * kHeadDim + z0 + c;
             sm.H[d][c] = src ? f * src[at] : 0.f;
         }
@@ -107,26 +117,46 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
     const T *x = static_cast<const T *>(w.x), *y = static_cast<const T *>(w.y), *z = static_cast<const T *>(w.z);
     const int xh = h / (w.Hv / w.hx), yh = h / (w.Hv / w.hy), zh = h / (w.Hv / w.hz);
     const int ti = tid >> 4, tj = tid & 15;      // 16 x 16 threads
+    // a chunk's rows: 8 float4 of x and of y and DZ / 16 of z per thread, zeros past the end
+    constexpr int kZ4 = DZ / 16;
+    float4 px[8], py[8], pz[kZ4];
+    auto fetch = [&](int c) {
+        int t0;
+        const int L = chunk_rows(sp, w.rev, c, t0);
+        const size_t tok = (size_t)sp.bt * w.T + t0;
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+            const int r = (tid >> 5) + 8 * m, d = (tid & 31) * 4;
+            px[m] = py[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < L) {
+                if (!state_only) px[m] = load4(x + ((tok + r) * w.hx + xh) * kHeadDim + d);
+                py[m] = load4(y + ((tok + r) * w.hy + yh) * kHeadDim + d);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < kZ4; ++m) {
+            const int i = tid + m * kSimtThreads, r = i / (DZ / 4), d = (i % (DZ / 4)) * 4;
+            pz[m] = r < L ? load4(z + ((tok + r) * w.hz + zh) * kHeadDim + z0 + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    };
+    if (DZ == 128 && sp.c0 < sp.c1) fetch(sp.c0);
     for (int c = sp.c0; c < sp.c1; ++c) {
         int t0;
         const int L = chunk_rows(sp, w.rev, c, t0);
         const size_t tok = (size_t)sp.bt * w.T + t0;
-        for (int i = tid; i < kChunk * (kHeadDim / 4); i += kSimtThreads) {
-            const int r = i >> 5, d = (i & 31) * 4;
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-            if (r < L) {
-                if (!state_only) a = load4(x + ((tok + r) * w.hx + xh) * kHeadDim + d);
-                b = load4(y + ((tok + r) * w.hy + yh) * kHeadDim + d);
-            }
-            *reinterpret_cast<float4 *>(&sm.x[r][d]) = a;
-            *reinterpret_cast<float4 *>(&sm.y[r][d]) = b;
+        if (DZ != 128) fetch(c);
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+            *reinterpret_cast<float4 *>(&sm.x[(tid >> 5) + 8 * m][(tid & 31) * 4]) = px[m];
+            *reinterpret_cast<float4 *>(&sm.y[(tid >> 5) + 8 * m][(tid & 31) * 4]) = py[m];
         }
-        for (int i = tid; i < kChunk * (kDz / 4); i += kSimtThreads) {
-            const int r = i >> 3, d = (i & 7) * 4;
-            *reinterpret_cast<float4 *>(&sm.z[r][d]) =
-                r < L ? load4(z + ((tok + r) * w.hz + zh) * kHeadDim + z0 + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int m = 0; m < kZ4; ++m) {
+            const int i = tid + m * kSimtThreads;
+            *reinterpret_cast<float4 *>(&sm.z[i / (DZ / 4)][(i % (DZ / 4)) * 4]) = pz[m];
         }
         __syncthreads();
+        if (DZ == 128 && c + 1 < sp.c1) fetch(c + 1);
         if (!state_only) {
             // ---- P: rows ti + 16 a, columns tj + 16 b
             float p[4][4] = {};
@@ -156,6 +186,53 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
                     sm.P[i][j] = e >= 0 ? sm.pw[max(e, 0)] * p[a][b] : 0.f;
                 }
             __syncthreads();
+            if constexpr (DZ == 128) {
+            // ---- o: warp = 8 rows, lane = four columns
+            const int r = tid >> 5, cc = (tid & 31) * 4;
+            float acc[8][4] = {};
+            for (int d = 0; d < kHeadDim; d += 4) {
+                float4 hv[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) hv[e] = *reinterpret_cast<const float4 *>(&sm.H[d + e][cc]);
+#pragma unroll
+                for (int a = 0; a < 8; ++a) {
+                    const float4 xv = *reinterpret_cast<const float4 *>(&sm.x[8 * r + a][d]);
+                    const float xx[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        acc[a][0] = fmaf(xx[e], hv[e].x, acc[a][0]); acc[a][1] = fmaf(xx[e], hv[e].y, acc[a][1]);
+                        acc[a][2] = fmaf(xx[e], hv[e].z, acc[a][2]); acc[a][3] = fmaf(xx[e], hv[e].w, acc[a][3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < 8; ++a) {
+                const int i = 8 * r + a;
+                const float f = sm.pw[w.rev ? max(L - 1 - i, 0) : i];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[a][e] *= f;
+            }
+            // columns of P that some of the 8 rows can see; rows past L of z are zeros
+            const int j0 = w.rev ? 8 * r : 0, j1 = w.rev ? L : min(L, 8 * r + 8);
+            for (int j = j0; j < j1; j += 4) {
+                float4 zv[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) zv[e] = *reinterpret_cast<const float4 *>(&sm.z[j + e][cc]);
+#pragma unroll
+                for (int a = 0; a < 8; ++a) {
+                    const float4 pv = *reinterpret_cast<const float4 *>(&sm.P[8 * r + a][j]);
+                    const float pp[4] = {pv.x, pv.y, pv.z, pv.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        acc[a][0] = fmaf(pp[e], zv[e].x, acc[a][0]); acc[a][1] = fmaf(pp[e], zv[e].y, acc[a][1]);
+                        acc[a][2] = fmaf(pp[e], zv[e].z, acc[a][2]); acc[a][3] = fmaf(pp[e], zv[e].w, acc[a][3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < 8; ++a)
+                if (8 * r + a < L) store4<T>(w, ((tok + 8 * r + a) * w.Hv + h) * kHeadDim + cc, acc[a]);
+            } else {
             // ---- o: rows 4 r .., four columns; the two halves of the block take half of d and of j
             const int part = tid >> 7, r = (tid & 127) >> 3, cc = (tid & 7) * 4;
             float acc[4][4] = {}, dia[4][4] = {};
@@ -207,40 +284,46 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
                     if (i >= L) continue;
                     const float4 o4 = *reinterpret_cast<const float4 *>(half + 4 * a);
                     const float v[4] = {acc[a][0] + o4.x, acc[a][1] + o4.y, acc[a][2] + o4.z, acc[a][3] + o4.w};
-                    const size_t at = ((tok + i) * w.Hv + h) * kHeadDim + z0 + cc;
-                    if (w.o_f32 || sizeof(T) == 4) {
-                        *reinterpret_cast<float4 *>(static_cast<float *>(w.o) + at) = make_float4(v[0], v[1], v[2], v[3]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) static_cast<T *>(w.o)[at + e] = from_f32<T>(v[e]);
-                    }
+                    store4<T>(w, ((tok + i) * w.Hv + h) * kHeadDim + z0 + cc, v);
                 }
+            }
             }
             __syncthreads();
         }
-        // ---- H: rows d0 .. d0 + 3, columns 4 (tid & 7) ..
+        // ---- H: rows d0 .., columns c0 .. (wide: and c0 + 64 ..)
         {
+            constexpr int RD = DZ == 128 ? 8 : 4, CZ = DZ == 128 ? 2 : 1;
             const int back = last_back && c == special ? 1 : 0;
             const float2 step = sm.step[c == special];
-            const int d0 = (tid >> 3) * 4, cc = (tid & 7) * 4;
-            float acc[4][4] = {};
+            const int d0 = (DZ == 128 ? tid >> 4 : tid >> 3) * RD, c0 = (DZ == 128 ? tid & 15 : tid & 7) * 4;
+            float acc[RD][4 * CZ] = {};
             for (int j = 0; j < L; ++j) {
                 const float f = sm.pw[(w.rev ? j + 1 : L - j) - back];
-                const float4 yv = *reinterpret_cast<const float4 *>(&sm.y[j][d0]);
-                const float4 zv = *reinterpret_cast<const float4 *>(&sm.z[j][cc]);
-                const float yy[4] = {f * yv.x, f * yv.y, f * yv.z, f * yv.w};
+                float yy[RD];
 #pragma unroll
-                for (int a = 0; a < 4; ++a) {
-                    acc[a][0] = fmaf(yy[a], zv.x, acc[a][0]); acc[a][1] = fmaf(yy[a], zv.y, acc[a][1]);
-                    acc[a][2] = fmaf(yy[a], zv.z, acc[a][2]); acc[a][3] = fmaf(yy[a], zv.w, acc[a][3]);
+                for (int e = 0; e < RD; e += 4) {
+                    const float4 yv = *reinterpret_cast<const float4 *>(&sm.y[j][d0 + e]);
+                    yy[e] = f * yv.x; yy[e + 1] = f * yv.y; yy[e + 2] = f * yv.z; yy[e + 3] = f * yv.w;
+                }
+#pragma unroll
+                for (int q = 0; q < CZ; ++q) {
+                    const float4 zv = *reinterpret_cast<const float4 *>(&sm.z[j][c0 + 64 * q]);
+#pragma unroll
+                    for (int a = 0; a < RD; ++a) {
+                        float *t = &acc[a][4 * q];
+                        t[0] = fmaf(yy[a], zv.x, t[0]); t[1] = fmaf(yy[a], zv.y, t[1]);
+                        t[2] = fmaf(yy[a], zv.z, t[2]); t[3] = fmaf(yy[a], zv.w, t[3]);
+                    }
                 }
             }
 #pragma unroll
-            for (int a = 0; a < 4; ++a)
+            for (int a = 0; a < RD; ++a)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float &hv = sm.H[d0 + a][cc + e];
-                    hv = fmaf(step.x, hv, fmaf(step.y, hv, acc[a][e]));
+                for (int q = 0; q < CZ; ++q) {
+                    float4 &hv = *reinterpret_cast<float4 *>(&sm.H[d0 + a][c0 + 64 * q]);
+                    const float *t = &acc[a][4 * q];
+                    hv = make_float4(fmaf(step.x, hv.x, fmaf(step.y, hv.x, t[0])), fmaf(step.x, hv.y, fmaf(step.y, hv.y, t[1])),
+                                     fmaf(step.x, hv.z, fmaf(step.y, hv.z, t[2])), fmaf(step.x, hv.w, fmaf(step.y, hv.w, t[3])));
                 }
         }
         __syncthreads();
@@ -250,26 +333,26 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
     if (state_only) dst = w.seg + (((size_t)sp.b * w.nseg + sp.seg) * w.Hv + h) * st;
     else if (w.fin && sp.c1 == sp.nchunks) dst = w.fin + ((size_t)sp.b * w.Hv + h) * st;
     if (dst)
-        for (int i = tid; i < kHeadDim * (kDz / 4); i += kSimtThreads) {
-            const int d = i >> 3, cc = (i & 7) * 4;
+        for (int i = tid; i < kHeadDim * (DZ / 4); i += kSimtThreads) {
+            const int d = i / (DZ / 4), cc = (i % (DZ / 4)) * 4;
             *reinterpret_cast<float4 *>(dst + (size_t)d * kHeadDim + z0 + cc) =
                 *reinterpret_cast<const float4 *>(&sm.H[d][cc]);
         }
 }
 
-template <typename T>
+template <typename T, int DZ>
 cudaError_t launch_typed(const DecayWalks &d, cudaStream_t stream)
 {
-    cudaError_t err = cudaFuncSetAttribute(decay_walk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)sizeof(SimtSmem));
+    const int smem = (int)sizeof(SimtSmem<DZ>);
+    cudaError_t err = cudaFuncSetAttribute(decay_walk_kernel<T, DZ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     const DecayWalk &w = d.w[0];
-    const dim3 grid((unsigned)w.Hv * kZSlices, (unsigned)(w.B * w.nseg), (unsigned)d.n);
+    const dim3 grid((unsigned)w.Hv * (kHeadDim / DZ), (unsigned)(w.B * w.nseg), (unsigned)d.n);
     if (w.nseg > 1) {
-        decay_walk_kernel<T><<<grid, kSimtThreads, sizeof(SimtSmem), stream>>>(d, true);
+        decay_walk_kernel<T, DZ><<<grid, kSimtThreads, smem, stream>>>(d, true);
         if ((err = cudaGetLastError()) != cudaSuccess) return err;
     }
-    decay_walk_kernel<T><<<grid, kSimtThreads, sizeof(SimtSmem), stream>>>(d, false);
+    decay_walk_kernel<T, DZ><<<grid, kSimtThreads, smem, stream>>>(d, false);
     return cudaGetLastError();
 }
 
@@ -304,7 +387,8 @@ head_sum_kernel(const float *__restrict__ part_a, const float *__restrict__ part
 
 cudaError_t launch_decay_walks_simt(const DecayWalks &d, gdn_dtype dtype, cudaStream_t stream)
 {
-    return dtype == GDN_BF16 ? launch_typed<__nv_bfloat16>(d, stream) : launch_typed<float>(d, stream);
+    if (d.wide) return dtype == GDN_BF16 ? launch_typed<__nv_bfloat16, 128>(d, stream) : launch_typed<float, 128>(d, stream);
+    return dtype == GDN_BF16 ? launch_typed<__nv_bfloat16, 32>(d, stream) : launch_typed<float, 32>(d, stream);
 }
 
 cudaError_t launch_head_sums(const float *part_a, const float *part_b, void *out_a, void *out_b, long long rows,

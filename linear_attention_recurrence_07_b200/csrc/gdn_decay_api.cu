@@ -30,22 +30,33 @@ int sm_count()
 
 constexpr size_t kStateBytes = (size_t)gdn::kHeadDim * gdn::kHeadDim * sizeof(float);
 constexpr int kMaxDecaySegments = 16;
+constexpr int kWideHeads = 100;
+
+// fp32: whether a CTA takes a whole head (half the arithmetic) or 32 of its columns (four
+// times the CTAs).
+bool wide_walk(const DecayWalk &w, int walks)
+{
+    const int nchunks = (w.T + gdn::kChunk - 1) / gdn::kChunk;
+    const long long heads = (long long)w.B * w.Hv * walks;
+    const int most = w.cu_seqlens ? 1 : nchunks < kMaxDecaySegments ? nchunks : kMaxDecaySegments;
+    return heads * most >= kWideHeads;
+}
 
 // Segments of `walks` dense walks that run side by side: as many as fill the device with
-// one CTA (fp32: one head's four half-SM CTAs) per walk, head and segment.  bf16: of at
-// least four chunks, because the launch that computes their start states reads y and z
+// one CTA (fp32, narrow: one head's four half-SM CTAs) per walk, head and segment.  bf16: of
+// at least four chunks, because the launch that computes their start states reads y and z
 // once more and starts anew; the fp32 kernel is bound by its arithmetic, of which that
-// launch has a fifth, so one chunk is enough.
+// launch has a quarter, so one chunk is enough.
 void choose_segments(DecayWalk &w, int walks, gdn_dtype dtype)
 {
-    const int kMinSegmentChunks = dtype == GDN_F32 ? 1 : 4;
+    const int least = dtype == GDN_F32 ? 1 : 4;
     const int nchunks = (w.T + gdn::kChunk - 1) / gdn::kChunk;
-    const long long units = (long long)w.B * w.Hv * walks * (dtype == GDN_F32 ? 2 : 1);
+    const long long units = (long long)w.B * w.Hv * walks * (dtype == GDN_F32 && !wide_walk(w, walks) ? 2 : 1);
     long long n = sm_count() / units;
     if (n > kMaxDecaySegments) n = kMaxDecaySegments;
     if (n < 1) n = 1;
     int per = (int)((nchunks + n - 1) / n);
-    if (per < kMinSegmentChunks) per = kMinSegmentChunks;
+    if (per < least) per = least;
     w.seg_chunks = per;
     w.nseg = (nchunks + per - 1) / per;
     if (w.nseg < 1) w.nseg = 1;
@@ -108,6 +119,7 @@ gdn_status fwd_common(const void *q, const void *k, const void *v, const float *
             w.seg = static_cast<float *>(workspace);
         }
     }
+    d.wide = wide_walk(w, 1);
     return launch_status(launch_walks(d, dtype, s));
 }
 
@@ -259,6 +271,7 @@ gdn_status gdn_decay_bwd(const void *q, const void *k, const void *v, const floa
 
     gdn::DecayWalks d{};
     d.n = 3;
+    d.wide = wide_walk(w, 3);
     for (int i = 0; i < 3; ++i) {
         d.w[i] = w;
         d.w[i].seg = seg ? reinterpret_cast<float *>(ws + i * seg) : nullptr;

@@ -108,6 +108,7 @@ constexpr int kMaxWalks = 3;
 struct DecayWalks {
     DecayWalk w[kMaxWalks];
     int n;
+    bool wide;      // CUDA cores: one CTA per head instead of four
 };
 cudaError_t launch_decay_walks_simt(const DecayWalks &d, gdn_dtype dtype, cudaStream_t stream);
 cudaError_t launch_decay_walks_tc(const DecayWalks &d, cudaStream_t stream);   // bf16 operands
