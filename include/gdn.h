@@ -452,9 +452,10 @@ gdn_status gdn_bwd_chunk(const void *q, const void *k, const void *v, const floa
  *      NULL (zeros).
  * Out: o [B, T, Hv, dv]; S_final [B, Hv, dk, dv] or NULL (may be S0).
  * dtype: GDN_F32 computes in fp32 on CUDA cores; GDN_BF16 on the tensor cores
- *      with an fp32 state: k's decayed copies enter in three bf16 pieces (the
- *      24 bits of an fp32), so S_final carries fp32 accuracy; the state that o
- *      reads enters in two.
+ *      with an fp32 state: v's decayed copies enter its update in three bf16
+ *      pieces (the 24 bits of an fp32), so S_final carries fp32 accuracy; where o
+ *      reads it, the state is rounded to bf16, and so are the decayed scores
+ *      (two pieces of 16 bits in all for T <= 64).
  * With few heads for the device (B * Hv below the number of SMs) each sequence
  * is cut into up to 16 segments whose states a first launch computes side by
  * side.  workspace: device scratch of gdn_decay_fwd_workspace(...) bytes for the

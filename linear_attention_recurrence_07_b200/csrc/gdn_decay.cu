@@ -16,6 +16,10 @@
 // and 8 x 8 register tiles, the next chunk's rows on their way into registers during the
 // sums.  Narrow: 32 columns, two CTAs per SM; the score tile is computed four times, but
 // short prompts of few heads still spread over the device.
+//
+// Bound by fp32 arithmetic: 1.8 M multiply-adds per chunk and head (wide), 14,400 cycles of
+// an SM; measured 17 us, of which shared-memory operands and the phases' barriers take the
+// rest.  48 heads, T=512: 120 us; gradients of B=2, T=206: 202 us (narrow: 369).
 #include "decay_common.cuh"
 
 namespace gdn {

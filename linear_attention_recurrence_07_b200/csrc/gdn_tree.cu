@@ -21,6 +21,11 @@
 // the row its ancestor has just finished, into registers, and the nodes of the next level
 // are finished.  A bushy tree costs its depth, not its size; non-ancestors are never read,
 // so that what is not finite stays below its node.
+//
+// Measured, 48 heads: 128 sequences of 8 nodes 128 us (3.2 TB/s, half of the copy bandwidth),
+// 32 of 30 nodes 73 us, 16 of 48 nodes 70 us.  Bound by latency: a CTA's way from the load
+// through the grams, the products and the levels is 6 to 12 us, and shared memory holds two
+// to five CTAs per SM.  Commit, 128 sequences of 7 nodes: 164 us, 4.9 TB/s.
 #include "gdn_internal.cuh"
 #include "sm100.cuh"
 
