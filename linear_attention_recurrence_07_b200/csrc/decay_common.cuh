@@ -12,6 +12,29 @@ namespace {
 __device__ __forceinline__ double decay_log(float lam) { return fmax(log((double)lam), -87.0); }
 __device__ __forceinline__ double decay_pow(double loglam, double e) { return exp(e * loglam); }
 
+// The two launches of a segmented walk overlap: the first lets the second start as its CTAs
+// leave (and may itself be gone before anything of it is read), the second sets itself up,
+// loads its first rows, and waits for the first's states just before it reads them.
+__device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launches the second of the two.
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream, Args... args)
+{
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // What one CTA of a walk does.  Chunk c of the walk (c0 <= c < c1) holds token rows
 // tb + 64 m .. of batch row bt, m = c forwards and nchunks - 1 - c backwards.
 struct WalkSpan {

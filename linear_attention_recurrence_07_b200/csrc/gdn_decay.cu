@@ -73,6 +73,7 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
     const int tid = threadIdx.x;
     const int h = blockIdx.x / kZSlices, z0 = (blockIdx.x - h * kZSlices) * DZ;
     const WalkSpan sp = walk_span(w, blockIdx.y, state_only);
+    if (state_only) let_next_launch_start();
     const size_t st = (size_t)kHeadDim * kHeadDim;
     const int tail = sp.L - (sp.nchunks - 1) * kChunk, special = w.rev ? 0 : sp.nchunks - 1;
     const int last_back = w.fin_back && !state_only;     // the end state is wanted undecayed
@@ -94,6 +95,7 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
     __syncthreads();
     // ---- start state
     if (w.nseg > 1 && !state_only) {
+        wait_for_launch_before();
         for (int i = tid; i < kHeadDim * (DZ / 4); i += kSimtThreads) {
             const int d = i / (DZ / 4), c = (i % (DZ / 4)) * 4;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -355,6 +357,7 @@ cudaError_t launch_typed(const DecayWalks &d, cudaStream_t stream)
     if (w.nseg > 1) {
         decay_walk_kernel<T, DZ><<<grid, kSimtThreads, smem, stream>>>(d, true);
         if ((err = cudaGetLastError()) != cudaSuccess) return err;
+        return launch_after(decay_walk_kernel<T, DZ>, grid, kSimtThreads, smem, stream, d, false);
     }
     decay_walk_kernel<T, DZ><<<grid, kSimtThreads, smem, stream>>>(d, false);
     return cudaGetLastError();

@@ -173,6 +173,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
     const int h = blockIdx.x;
     const WalkSpan sp = walk_span(w, blockIdx.y, STATE_ONLY);
     const int n = sp.c1 - sp.c0;                             // chunks of this CTA
+    if (STATE_ONLY) let_next_launch_start();
     const uint32_t sbase = smem_u32(sm);
     const size_t hstate = (size_t)kHeadDim * kHeadDim;
 
@@ -393,6 +394,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
             for (int e = 0; e < 32; ++e) H[e] = mul2(pack2(f, f), H[e]);
         }
         if (w.nseg > 1 && !STATE_ONLY) {
+            wait_for_launch_before();
 #pragma unroll 1
             for (int g = 0; g <= sp.seg; ++g) {
                 const float f = tab[TAB_SEG + g];
@@ -745,8 +747,9 @@ cudaError_t launch_tc(const TcWalks &p, cudaStream_t stream)
                                            (int)D_SMEM);
     if (err != cudaSuccess) return err;
     const DecayWalk &w = p.d.w[0];
-    decay_tc_kernel<STATE_ONLY, NZ, NP>
-        <<<dim3((unsigned)w.Hv, (unsigned)(w.B * w.nseg), (unsigned)p.d.n), kDtThreads, D_SMEM, stream>>>(p);
+    const dim3 grid((unsigned)w.Hv, (unsigned)(w.B * w.nseg), (unsigned)p.d.n);
+    if (!STATE_ONLY && w.nseg > 1) return launch_after(decay_tc_kernel<STATE_ONLY, NZ, NP>, grid, kDtThreads, (int)D_SMEM, stream, p);
+    decay_tc_kernel<STATE_ONLY, NZ, NP><<<grid, kDtThreads, D_SMEM, stream>>>(p);
     return cudaGetLastError();
 }
 
