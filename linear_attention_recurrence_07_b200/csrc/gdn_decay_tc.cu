@@ -62,7 +62,7 @@ constexpr uint32_t DOFF_P = kStages * kStageBytes;    // two buffers, chunk c us
 constexpr uint32_t DOFF_O = DOFF_P + 2 * TILE;
 constexpr uint32_t DOFF_TAB = DOFF_O + 2 * TILE;      // powers; per token: Z weights, O scales, P scales
 constexpr uint32_t TAB_PW = 0, TAB_W = 66, TAB_F = 66 + 128, TAB_C = 66 + 256, TAB_L = 66 + 3 * 128,
-                   TAB_SEG = TAB_L + 4, TAB_FLOATS = TAB_SEG + 16;
+                   TAB_FLOATS = TAB_L + 6;
 constexpr uint32_t DOFF_BAR = DOFF_TAB + TAB_FLOATS * 4;
 enum : int {
     D_FULL = 0,                    // x4: tiles of a stage landed
@@ -78,7 +78,8 @@ enum : int {
     D_GFULL = 14,                  // G done
     D_PREADY = 16,                 // P written, G read (4 warps)
     D_OFULL = 18,                  // O done
-    D_NBAR = 20
+    D_CUT = 20,                    // once: rows behind a packed sequence are zeros (8 warps)
+    D_NBAR = 21
 };
 constexpr uint32_t DOFF_MISC = DOFF_BAR + D_NBAR * 8;
 constexpr uint32_t D_SMEM = DOFF_MISC + 8 + 1024;
@@ -168,6 +169,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + DOFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + DOFF_MISC + 4);
     float *tab = reinterpret_cast<float *>(sm + DOFF_TAB);
+    float *seg_decay = reinterpret_cast<float *>(sm + DOFF_O);       // read before any O
     const DecayCtl ctl{bar, abort_flag};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x;
@@ -203,7 +205,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
     };
     if (tid == 0) {
         for (int i = 0; i < (int)D_NBAR; ++i)
-            mbar_init(&bar[i], i == D_ZP || i == D_HREADY ? 8 : i == D_PREADY || i == D_PREADY + 1 || i == D_OFREE ? 4
+            mbar_init(&bar[i], i == D_ZP || i == D_HREADY || i == D_CUT ? 8 : i == D_PREADY || i == D_PREADY + 1 || i == D_OFREE ? 4
                                : ((i >= D_EMPTY && i < D_EMPTY + kStages) || i == D_DRAIN) && !STATE_ONLY ? 2 : 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -239,7 +241,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
         if (ti < 18 && ti >= 2) {    // decay of segment ti - 2's start state up to this segment
             const int g = ti - 2, here = tokens_before(sp, w.rev, sp.c0);
             if (w.nseg > 1 && g <= sp.seg)
-                tab[TAB_SEG + g] = (float)decay_pow(loglam, here - tokens_before(sp, w.rev, g * w.seg_chunks));
+                seg_decay[g] = (float)decay_pow(loglam, here - tokens_before(sp, w.rev, g * w.seg_chunks));
         } else if (ti < 2) {         // lambda^L of full chunks and of the special one, in two floats
             const double p = decay_pow(loglam, ti ? tail - back : C);
             tab[TAB_L + 2 * ti] = (float)p;
@@ -303,8 +305,8 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
             auto issue_g = [&](int c) -> bool {
                 const int s = c % kStages;
                 if (!ctl.wait(D_FULL + s, (c / kStages) & 1)) return false;
-                // rows past a packed sequence's end are zeroed before Z' is announced
-                if (w.cu_seqlens && sp.c0 + c == special && !ctl.wait(D_ZP, c & 1)) return false;
+                // not on D_ZP, which can still be a phase short of the one before this chunk's
+                if (w.cu_seqlens && sp.c0 + c == special && tail < C && !ctl.wait(D_CUT, 0)) return false;
                 tc_fence_after();                            // G of two chunks before has been read
                 if (elect_one()) {
                     const uint64_t xd = smem_desc_sw128(sbase + s * kStageBytes, 16, 1024);
@@ -397,7 +399,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
             wait_for_launch_before();
 #pragma unroll 1
             for (int g = 0; g <= sp.seg; ++g) {
-                const float f = tab[TAB_SEG + g];
+                const float f = seg_decay[g];
                 const float *src = w.seg + (((size_t)sp.b * w.nseg + g) * w.Hv + h) * hstate + (size_t)64 * part * kHeadDim + dz;
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
@@ -440,6 +442,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
                         *reinterpret_cast<uint4 *>(z + sw128_chunk(32 * part + lane, 4 * (q4 & 1) + k)) = make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
                 __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[D_CUT]);
             }
             const float *wt = tab + TAB_W + (sp_c ? 64 : 0) + my_token;
             const uint32_t at = z_at + s * kStageBytes;

@@ -160,6 +160,27 @@ def test_packed_prefill_keeps_bad_values_apart(dtype, value):
         check_forward(part, o[None, a:e], SF[i:i + 1], f"sequence {i}")
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_packed_prefill_keeps_bad_values_from_long_sequences(dtype, value):
+    """As above behind sequences of two to six chunks, whose last chunk is cut by their end."""
+    n = [70, 3, 101, 20, 190, 64, 230, 5, 129, 1, 333, 40]
+    d = inputs((sum(n),), 2, 4, dtype, 87, states=len(n))
+    clean = {k: v.clone() for k, v in d.items()}
+    cu = torch.tensor(np.cumsum([0] + n), dtype=torch.int32)
+    for i in range(1, len(n), 2):
+        for name in ("q", "k", "v"):
+            d[name][cu[i]:cu[i + 1]] = value
+    x = dev(d)
+    o, SF = torch.empty_like(x["v"]), torch.empty((len(n), 4, 128, 128), device=DEV)
+    binding.gdn_decay_fwd_varlen(x["q"], x["k"], x["v"], x["decay"], x["S0"], o, SF, cu.to(DEV))
+    for i in range(0, len(n), 2):
+        a, e = int(cu[i]), int(cu[i + 1])
+        part = {k: (v[None, a:e] if k in ("q", "k", "v") else v) for k, v in clean.items()}
+        part["S0"] = clean["S0"][i:i + 1]
+        check_forward(part, o[None, a:e], SF[i:i + 1], f"sequence {i}")
+
+
 def test_packed_prefill_clamps_a_bad_table():
     """Offsets out of range or out of order: some result, every access inside the arrays."""
     d = inputs((100,), 1, 2, torch.bfloat16, 82, states=4)
