@@ -492,14 +492,15 @@ def gdn_chunk_fwd_pipelined(q, k, v, alpha, beta, S0, o, S_final, chain_ctas=0,
 
 
 def _workspace(workspace, nbytes, dev, stream):
-    """The caller's workspace checked, or one for this call, kept by the allocator until the
-    work on ``stream`` is done."""
+    """The caller's workspace checked, or one for this call: memory of ``stream``, which the
+    allocator hands out again in that stream's order only."""
     if workspace is None:
         if nbytes == 0:
             return None
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        if stream is not None:
-            workspace.record_stream(stream)
+        if stream is None:
+            return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        with torch.cuda.stream(stream):
+            return torch.empty(nbytes, dtype=torch.uint8, device=dev)
     elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise GdnError("workspace must be a contiguous uint8 tensor on the inputs' device")
     return workspace

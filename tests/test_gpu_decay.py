@@ -350,6 +350,26 @@ def test_allocated_workspace_outlives_the_call_on_a_side_stream():
     assert torch.equal(o, want[0]) and torch.equal(SF, want[1])
 
 
+def test_allocated_workspace_is_not_memory_of_another_streams_work():
+    """Fills of a freed block still run on the default stream while the call runs on another."""
+    d = inputs((1, 1130), 1, 2, torch.bfloat16, 211)
+    want = forward(d)
+    x = dev(d)
+    s = torch.cuda.Stream()
+    size = binding.decay_fwd_workspace_bytes(1, 1130, 2, torch.bfloat16)
+    o, SF = torch.empty_like(x["v"]), torch.empty_like(x["S0"])
+    torch.cuda.synchronize()
+    for _ in range(10):
+        block = torch.empty(size, dtype=torch.uint8, device=DEV)
+        torch.cuda._sleep(3_500_000)                     # so that the fills are queued up
+        for _ in range(800):
+            block.fill_(255)
+        del block
+        binding.gdn_decay_fwd(x["q"], x["k"], x["v"], x["decay"], x["S0"], o, SF, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(SF, want[1])
+
+
 # ------------------------------------------------------------------ decode
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
