@@ -463,6 +463,7 @@ gdn_status gdn_bwd_chunk(const void *q, const void *k, const void *v, const floa
  * caller; contents on entry do not matter; calls sharing it must not overlap.
  * Too small or misaligned: GDN_ERR_INVALID_ARG.
  * Sizes: as gdn_chunk_fwd (B <= 65535, dk == dv == 128, Hv % Hqk == 0).
+ * GDN_ERR_UNSUPPORTED also where the tensor-map encoder is missing (GDN_BF16).
  * Repeated calls return the same bits.
  */
 size_t gdn_decay_fwd_workspace(int B, int T, int Hv, int dk, int dv, gdn_dtype dtype);

@@ -41,28 +41,7 @@ struct SimtSmem {
     float2 step[2];                          // lambda^L as two floats: full chunks, the sequence's last
 };
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T *p);
-template <> __device__ __forceinline__ float4 load4<float>(const float *p) {
-    return *reinterpret_cast<const float4 *>(p);
-}
-template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-}
-
-template <typename T>
-__device__ __forceinline__ void store4(const DecayWalk &w, size_t at, const float (&v)[4]) {
-    if (w.o_f32 || sizeof(T) == 4) {
-        *reinterpret_cast<float4 *>(static_cast<float *>(w.o) + at) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) static_cast<T *>(w.o)[at + e] = from_f32<T>(v[e]);
-    }
-}
-
-template <typename T, int DZ>
+template <int DZ>
 __global__ void __launch_bounds__(kSimtThreads)
 decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
 {
@@ -120,7 +99,8 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
     }
     __syncthreads();
 
-    const T *x = static_cast<const T *>(w.x), *y = static_cast<const T *>(w.y), *z = static_cast<const T *>(w.z);
+    const float *x = static_cast<const float *>(w.x), *y = static_cast<const float *>(w.y), *z = static_cast<const float *>(w.z);
+    float *o = static_cast<float *>(w.o);
     const int xh = h / (w.Hv / w.hx), yh = h / (w.Hv / w.hy), zh = h / (w.Hv / w.hz);
     const int ti = tid >> 4, tj = tid & 15;      // 16 x 16 threads
     // a chunk's rows: 8 float4 of x and of y and DZ / 16 of z per thread, zeros past the end
@@ -135,14 +115,14 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
             const int r = (tid >> 5) + 8 * m, d = (tid & 31) * 4;
             px[m] = py[m] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < L) {
-                if (!state_only) px[m] = load4(x + ((tok + r) * w.hx + xh) * kHeadDim + d);
-                py[m] = load4(y + ((tok + r) * w.hy + yh) * kHeadDim + d);
+                if (!state_only) px[m] = *reinterpret_cast<const float4 *>(x + ((tok + r) * w.hx + xh) * kHeadDim + d);
+                py[m] = *reinterpret_cast<const float4 *>(y + ((tok + r) * w.hy + yh) * kHeadDim + d);
             }
         }
 #pragma unroll
         for (int m = 0; m < kZ4; ++m) {
             const int i = tid + m * kSimtThreads, r = i / (DZ / 4), d = (i % (DZ / 4)) * 4;
-            pz[m] = r < L ? load4(z + ((tok + r) * w.hz + zh) * kHeadDim + z0 + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+            pz[m] = r < L ? *reinterpret_cast<const float4 *>(z + ((tok + r) * w.hz + zh) * kHeadDim + z0 + d) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
     };
     if (DZ == 128 && sp.c0 < sp.c1) fetch(sp.c0);
@@ -237,7 +217,9 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
             }
 #pragma unroll
             for (int a = 0; a < 8; ++a)
-                if (8 * r + a < L) store4<T>(w, ((tok + 8 * r + a) * w.Hv + h) * kHeadDim + cc, acc[a]);
+                if (8 * r + a < L)
+                    *reinterpret_cast<float4 *>(o + ((tok + 8 * r + a) * w.Hv + h) * kHeadDim + cc) =
+                        make_float4(acc[a][0], acc[a][1], acc[a][2], acc[a][3]);
             } else {
             // ---- o: rows 4 r .., four columns; the two halves of the block take half of d and of j
             const int part = tid >> 7, r = (tid & 127) >> 3, cc = (tid & 7) * 4;
@@ -289,8 +271,8 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
                     const int i = 4 * r + a;
                     if (i >= L) continue;
                     const float4 o4 = *reinterpret_cast<const float4 *>(half + 4 * a);
-                    const float v[4] = {acc[a][0] + o4.x, acc[a][1] + o4.y, acc[a][2] + o4.z, acc[a][3] + o4.w};
-                    store4<T>(w, ((tok + i) * w.Hv + h) * kHeadDim + z0 + cc, v);
+                    *reinterpret_cast<float4 *>(o + ((tok + i) * w.Hv + h) * kHeadDim + z0 + cc) =
+                        make_float4(acc[a][0] + o4.x, acc[a][1] + o4.y, acc[a][2] + o4.z, acc[a][3] + o4.w);
                 }
             }
             }
@@ -346,20 +328,20 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
         }
 }
 
-template <typename T, int DZ>
-cudaError_t launch_typed(const DecayWalks &d, cudaStream_t stream)
+template <int DZ>
+cudaError_t launch_form(const DecayWalks &d, cudaStream_t stream)
 {
     const int smem = (int)sizeof(SimtSmem<DZ>);
-    cudaError_t err = cudaFuncSetAttribute(decay_walk_kernel<T, DZ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t err = cudaFuncSetAttribute(decay_walk_kernel<DZ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     const DecayWalk &w = d.w[0];
     const dim3 grid((unsigned)w.Hv * (kHeadDim / DZ), (unsigned)(w.B * w.nseg), (unsigned)d.n);
     if (w.nseg > 1) {
-        decay_walk_kernel<T, DZ><<<grid, kSimtThreads, smem, stream>>>(d, true);
+        decay_walk_kernel<DZ><<<grid, kSimtThreads, smem, stream>>>(d, true);
         if ((err = cudaGetLastError()) != cudaSuccess) return err;
-        return launch_after(decay_walk_kernel<T, DZ>, grid, kSimtThreads, smem, stream, d, false);
+        return launch_after(decay_walk_kernel<DZ>, grid, kSimtThreads, smem, stream, d, false);
     }
-    decay_walk_kernel<T, DZ><<<grid, kSimtThreads, smem, stream>>>(d, false);
+    decay_walk_kernel<DZ><<<grid, kSimtThreads, smem, stream>>>(d, false);
     return cudaGetLastError();
 }
 
@@ -392,10 +374,9 @@ head_sum_kernel(const float *__restrict__ part_a, const float *__restrict__ part
 
 }  // namespace
 
-cudaError_t launch_decay_walks_simt(const DecayWalks &d, gdn_dtype dtype, cudaStream_t stream)
+cudaError_t launch_decay_walks_simt(const DecayWalks &d, cudaStream_t stream)
 {
-    if (d.wide) return dtype == GDN_BF16 ? launch_typed<__nv_bfloat16, 128>(d, stream) : launch_typed<float, 128>(d, stream);
-    return dtype == GDN_BF16 ? launch_typed<__nv_bfloat16, 32>(d, stream) : launch_typed<float, 32>(d, stream);
+    return d.wide ? launch_form<128>(d, stream) : launch_form<32>(d, stream);
 }
 
 cudaError_t launch_head_sums(const float *part_a, const float *part_b, void *out_a, void *out_b, long long rows,

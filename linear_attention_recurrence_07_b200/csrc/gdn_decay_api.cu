@@ -67,10 +67,11 @@ size_t segment_bytes(const DecayWalk &w)
     return w.nseg > 1 ? (size_t)w.B * w.nseg * w.Hv * kStateBytes : 0;
 }
 
-cudaError_t launch_walks(const gdn::DecayWalks &d, gdn_dtype dtype, cudaStream_t s)
+gdn_status run_walks(const gdn::DecayWalks &d, gdn_dtype dtype, cudaStream_t s)
 {
-    if (dtype == GDN_BF16 && gdn::chunk_tc_available()) return gdn::launch_decay_walks_tc(d, s);
-    return gdn::launch_decay_walks_simt(d, dtype, s);
+    if (dtype == GDN_F32) return launch_status(gdn::launch_decay_walks_simt(d, s));
+    if (!gdn::chunk_tc_available()) return GDN_ERR_UNSUPPORTED;
+    return launch_status(gdn::launch_decay_walks_tc(d, s));
 }
 
 // T == 0: the state passes through.
@@ -121,7 +122,7 @@ gdn_status fwd_common(const void *q, const void *k, const void *v, const float *
         }
     }
     d.wide = wide_walk(w, 1);
-    return launch_status(launch_walks(d, dtype, s));
+    return run_walks(d, dtype, s);
 }
 
 gdn_status check_token_op(int B, int Hqk, int Hv, int dk, int dv, gdn_dtype dtype, long long ctas_per_head)
@@ -300,9 +301,9 @@ gdn_status gdn_decay_bwd(const void *q, const void *k, const void *v, const floa
     wv.init = dS_final;
     wv.fin = dS0;
     wv.o = dv;
-    cudaError_t err = launch_walks(d, dtype, s);
-    if (err == cudaSuccess && shared) err = gdn::launch_head_sums(rows_q, rows_k, dq, dk, tokens, Hqk, Hv, dtype, s);
-    return launch_status(err);
+    st = run_walks(d, dtype, s);
+    if (st != GDN_OK || !shared) return st;
+    return launch_status(gdn::launch_head_sums(rows_q, rows_k, dq, dk, tokens, Hqk, Hv, dtype, s));
 }
 
 gdn_status gdn_decode_tree(const void *q, const void *k, const void *v, const float *alpha, const float *beta,

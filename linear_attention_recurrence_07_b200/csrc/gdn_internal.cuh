@@ -110,7 +110,7 @@ struct DecayWalks {
     int n;
     bool wide;      // CUDA cores: one CTA per head instead of four
 };
-cudaError_t launch_decay_walks_simt(const DecayWalks &d, gdn_dtype dtype, cudaStream_t stream);
+cudaError_t launch_decay_walks_simt(const DecayWalks &d, cudaStream_t stream);
 cudaError_t launch_decay_walks_tc(const DecayWalks &d, cudaStream_t stream);   // bf16 operands
 cudaError_t decay_tc_take_error(unsigned *out);
 // out_a, out_b [rows, Hqk, 128] = sums over each QK head's V heads of part_a, part_b [rows, Hv, 128]

@@ -256,13 +256,9 @@ __device__ __forceinline__ void tmem_ld16x256b_x1(uint32_t taddr, uint32_t *r) {
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr));
 }
-// 16 lanes x 128 bits, two (four) times along the columns (8, 16 columns), stored: thread t of the
-// warp gives, for k = 0, 1 (.. 3), r[2k] = lane (base + t/4), column col + 4k + t%4, and r[2k+1] = the same
+// 16 lanes x 128 bits, four times along the columns (16 columns), stored: thread t of the
+// warp gives, for k = 0 .. 3, r[2k] = lane (base + t/4), column col + 4k + t%4, and r[2k+1] = the same
 // column of lane (base + 8 + t/4): pairs as ldmatrix.trans delivers them.
-__device__ __forceinline__ void tmem_st16x128b_x2(uint32_t taddr, const uint32_t *r) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};"
-                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
-}
 __device__ __forceinline__ void tmem_st16x128b_x4(uint32_t taddr, const uint32_t *r) {
     asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
                  ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
