@@ -89,13 +89,15 @@ struct TreeSmem {
         struct { float U[N][kLdS], QS[N][kLdS]; } r;     // after the products with S
     };
     __nv_bfloat16 kq[kPlanes][2][N][kLdK];               // k rows, q rows
-    float A[N][N + 4], P[N][N + 4];                      // [node][level of its ancestor]
+    // [node][level of its ancestor], rows of 1, 2, .. N entries (a third CTA per SM at N = 48)
+    static constexpr int kTri = N * (N + 1) / 2;
+    float A[kTri], P[kTri];
     double b[N];                                         // log2 of root_i
     float2 b2[N];                                        // the same as a sum of two floats
     unsigned long long mask[N];                          // path(i), bit j; 0 for padding
     float beta[N], root[N];
     int jump[N];
-    unsigned char list[N][N];                            // path(i) in node order: [node][level]
+    unsigned char list[(kTri + 3) / 4 * 4];              // path(i) in node order: [node][level]
     unsigned char len[N];
     int levels;
 };
@@ -227,7 +229,7 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
         most = __reduce_max_sync(0xffffffffu, most);
         if (lane == 0) sm.levels = most;
     } else {
-        for (int i = tid - 32; i < N * N / 4; i += kTreeThreads - 32) reinterpret_cast<uint32_t *>(&sm.list[0][0])[i] = 0u;
+        for (int i = tid - 32; i < (int)sizeof(sm.list) / 4; i += kTreeThreads - 32) reinterpret_cast<uint32_t *>(sm.list)[i] = 0u;
         if constexpr (kPlanes > 1) {
             for (int i = tid - 32; i < 2 * N * (kHeadDim / 4); i += kTreeThreads - 32) {
                 const int which = i / (N * (kHeadDim / 4)), r = (i / (kHeadDim / 4)) % N, d = (i % (kHeadDim / 4)) * 4;
@@ -279,13 +281,13 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
                     const unsigned long long m = sm.mask[i];
                     const float2 bi = sm.b2[i], bj = sm.b2[j];
                     const float x = exp2f((bi.x - bj.x) + (bi.y - bj.y)) * (acc[0][e] + acc[1][e]);
-                    const int at = __popcll(m & ((1ull << j) - 1ull));
+                    const int at = i * (i + 1) / 2 + __popcll(m & ((1ull << j) - 1ull));
                     if ((m >> j) & 1ull) {
                         if (gr == 0) {
-                            if (j < i) sm.A[i][at] = sm.beta[i] * x;
+                            if (j < i) sm.A[at] = sm.beta[i] * x;
                         } else {
-                            sm.P[i][at] = x;
-                            sm.list[i][at] = (unsigned char)j;
+                            sm.P[at] = x;
+                            sm.list[at] = (unsigned char)j;
                         }
                     }
                 }
@@ -392,13 +394,14 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
 #pragma unroll
         for (int x = 0; x < kOwn; ++x) {
             const int i = warp + W * x;
-            const float2 w = *reinterpret_cast<const float2 *>(&sm.r.U[sm.list[i][L]][2 * lane]);
-            const float p = sm.P[i][L];
+            const int at = i * (i + 1) / 2 + L;              // in the arrays for every L < N, a row's or not
+            const float2 w = *reinterpret_cast<const float2 *>(&sm.r.U[sm.list[at]][2 * lane]);
+            const float p = sm.P[at];
             const bool on = len[x] > L;
             out[x].x = on ? fmaf(p, w.x, out[x].x) : out[x].x;
             out[x].y = on ? fmaf(p, w.y, out[x].y) : out[x].y;
             if (DELTA) {
-                const float a = sm.A[i][L];
+                const float a = sm.A[at];
                 const bool deeper = len[x] > L + 1;
                 u[x].x = deeper ? fmaf(-a, w.x, u[x].x) : u[x].x;
                 u[x].y = deeper ? fmaf(-a, w.y, u[x].y) : u[x].y;
