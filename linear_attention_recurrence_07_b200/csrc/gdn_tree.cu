@@ -36,7 +36,10 @@ using namespace sm100;
 
 constexpr int kTreeCols = 64;            // columns of the state per CTA
 constexpr int kTreeSlices = kHeadDim / kTreeCols;
-constexpr int kLdS = kTreeCols + 4;      // floats per row of S, U, QS in shared memory
+// Columns of S, and of U and QS, in shared memory: no padding (room for one more CTA per SM with
+// up to 32 nodes), blocks of 8 and of 16 exchanged by row so that a fragment's rows meet other banks.
+__device__ __forceinline__ int s_col(int row, int c) { return c ^ (((row >> 1) & 3) << 3); }
+__device__ __forceinline__ int r_col(int row, int c) { return c ^ ((row & 1) << 4); }
 constexpr int kLdK = kHeadDim + 8;       // bf16 per row of K and Q
 constexpr float kLog2Clamp = -87.0f * 1.4426950408889634f;
 
@@ -85,8 +88,8 @@ template <typename T, int N>
 struct TreeSmem {
     static constexpr int kPlanes = TreeTypes<T>::kPlanes;
     union {
-        float S[kHeadDim][kLdS];
-        struct { float U[N][kLdS], QS[N][kLdS]; } r;     // after the products with S
+        float S[kHeadDim][kTreeCols];
+        struct { float U[N][kTreeCols], QS[N][kTreeCols]; } r;     // after the products with S
     };
     __nv_bfloat16 kq[kPlanes][2][N][kLdK];               // k rows, q rows
     // [node][level of its ancestor], rows of 1, 2, .. N entries (a third CTA per SM at N = 48)
@@ -156,7 +159,7 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
 #pragma unroll
     for (int m = 0; m < 2048 / kTreeThreads; ++m) {
         const int row = (tid >> 4) + (kTreeThreads / 16) * m, c = (tid & 15) * 4;
-        cp_async16(&sm.S[row][c], S + row * kHeadDim + c);
+        cp_async16(&sm.S[row][s_col(row, c)], S + row * kHeadDim + c);
     }
     // warps by columns of S, and with eight of them by row set (0: k, 1: q)
     constexpr int RW = W == 8 ? 1 : 2;                   // row sets per warp
@@ -310,9 +313,9 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
     if (DELTA || W == 4 || role == 1)
 #pragma unroll 1
     for (int ks = 0; ks < kHeadDim / 16; ++ks) {
-        const float *sr = &sm.S[ks * 16 + 2 * t][cw + 2 * g];
-        float2 s0 = *reinterpret_cast<const float2 *>(sr), s1 = *reinterpret_cast<const float2 *>(sr + kLdS);
-        float2 s2 = *reinterpret_cast<const float2 *>(sr + 8 * kLdS), s3 = *reinterpret_cast<const float2 *>(sr + 9 * kLdS);
+        const float *sr = &sm.S[ks * 16 + 2 * t][s_col(2 * t, cw + 2 * g)];      // rows 2t + 1, + 8, + 9 alike
+        float2 s0 = *reinterpret_cast<const float2 *>(sr), s1 = *reinterpret_cast<const float2 *>(sr + kTreeCols);
+        float2 s2 = *reinterpret_cast<const float2 *>(sr + 8 * kTreeCols), s3 = *reinterpret_cast<const float2 *>(sr + 9 * kTreeCols);
         uint32_t bp[kPieces][2][2];
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
@@ -361,11 +364,11 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     x[e] = DELTA ? be_i * (vv[mt][half][e] - f * acc[0][mt][e & 1][2 * half + (e >> 1)]) : vv[mt][half][e];
-                *reinterpret_cast<float4 *>(&sm.r.U[i][c]) = make_float4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<float4 *>(&sm.r.U[i][r_col(i, c)]) = make_float4(x[0], x[1], x[2], x[3]);
             }
             if (W == 4 || role == 1) {
                 const float(&y)[2][4] = acc[RW - 1][mt];
-                *reinterpret_cast<float4 *>(&sm.r.QS[i][c]) = make_float4(y[0][2 * half], y[1][2 * half], y[0][2 * half + 1], y[1][2 * half + 1]);
+                *reinterpret_cast<float4 *>(&sm.r.QS[i][r_col(i, c)]) = make_float4(y[0][2 * half], y[1][2 * half], y[0][2 * half + 1], y[1][2 * half + 1]);
             }
         }
     __syncthreads();
@@ -377,9 +380,9 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
     for (int x = 0; x < kOwn; ++x) {
         const int i = warp + W * x;
         len[x] = sm.len[i];
-        const float2 r = *reinterpret_cast<const float2 *>(&sm.r.QS[i][2 * lane]);
+        const float2 r = *reinterpret_cast<const float2 *>(&sm.r.QS[i][r_col(i, 2 * lane)]);
         out[x] = make_float2(sm.root[i] * r.x, sm.root[i] * r.y);
-        u[x] = *reinterpret_cast<const float2 *>(&sm.r.U[i][2 * lane]);
+        u[x] = *reinterpret_cast<const float2 *>(&sm.r.U[i][r_col(i, 2 * lane)]);
     }
     const int levels = sm.levels;
 #pragma unroll 1
@@ -387,7 +390,7 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
         if (DELTA && L > 0) {                            // the nodes of this level are finished
 #pragma unroll
             for (int x = 0; x < kOwn; ++x)
-                if (len[x] == L + 1) *reinterpret_cast<float2 *>(&sm.r.U[warp + W * x][2 * lane]) = u[x];
+                if (len[x] == L + 1) *reinterpret_cast<float2 *>(&sm.r.U[warp + W * x][r_col(warp + W * x, 2 * lane)]) = u[x];
             __syncthreads();
         }
         // selected, not branched over, so that all rows are on their way at once
@@ -395,7 +398,8 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
         for (int x = 0; x < kOwn; ++x) {
             const int i = warp + W * x;
             const int at = i * (i + 1) / 2 + L;              // in the arrays for every L < N, a row's or not
-            const float2 w = *reinterpret_cast<const float2 *>(&sm.r.U[sm.list[at]][2 * lane]);
+            const int j = sm.list[at];
+            const float2 w = *reinterpret_cast<const float2 *>(&sm.r.U[j][r_col(j, 2 * lane)]);
             const float p = sm.P[at];
             const bool on = len[x] > L;
             out[x].x = on ? fmaf(p, w.x, out[x].x) : out[x].x;
