@@ -108,8 +108,13 @@ struct TreeSmem {
 // Warps per CTA: four for small trees (of which more CTAs fit on an SM), eight for large ones.
 template <int N> struct TreeWarps { static constexpr int kWarps = N <= 16 ? 4 : 8; };
 
+// CTAs per SM that shared memory (227 KB) allows: registers are held to that.
+template <typename T, int N> constexpr int tree_ctas() { return 227 * 1024 / ((int)sizeof(TreeSmem<T, N>) + 1024); }
+static_assert(tree_ctas<__nv_bfloat16, 16>() == 5 && tree_ctas<__nv_bfloat16, 32>() == 4 &&
+              tree_ctas<__nv_bfloat16, 48>() == 3 && tree_ctas<__nv_bfloat16, 64>() == 2, "CTAs per SM");
+
 template <typename T, bool DELTA, int N>
-__global__ void __launch_bounds__(TreeWarps<N>::kWarps * 32)
+__global__ void __launch_bounds__(TreeWarps<N>::kWarps * 32, tree_ctas<T, N>())
 tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
             const float *__restrict__ alpha, const float *__restrict__ beta, const float *__restrict__ decay,
             const int *__restrict__ parents, const float *__restrict__ pool, const int *__restrict__ slots,
