@@ -22,10 +22,10 @@
 // are finished.  A bushy tree costs its depth, not its size; non-ancestors are never read,
 // so that what is not finite stays below its node.
 //
-// Measured, 48 heads: 128 sequences of 8 nodes 128 us (3.2 TB/s, half of the copy bandwidth),
-// 32 of 30 nodes 73 us, 16 of 48 nodes 70 us.  Bound by latency: a CTA's way from the load
-// through the grams, the products and the levels is 6 to 12 us, and shared memory holds two
-// to five CTAs per SM.  Commit, 128 sequences of 7 nodes: 164 us, 4.9 TB/s.
+// Measured, 48 heads: 128 sequences of 8 nodes 108 us (3.9 TB/s, 60% of the copy bandwidth),
+// 32 of 30 nodes 67 us, 16 of 48 nodes 60 us.  Shared memory holds five (16 nodes) to two (64)
+// CTAs per SM.  Small trees are bound by the way of a CTA from the load to the levels; large ones
+// by instructions (24 thousand per CTA of 48 nodes, two thirds of the issue slots).  Commit, 128 sequences of 7 nodes: 164 us, 4.9 TB/s.
 #include "gdn_internal.cuh"
 #include "sm100.cuh"
 
@@ -284,18 +284,27 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
                             mma16816(acc[ks & 1], a, kb[sum - pa][ks][0], kb[sum - pa][ks][1]);
                         }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = mt * 16 + g + (e >> 1) * 8, j = nt * 8 + 2 * t + (e & 1);
+                for (int half = 0; half < 2; ++half) {
+                    const int i = mt * 16 + g + half * 8, j0 = nt * 8 + 2 * t;
                     const unsigned long long m = sm.mask[i];
-                    const float2 bi = sm.b2[i], bj = sm.b2[j];
-                    const float x = exp2f((bi.x - bj.x) + (bi.y - bj.y)) * (acc[0][e] + acc[1][e]);
-                    const int at = i * (i + 1) / 2 + __popcll(m & ((1ull << j) - 1ull));
-                    if ((m >> j) & 1ull) {
-                        if (gr == 0) {
-                            if (j < i) sm.A[at] = sm.beta[i] * x;
-                        } else {
-                            sm.P[at] = x;
-                            sm.list[at] = (unsigned char)j;
+                    const uint32_t lo = (uint32_t)m, hi = (uint32_t)(m >> 32);
+                    // path bits below j0, and of j0 and j0 + 1 (of the same word: j0 is even)
+                    const uint32_t word = j0 < 32 ? lo : hi, bits = word >> (j0 & 31);
+                    int at = i * (i + 1) / 2 + __popc(word & ((1u << (j0 & 31)) - 1u)) + (j0 < 32 ? 0 : __popc(lo));
+                    const float2 bi = sm.b2[i];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if ((bits >> e) & 1u) {
+                            const int j = j0 + e;
+                            const float2 bj = sm.b2[j];
+                            const float x = exp2f((bi.x - bj.x) + (bi.y - bj.y)) * (acc[0][2 * half + e] + acc[1][2 * half + e]);
+                            if (gr == 0) {
+                                if (j < i) sm.A[at] = sm.beta[i] * x;
+                            } else {
+                                sm.P[at] = x;
+                                sm.list[at] = (unsigned char)j;
+                            }
+                            ++at;
                         }
                     }
                 }
@@ -398,7 +407,7 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
                 if (len[x] == L + 1) *reinterpret_cast<float2 *>(&sm.r.U[warp + W * x][r_col(warp + W * x, 2 * lane)]) = u[x];
             __syncthreads();
         }
-        // selected, not branched over, so that all rows are on their way at once
+        // loads outside the conditions, so that all rows are on their way at once
 #pragma unroll
         for (int x = 0; x < kOwn; ++x) {
             const int i = warp + W * x;
@@ -407,13 +416,11 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
             const float2 w = *reinterpret_cast<const float2 *>(&sm.r.U[j][r_col(j, 2 * lane)]);
             const float p = sm.P[at];
             const bool on = len[x] > L;
-            out[x].x = on ? fmaf(p, w.x, out[x].x) : out[x].x;
-            out[x].y = on ? fmaf(p, w.y, out[x].y) : out[x].y;
+            if (on) { out[x].x = fmaf(p, w.x, out[x].x); out[x].y = fmaf(p, w.y, out[x].y); }
             if (DELTA) {
                 const float a = sm.A[at];
                 const bool deeper = len[x] > L + 1;
-                u[x].x = deeper ? fmaf(-a, w.x, u[x].x) : u[x].x;
-                u[x].y = deeper ? fmaf(-a, w.y, u[x].y) : u[x].y;
+                if (deeper) { u[x].x = fmaf(-a, w.x, u[x].x); u[x].y = fmaf(-a, w.y, u[x].y); }
             }
         }
     }
