@@ -17,9 +17,9 @@
 // Roundings: H and P are rounded to bf16 where they meet X and Z, as every operand of a bf16
 // product: the terms of a row average it out to about the rounding of O itself.  Sequences of
 // one chunk, whose first rows have few terms and no H, get 16 bits of P in two pieces (they
-// are bound by latency, and the pieces share the room of P's second buffer).  Z' has three pieces, all 24 bits, where an end
-// state is wanted, two where the state only feeds O; small pieces are accumulated first,
-// because the tensor core truncates.  lambda^{-p_j}
+// are bound by latency, and the pieces share the room of P's second buffer).  Z' has three
+// pieces, all 24 bits, where an end state is wanted, two where the state only feeds O; small
+// pieces are accumulated first, because the tensor core truncates.  lambda^{-p_j}
 // grows to lambda^{-63}: below lambda = 2^-(100/63) the scale is held at 2^100, which
 // replaces a factor lambda^p < 2^-100 on H's share of a row by 2^-100.
 //
@@ -31,12 +31,15 @@
 //   warps 12-15 G -> P (shared memory)
 //   warps 16-19 O epilogue (stmatrix, TMA store)
 //
-// Measured: 16 QK / 48 V heads, B=8, T=8192: 0.66-0.69 ms, 3.2 TB/s (50% of the copy
-// bandwidth), 300 TF/s of the recurrence's own arithmetic; B=1, T=4096: 72 us (three
-// segments); gradients at 48 heads, T=4096: 129 us.  A chunk takes about 2400 cycles per SM.
-// What bounds it is the state's two warpgroups (pieces 1100, D 550, H 280 cycles, latency and
-// the half-rate pipe of the bit operations), next the tensor core: 65 cycles per 128 x 128 x 16
-// MMA make 780 for D, 270 for H X, 400 for Z P (Z from shared memory: 50 each), 280 for G.
+// Measured: 16 QK / 48 V heads, B=8, T=8192: 0.65-0.68 ms, 3.3 TB/s (half of the copy
+// bandwidth), 300 TF/s of the recurrence's own arithmetic; B=1, T=4096: 70 us (three
+// segments); gradients at 48 heads, T=4096: 124-131 us.  A chunk takes 2400 to 2700 cycles per
+// SM (the clock settles at 1.65 GHz under this load).  No single unit bounds it: the chain from D
+// through the state's registers to the next D (pieces of Z 1100, reading D 550, H 280 cycles of
+// its two warpgroups, and D itself), the tensor core 57-65% of the time (65 cycles per 128 x 128 x 16
+// MMA make 780 for D; H X 270, Z P 200, G 280), shared memory 70%.  Giving Z' warps of its own,
+// Z' or O a second buffer, or Z P a place before H X was no faster: what runs earlier takes the
+// tensor core from D.
 // What counted on the way: no spills (setmaxnreg; 1.6 times), MMAs issued by an elected lane,
 // and the size of the loops: unrolled roles of 98 KB of code waited for instructions a quarter
 // of the time.

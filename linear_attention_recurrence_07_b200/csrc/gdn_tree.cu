@@ -25,7 +25,8 @@
 // Measured, 48 heads: 128 sequences of 8 nodes 108 us (3.9 TB/s, 60% of the copy bandwidth),
 // 32 of 30 nodes 67 us, 16 of 48 nodes 60 us.  Shared memory holds five (16 nodes) to two (64)
 // CTAs per SM.  Small trees are bound by the way of a CTA from the load to the levels; large ones
-// by instructions (24 thousand per CTA of 48 nodes, two thirds of the issue slots).  Commit, 128 sequences of 7 nodes: 164 us, 4.9 TB/s.
+// by instructions (24 thousand per CTA of 48 nodes, two thirds of the issue slots).
+// Commit, 128 sequences of 7 nodes: 164 us, 4.9 TB/s.
 #include "gdn_internal.cuh"
 #include "sm100.cuh"
 
