@@ -509,9 +509,31 @@ def _workspace(workspace, nbytes, dev, stream):
 def _shape(t, name, dims):
     if t is None:
         raise GdnError(f"{name} is required")
-    if t.dim() != dims:
-        raise GdnError(f"{name}: expected {dims} dimensions, got shape {tuple(t.shape)}")
-    return tuple(t.shape)
+    shape = t.shape
+    if len(shape) != dims:
+        raise GdnError(f"{name}: expected {dims} dimensions, got shape {tuple(shape)}")
+    return shape
+
+
+def _pointers(dev, *expected):
+    """Data pointers of (name, tensor, shape, dtype) entries, each checked as _expect does; a
+    name ending in "?" may be None.  (The checks are most of a small call's time on the host.)"""
+    index, out = dev.index, []
+    for name, t, shape, dtype in expected:
+        if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+            if t is None and name[-1] == "?":
+                out.append(None)
+                continue
+            _expect(t, name.rstrip("?"), shape, dtype, dev)
+        out.append(t.data_ptr())
+    return out
+
+
+def _dtype_code(q):
+    code = _DTYPES.get(q.dtype)
+    if code is None or not q.is_cuda:
+        _expect_cuda(q)
+    return code
 
 
 def decay_fwd_workspace_bytes(B, T, Hv, dtype, dk=128, dv=128):
@@ -534,21 +556,15 @@ def gdn_decay_fwd(q, k, v, decay, S0, o, S_final, workspace=None, stream=None):
     float32; S0, S_final [B, Hv, dk, dv] float32 or None (S_final may be S0).
     ``workspace``: uint8 CUDA tensor of decay_fwd_workspace_bytes(...) bytes; None
     allocates one for this call."""
-    B, T, Hqk, dk = _shape(q, "q", 4)
+    qk = B, T, Hqk, dk = _shape(q, "q", 4)
     _, _, Hv, dv = _shape(v, "v", 4)
-    dev = q.device
-    _expect_cuda(q)
-    for name, t, shape, dt in (("q", q, q.shape, q.dtype), ("k", k, q.shape, q.dtype),
-                               ("v", v, (B, T, Hv, dv), q.dtype), ("o", o, (B, T, Hv, dv), q.dtype),
-                               ("decay", decay, (Hv,), torch.float32)):
-        _expect(t, name, shape, dt, dev)
-    for name, t in (("S0", S0), ("S_final", S_final)):
-        if t is not None:
-            _expect(t, name, (B, Hv, dk, dv), torch.float32, dev)
-    need = _call(dev, library().gdn_decay_fwd_workspace, B, T, Hv, dk, dv, _DTYPES[q.dtype])
+    dev, dt, code = q.device, q.dtype, _dtype_code(q)
+    rows, state = (B, T, Hv, dv), (B, Hv, dk, dv)
+    ptrs = _pointers(dev, ("q", q, qk, dt), ("k", k, qk, dt), ("v", v, rows, dt), ("decay", decay, (Hv,), torch.float32),
+                     ("S0?", S0, state, torch.float32), ("o", o, rows, dt), ("S_final?", S_final, state, torch.float32))
+    need = _call(dev, library().gdn_decay_fwd_workspace, B, T, Hv, dk, dv, code)
     workspace = _workspace(workspace, need, dev, stream)
-    _check(_call(dev, library().gdn_decay_fwd, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0), _ptr(o),
-                 _ptr(S_final), B, T, Hqk, Hv, dk, dv, _DTYPES[q.dtype], _ptr(workspace),
+    _check(_call(dev, library().gdn_decay_fwd, *ptrs, B, T, Hqk, Hv, dk, dv, code, _ptr(workspace),
                  0 if workspace is None else workspace.numel(), _stream_handle(stream, dev)),
            "gdn_decay_fwd")
 
@@ -557,24 +573,17 @@ def gdn_decay_fwd_varlen(q, k, v, decay, S0, o, S_final, cu_seqlens, stream=None
     """gdn_decay_fwd of N packed sequences (C entry point ``gdn_decay_fwd_varlen``).
     q, k [T_total, Hqk, dk]; v, o [T_total, Hv, dv]; decay [Hv]; cu_seqlens [N + 1]
     int32; S0, S_final [N, Hv, dk, dv] float32 or None."""
-    T, Hqk, dk = _shape(q, "q", 3)
+    qk = T, Hqk, dk = _shape(q, "q", 3)
     _, Hv, dv = _shape(v, "v", 3)
     N = _shape(cu_seqlens, "cu_seqlens", 1)[0] - 1
     if N < 0:
         raise GdnError("cu_seqlens: at least one entry is required")
-    dev = q.device
-    _expect_cuda(q)
-    for name, t, shape, dt in (("q", q, q.shape, q.dtype), ("k", k, q.shape, q.dtype),
-                               ("v", v, (T, Hv, dv), q.dtype), ("o", o, (T, Hv, dv), q.dtype),
-                               ("decay", decay, (Hv,), torch.float32),
-                               ("cu_seqlens", cu_seqlens, (N + 1,), torch.int32)):
-        _expect(t, name, shape, dt, dev)
-    for name, t in (("S0", S0), ("S_final", S_final)):
-        if t is not None:
-            _expect(t, name, (N, Hv, dk, dv), torch.float32, dev)
-    _check(_call(dev, library().gdn_decay_fwd_varlen, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0),
-                 _ptr(o), _ptr(S_final), _ptr(cu_seqlens), N, T, Hqk, Hv, dk, dv, _DTYPES[q.dtype],
-                 _stream_handle(stream, dev)),
+    dev, dt, code = q.device, q.dtype, _dtype_code(q)
+    rows, state = (T, Hv, dv), (N, Hv, dk, dv)
+    ptrs = _pointers(dev, ("q", q, qk, dt), ("k", k, qk, dt), ("v", v, rows, dt), ("decay", decay, (Hv,), torch.float32),
+                     ("S0?", S0, state, torch.float32), ("o", o, rows, dt), ("S_final?", S_final, state, torch.float32),
+                     ("cu_seqlens", cu_seqlens, (N + 1,), torch.int32))
+    _check(_call(dev, library().gdn_decay_fwd_varlen, *ptrs, N, T, Hqk, Hv, dk, dv, code, _stream_handle(stream, dev)),
            "gdn_decay_fwd_varlen")
 
 
@@ -582,17 +591,13 @@ def gdn_decay_decode_step(q, k, v, decay, S, o, S_new, stream=None):
     """One decode token with a constant decay per head (C entry point
     ``gdn_decay_decode_step``); writes o and S_new (which may be S).  q, k
     [B, Hqk, dk]; v, o [B, Hv, dv]; decay [Hv]; S, S_new [B, Hv, dk, dv] float32."""
-    B, Hqk, dk = _shape(q, "q", 3)
+    qk = B, Hqk, dk = _shape(q, "q", 3)
     _, Hv, dv = _shape(v, "v", 3)
-    dev = q.device
-    _expect_cuda(q)
-    for name, t, shape, dt in (("q", q, q.shape, q.dtype), ("k", k, q.shape, q.dtype), ("v", v, (B, Hv, dv), q.dtype),
-                               ("o", o, (B, Hv, dv), q.dtype), ("decay", decay, (Hv,), torch.float32),
-                               ("S", S, (B, Hv, dk, dv), torch.float32),
-                               ("S_new", S_new, (B, Hv, dk, dv), torch.float32)):
-        _expect(t, name, shape, dt, dev)
-    _check(_call(dev, library().gdn_decay_decode_step, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S), _ptr(o),
-                 _ptr(S_new), B, Hqk, Hv, dk, dv, _DTYPES[q.dtype], _stream_handle(stream, dev)),
+    dev, dt, code = q.device, q.dtype, _dtype_code(q)
+    rows, state = (B, Hv, dv), (B, Hv, dk, dv)
+    ptrs = _pointers(dev, ("q", q, qk, dt), ("k", k, qk, dt), ("v", v, rows, dt), ("decay", decay, (Hv,), torch.float32),
+                     ("S", S, state, torch.float32), ("o", o, rows, dt), ("S_new", S_new, state, torch.float32))
+    _check(_call(dev, library().gdn_decay_decode_step, *ptrs, B, Hqk, Hv, dk, dv, code, _stream_handle(stream, dev)),
            "gdn_decay_decode_step")
 
 
@@ -600,18 +605,15 @@ def gdn_decay_decode_step_slots(q, k, v, decay, state_pool, slots, o, stream=Non
     """gdn_decay_decode_step with states in a pool, updated in place (C entry point
     ``gdn_decay_decode_step_slots``): state_pool [n_slots, Hv, dk, dv] float32;
     slots [B] int32, out of range = padding."""
-    B, Hqk, dk = _shape(q, "q", 3)
+    qk = B, Hqk, dk = _shape(q, "q", 3)
     _, Hv, dv = _shape(v, "v", 3)
     n_slots = _shape(state_pool, "state_pool", 4)[0]
-    dev = q.device
-    _expect_cuda(q)
-    for name, t, shape, dt in (("q", q, q.shape, q.dtype), ("k", k, q.shape, q.dtype), ("v", v, (B, Hv, dv), q.dtype),
-                               ("o", o, (B, Hv, dv), q.dtype), ("decay", decay, (Hv,), torch.float32),
-                               ("state_pool", state_pool, (n_slots, Hv, dk, dv), torch.float32),
-                               ("slots", slots, (B,), torch.int32)):
-        _expect(t, name, shape, dt, dev)
-    _check(_call(dev, library().gdn_decay_decode_step_slots, _ptr(q), _ptr(k), _ptr(v), _ptr(decay),
-                 _ptr(state_pool), _ptr(slots), _ptr(o), B, n_slots, Hqk, Hv, dk, dv, _DTYPES[q.dtype],
+    dev, dt, code = q.device, q.dtype, _dtype_code(q)
+    rows = (B, Hv, dv)
+    ptrs = _pointers(dev, ("q", q, qk, dt), ("k", k, qk, dt), ("v", v, rows, dt), ("decay", decay, (Hv,), torch.float32),
+                     ("state_pool", state_pool, (n_slots, Hv, dk, dv), torch.float32),
+                     ("slots", slots, (B,), torch.int32), ("o", o, rows, dt))
+    _check(_call(dev, library().gdn_decay_decode_step_slots, *ptrs, B, n_slots, Hqk, Hv, dk, dv, code,
                  _stream_handle(stream, dev)),
            "gdn_decay_decode_step_slots")
 
@@ -622,45 +624,41 @@ def gdn_decay_bwd(q, k, v, decay, S0, dO, dS_final, dq, dk, dv, dS0, workspace=N
     dS_final float32 or None.  Outputs (overwritten): dq, dk, dv like q, k, v, in their
     dtype; dS0 [B, Hv, dk, dv] float32 or None.  ``workspace``: uint8 CUDA tensor of
     decay_bwd_workspace_bytes(...) bytes; None allocates one."""
-    B, T, Hqk, dkk = _shape(q, "q", 4)
+    qk = B, T, Hqk, dkk = _shape(q, "q", 4)
     _, _, Hv, dvv = _shape(v, "v", 4)
-    dev = q.device
-    _expect_cuda(q)
-    for name, t, shape, dt in (("q", q, q.shape, q.dtype), ("k", k, q.shape, q.dtype),
-                               ("v", v, (B, T, Hv, dvv), q.dtype), ("dO", dO, (B, T, Hv, dvv), q.dtype),
-                               ("dq", dq, q.shape, q.dtype), ("dk", dk, q.shape, q.dtype),
-                               ("dv", dv, (B, T, Hv, dvv), q.dtype), ("decay", decay, (Hv,), torch.float32)):
-        _expect(t, name, shape, dt, dev)
-    for name, t in (("S0", S0), ("dS_final", dS_final), ("dS0", dS0)):
-        if t is not None:
-            _expect(t, name, (B, Hv, dkk, dvv), torch.float32, dev)
-    need = _call(dev, library().gdn_decay_bwd_workspace, B, T, Hqk, Hv, dkk, dvv, _DTYPES[q.dtype])
+    dev, dt, code = q.device, q.dtype, _dtype_code(q)
+    rows, state = (B, T, Hv, dvv), (B, Hv, dkk, dvv)
+    ptrs = _pointers(dev, ("q", q, qk, dt), ("k", k, qk, dt), ("v", v, rows, dt), ("decay", decay, (Hv,), torch.float32),
+                     ("S0?", S0, state, torch.float32), ("dO", dO, rows, dt),
+                     ("dS_final?", dS_final, state, torch.float32), ("dq", dq, qk, dt), ("dk", dk, qk, dt),
+                     ("dv", dv, rows, dt), ("dS0?", dS0, state, torch.float32))
+    need = _call(dev, library().gdn_decay_bwd_workspace, B, T, Hqk, Hv, dkk, dvv, code)
     workspace = _workspace(workspace, need, dev, stream)
-    _check(_call(dev, library().gdn_decay_bwd, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0), _ptr(dO),
-                 _ptr(dS_final), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dS0), B, T, Hqk, Hv, dkk, dvv,
-                 _DTYPES[q.dtype], _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                 _stream_handle(stream, dev)),
+    _check(_call(dev, library().gdn_decay_bwd, *ptrs, B, T, Hqk, Hv, dkk, dvv, code, _ptr(workspace),
+                 0 if workspace is None else workspace.numel(), _stream_handle(stream, dev)),
            "gdn_decay_bwd")
 
 
-def _tree_sizes(k, v, parents, state_pool, slots, dtype_of):
-    B, n, Hqk, dk = _shape(k, "k", 4)
+def _tree_call(what, q, k, v, gates, parents, accepted, state_pool, slots, o, stream):
+    """The four tree entry points: q and o, or accepted; gates (alpha, beta) or (decay,)."""
+    qk = B, n, Hqk, dk = _shape(k, "k", 4)
     _, _, Hv, dv = _shape(v, "v", 4)
     n_slots = _shape(state_pool, "state_pool", 4)[0]
-    dev = k.device
-    _expect_cuda(k)
-    for name, t, shape, dt in (("k", k, k.shape, dtype_of), ("v", v, (B, n, Hv, dv), dtype_of),
-                               ("parents", parents, (B, n), torch.int32),
-                               ("state_pool", state_pool, (n_slots, Hv, dk, dv), torch.float32)):
-        _expect(t, name, shape, dt, dev)
-    if slots is not None:
-        _expect(slots, "slots", (B,), torch.int32, dev)
-    return B, n, n_slots, Hqk, Hv, dk, dv
-
-
-def _gates(alpha, beta, B, n, Hv, dev):
-    _expect(alpha, "alpha", (B, n, Hv), torch.float32, dev)
-    _expect(beta, "beta", (B, n, Hv), torch.float32, dev)
+    dev, dt, code = k.device, k.dtype, _dtype_code(k)
+    rows = (B, n, Hv, dv)
+    names = ("decay",) if len(gates) == 1 else ("alpha", "beta")
+    gate = (Hv,) if len(gates) == 1 else (B, n, Hv)
+    expected = [] if accepted is not None else [("q", q, qk, dt)]
+    expected += [("k", k, qk, dt), ("v", v, rows, dt)]
+    expected += [(name, t, gate, torch.float32) for name, t in zip(names, gates)]
+    expected.append(("parents", parents, (B, n), torch.int32))
+    if accepted is not None:
+        expected.append(("accepted", accepted, (B,), torch.int32))
+    expected += [("state_pool", state_pool, (n_slots, Hv, dk, dv), torch.float32), ("slots?", slots, (B,), torch.int32)]
+    if accepted is None:
+        expected.append(("o", o, rows, dt))
+    _check(_call(dev, getattr(library(), what), *_pointers(dev, *expected), B, n, n_slots, Hqk, Hv, dk, dv, code,
+                 _stream_handle(stream, dev)), what)
 
 
 def gdn_decode_tree(q, k, v, alpha, beta, parents, state_pool, slots, o, stream=None):
@@ -671,73 +669,46 @@ def gdn_decode_tree(q, k, v, alpha, beta, parents, state_pool, slots, o, stream=
     q, k [B, n, Hqk, dk]; v, o [B, n, Hv, dv]; alpha, beta [B, n, Hv] float32;
     parents [B, n] int32; state_pool [n_slots, Hv, dk, dv] float32 (not changed);
     slots [B] int32 or None (sequence b uses row b).  n <= 64."""
-    B, n, n_slots, Hqk, Hv, dk, dv = _tree_sizes(k, v, parents, state_pool, slots, q.dtype)
-    dev = k.device
-    _expect(q, "q", k.shape, k.dtype, dev)
-    _expect(o, "o", v.shape, v.dtype, dev)
-    _gates(alpha, beta, B, n, Hv, dev)
-    _check(_call(dev, library().gdn_decode_tree, _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(parents),
-                 _ptr(state_pool), _ptr(slots), _ptr(o), B, n, n_slots, Hqk, Hv, dk, dv, _DTYPES[k.dtype],
-                 _stream_handle(stream, dev)),
-           "gdn_decode_tree")
+    _tree_call("gdn_decode_tree", q, k, v, (alpha, beta), parents, None, state_pool, slots, o, stream)
 
 
 def gdn_tree_commit(k, v, alpha, beta, parents, accepted, state_pool, slots, stream=None):
     """Moves state_pool[slots[b]] to the state after node accepted[b] of its tree, in
     place (C entry point ``gdn_tree_commit``); accepted [B] int32, out of range =
     nothing accepted.  Other arguments as gdn_decode_tree."""
-    B, n, n_slots, Hqk, Hv, dk, dv = _tree_sizes(k, v, parents, state_pool, slots, k.dtype)
-    dev = k.device
-    _gates(alpha, beta, B, n, Hv, dev)
-    _expect(accepted, "accepted", (B,), torch.int32, dev)
-    _check(_call(dev, library().gdn_tree_commit, _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(parents),
-                 _ptr(accepted), _ptr(state_pool), _ptr(slots), B, n, n_slots, Hqk, Hv, dk, dv, _DTYPES[k.dtype],
-                 _stream_handle(stream, dev)),
-           "gdn_tree_commit")
+    if accepted is None:
+        raise GdnError("accepted is required")
+    _tree_call("gdn_tree_commit", None, k, v, (alpha, beta), parents, accepted, state_pool, slots, None, stream)
 
 
 def gdn_decay_decode_tree(q, k, v, decay, parents, state_pool, slots, o, stream=None):
     """gdn_decode_tree for the constant-decay rule (C entry point
     ``gdn_decay_decode_tree``): decay [Hv] float32 in place of the gates."""
-    B, n, n_slots, Hqk, Hv, dk, dv = _tree_sizes(k, v, parents, state_pool, slots, q.dtype)
-    dev = k.device
-    _expect(q, "q", k.shape, k.dtype, dev)
-    _expect(o, "o", v.shape, v.dtype, dev)
-    _expect(decay, "decay", (Hv,), torch.float32, dev)
-    _check(_call(dev, library().gdn_decay_decode_tree, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(parents),
-                 _ptr(state_pool), _ptr(slots), _ptr(o), B, n, n_slots, Hqk, Hv, dk, dv, _DTYPES[k.dtype],
-                 _stream_handle(stream, dev)),
-           "gdn_decay_decode_tree")
+    _tree_call("gdn_decay_decode_tree", q, k, v, (decay,), parents, None, state_pool, slots, o, stream)
 
 
 def gdn_decay_tree_commit(k, v, decay, parents, accepted, state_pool, slots, stream=None):
     """gdn_tree_commit for the constant-decay rule (C entry point
     ``gdn_decay_tree_commit``)."""
-    B, n, n_slots, Hqk, Hv, dk, dv = _tree_sizes(k, v, parents, state_pool, slots, k.dtype)
-    dev = k.device
-    _expect(decay, "decay", (Hv,), torch.float32, dev)
-    _expect(accepted, "accepted", (B,), torch.int32, dev)
-    _check(_call(dev, library().gdn_decay_tree_commit, _ptr(k), _ptr(v), _ptr(decay), _ptr(parents), _ptr(accepted),
-                 _ptr(state_pool), _ptr(slots), B, n, n_slots, Hqk, Hv, dk, dv, _DTYPES[k.dtype],
-                 _stream_handle(stream, dev)),
-           "gdn_decay_tree_commit")
+    if accepted is None:
+        raise GdnError("accepted is required")
+    _tree_call("gdn_decay_tree_commit", None, k, v, (decay,), parents, accepted, state_pool, slots, None, stream)
 
 
-def _cache_sizes(state_pool, slots, codes, scales, cache_slots):
-    n_slots, Hv, dk, dv = _shape(state_pool, "state_pool", 4)
+def _cache_args(state_pool, slots, codes, scales, cache_slots):
+    """Pointers of state_pool, slots, codes, scales, cache_slots, and the sizes."""
+    pool = n_slots, Hv, dk, dv = _shape(state_pool, "state_pool", 4)
     n_cache = _shape(codes, "codes", 4)[0]
     N = _shape(slots, "slots", 1)[0]
-    dev = state_pool.device
-    if dev.type != "cuda":
+    dev, code = state_pool.device, _CODES.get(codes.dtype)
+    if not state_pool.is_cuda:
         raise GdnError(f"tensors must be on a CUDA device, got {dev}")
-    if codes.dtype not in _CODES:
+    if code is None:
         raise GdnError(f"codes: expected torch.int8 or torch.float8_e4m3fn, got {codes.dtype}")
-    for name, t, shape, dt in (("state_pool", state_pool, state_pool.shape, torch.float32),
-                               ("codes", codes, (n_cache, Hv, dk, dv), codes.dtype),
-                               ("scales", scales, (n_cache, Hv, dk), torch.float32),
-                               ("slots", slots, (N,), torch.int32), ("cache_slots", cache_slots, (N,), torch.int32)):
-        _expect(t, name, shape, dt, dev)
-    return N, n_slots, n_cache, Hv, dk, dv, _CODES[codes.dtype]
+    ptrs = _pointers(dev, ("state_pool", state_pool, pool, torch.float32), ("slots", slots, (N,), torch.int32),
+                     ("codes", codes, (n_cache, Hv, dk, dv), codes.dtype),
+                     ("scales", scales, (n_cache, Hv, dk), torch.float32), ("cache_slots", cache_slots, (N,), torch.int32))
+    return ptrs, (N, n_slots, n_cache, Hv, dk, dv, code)
 
 
 def gdn_state_store(state_pool, slots, codes, scales, cache_slots, stream=None):
@@ -746,20 +717,17 @@ def gdn_state_store(state_pool, slots, codes, scales, cache_slots, stream=None):
     state_pool[slots[i]].  state_pool [n_slots, Hv, dk, dv] float32; codes
     [n_cache, Hv, dk, dv] int8 or float8_e4m3fn; scales [n_cache, Hv, dk] float32;
     slots, cache_slots [N] int32, out of range = skipped."""
-    sizes = _cache_sizes(state_pool, slots, codes, scales, cache_slots)
+    ptrs, sizes = _cache_args(state_pool, slots, codes, scales, cache_slots)
     dev = state_pool.device
-    _check(_call(dev, library().gdn_state_store, _ptr(state_pool), _ptr(slots), _ptr(codes), _ptr(scales),
-                 _ptr(cache_slots), *sizes, _stream_handle(stream, dev)),
-           "gdn_state_store")
+    _check(_call(dev, library().gdn_state_store, *ptrs, *sizes, _stream_handle(stream, dev)), "gdn_state_store")
 
 
 def gdn_state_load(codes, scales, cache_slots, state_pool, slots, stream=None):
     """Brings snapshots back (C entry point ``gdn_state_load``): state_pool[slots[i]] =
     codes * scales of cache row cache_slots[i].  Arguments as gdn_state_store."""
-    sizes = _cache_sizes(state_pool, slots, codes, scales, cache_slots)
+    (pool, slot, code, scale, cache_slot), sizes = _cache_args(state_pool, slots, codes, scales, cache_slots)
     dev = state_pool.device
-    _check(_call(dev, library().gdn_state_load, _ptr(codes), _ptr(scales), _ptr(cache_slots), _ptr(state_pool),
-                 _ptr(slots), *sizes, _stream_handle(stream, dev)),
+    _check(_call(dev, library().gdn_state_load, code, scale, cache_slot, pool, slot, *sizes, _stream_handle(stream, dev)),
            "gdn_state_load")
 
 
