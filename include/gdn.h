@@ -457,8 +457,8 @@ gdn_status gdn_bwd_chunk(const void *q, const void *k, const void *v, const floa
  *      reads it, the state is rounded to bf16, and so are the decayed scores
  *      (two pieces of 16 bits in all for T <= 64).
  * With few heads for the device (B * Hv below the number of SMs) each sequence
- * is cut into up to 16 segments whose states a first launch computes side by
- * side.  workspace: device scratch of gdn_decay_fwd_workspace(...) bytes for the
+ * is cut into a head and up to 16 segments, whose states a first launch computes
+ * side by side with the head.  workspace: device scratch of gdn_decay_fwd_workspace(...) bytes for the
  * current device (0: no segments, may be NULL), 256-byte aligned, owned by the
  * caller; contents on entry do not matter; calls sharing it must not overlap.
  * Too small or misaligned: GDN_ERR_INVALID_ARG.

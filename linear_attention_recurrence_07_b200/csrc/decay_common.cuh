@@ -42,7 +42,7 @@ struct WalkSpan {
     int nchunks;           // chunks of the whole sequence
     int c0, c1;            // this CTA's chunks
     int b, seg;            // sequence, segment
-    bool copy_init;        // first launch, segment 0: only carry the start state over
+    bool state_only;       // first launch: no output rows, the segment's state from zero
 };
 
 __device__ __forceinline__ int chunk_rows(const WalkSpan &s, bool rev, int c, int &t0)
@@ -52,11 +52,16 @@ __device__ __forceinline__ int chunk_rows(const WalkSpan &s, bool rev, int c, in
     return min(kChunk, s.L - m * kChunk);
 }
 
-// y: index over sequences x segments.  state_only: the first launch of a segmented walk.
-__device__ __forceinline__ WalkSpan walk_span(const DecayWalk &w, int y, bool state_only)
+// First chunk of segment g of the second launch.
+__device__ __forceinline__ int segment_start(const DecayWalk &w, int g) { return w.head_chunks + g * w.seg_chunks; }
+
+// y: index over sequences x segments.  first: the first launch of a segmented walk, which walks the
+// head of the sequence (entry 0, from its start state) and the states of the segments but the last
+// (entry g + 1: segment g).
+__device__ __forceinline__ WalkSpan walk_span(const DecayWalk &w, int y, bool first)
 {
     WalkSpan s;
-    s.copy_init = false;
+    s.state_only = false;
     if (w.cu_seqlens) {
         const int a = min(max(w.cu_seqlens[y], 0), w.T);
         const int e = min(max(w.cu_seqlens[y + 1], a), w.T);
@@ -69,12 +74,12 @@ __device__ __forceinline__ WalkSpan walk_span(const DecayWalk &w, int y, bool st
     s.seg = y - s.b * w.nseg;
     s.bt = s.b; s.tb = 0; s.L = w.T;
     s.nchunks = (w.T + kChunk - 1) / kChunk;
-    if (state_only) {
-        s.copy_init = s.seg == 0;
-        s.c0 = (s.seg - 1) * w.seg_chunks;
-        s.c1 = s.copy_init ? s.c0 : s.c0 + w.seg_chunks;
+    if (first) {
+        s.state_only = s.seg > 0;
+        s.c0 = s.state_only ? segment_start(w, s.seg - 1) : 0;
+        s.c1 = segment_start(w, s.seg);
     } else {
-        s.c0 = s.seg * w.seg_chunks;
+        s.c0 = segment_start(w, s.seg);
         s.c1 = s.seg == w.nseg - 1 ? s.nchunks : s.c0 + w.seg_chunks;
     }
     return s;

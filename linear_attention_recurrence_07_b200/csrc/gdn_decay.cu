@@ -43,7 +43,7 @@ struct SimtSmem {
 
 template <int DZ>
 __global__ void __launch_bounds__(kSimtThreads)
-decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
+decay_walk_kernel(const __grid_constant__ DecayWalks d, bool first)
 {
     constexpr int kZSlices = kHeadDim / DZ;
     const DecayWalk &w = d.w[blockIdx.z];
@@ -51,11 +51,12 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
     SimtSmem<DZ> &sm = *reinterpret_cast<SimtSmem<DZ> *>(raw);
     const int tid = threadIdx.x;
     const int h = blockIdx.x / kZSlices, z0 = (blockIdx.x - h * kZSlices) * DZ;
-    const WalkSpan sp = walk_span(w, blockIdx.y, state_only);
-    if (state_only) let_next_launch_start();
+    const WalkSpan sp = walk_span(w, blockIdx.y, first);
+    const bool state_only = sp.state_only;
+    if (first) let_next_launch_start();
     const size_t st = (size_t)kHeadDim * kHeadDim;
     const int tail = sp.L - (sp.nchunks - 1) * kChunk, special = w.rev ? 0 : sp.nchunks - 1;
-    const int last_back = w.fin_back && !state_only;     // the end state is wanted undecayed
+    const int last_back = w.fin_back && !first;     // the end state is wanted undecayed
 
     if (tid < kChunk + 1 + 16 + 2) {
         const double loglam = decay_log(w.decay[h]);
@@ -63,8 +64,8 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
             sm.pw[tid] = (float)decay_pow(loglam, tid);
         } else if (tid <= kChunk + 16) {
             const int g = tid - kChunk - 1, here = tokens_before(sp, w.rev, sp.c0);
-            if (w.nseg > 1 && !state_only && g <= sp.seg)
-                sm.seg[g] = (float)decay_pow(loglam, here - tokens_before(sp, w.rev, g * w.seg_chunks));
+            if (w.nseg > 1 && !first && g <= sp.seg)
+                sm.seg[g] = (float)decay_pow(loglam, here - tokens_before(sp, w.rev, segment_start(w, g)));
         } else {
             const int last = tid - kChunk - 17;
             const double p = decay_pow(loglam, last ? tail - last_back : kChunk);
@@ -73,7 +74,7 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
     }
     __syncthreads();
     // ---- start state
-    if (w.nseg > 1 && !state_only) {
+    if (w.nseg > 1 && !first) {
         wait_for_launch_before();
         for (int i = tid; i < kHeadDim * (DZ / 4); i += kSimtThreads) {
             const int d = i / (DZ / 4), c = (i % (DZ / 4)) * 4;
@@ -88,7 +89,7 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
             *reinterpret_cast<float4 *>(&sm.H[d][c]) = a;
         }
     } else {
-        const float *src = (w.init && (!state_only || sp.copy_init)) ? w.init + ((size_t)sp.b * w.Hv + h) * st : nullptr;
+        const float *src = (w.init && !state_only) ? w.init + ((size_t)sp.b * w.Hv + h) * st : nullptr;
         const float f = (w.init_decays && sp.L > 0) ? sm.pw[1] : 1.f;
         for (int i = tid; i < kHeadDim * DZ; i += kSimtThreads) {
             const int d = w.init_trans ? (i & (kHeadDim - 1)) : i / DZ;
@@ -318,7 +319,7 @@ decay_walk_kernel(const __grid_constant__ DecayWalks d, bool state_only)
     }
     // ---- end state
     float *dst = nullptr;
-    if (state_only) dst = w.seg + (((size_t)sp.b * w.nseg + sp.seg) * w.Hv + h) * st;
+    if (first) dst = w.seg + (((size_t)sp.b * w.nseg + sp.seg) * w.Hv + h) * st;
     else if (w.fin && sp.c1 == sp.nchunks) dst = w.fin + ((size_t)sp.b * w.Hv + h) * st;
     if (dst)
         for (int i = tid; i < kHeadDim * (DZ / 4); i += kSimtThreads) {

@@ -44,10 +44,14 @@ bool wide_walk(const DecayWalk &w, int walks)
 }
 
 // Segments of `walks` dense walks that run side by side: as many as fill the device with
-// one CTA (fp32, narrow: one head's four half-SM CTAs) per walk, head and segment.  bf16: of
-// at least four chunks, because the launch that computes their start states reads y and z
-// once more and starts anew; the fp32 kernel is bound by its arithmetic, of which that
-// launch has a quarter, so one chunk is enough.
+// one CTA (fp32, narrow: one head's four half-SM CTAs) per walk, head and segment.  The launch
+// that computes their start states has one such CTA to spare, the last segment's, and walks
+// the head of the sequence with it: as much of a segment as takes the time of a state alone
+// (bf16: 85% of a chunk's, which D and the state take; fp32: 25%, of its arithmetic).  48 heads,
+// T=4096, three segments of 17 chunks behind 13: 58 us, of 22 each: 65; parts of 45% 61, 60% 59,
+// 100% 61 us.  bf16: segments of
+// at least four chunks, because that launch reads y and z once more and starts anew; the fp32
+// kernel is bound by its arithmetic, so one chunk is enough.
 void choose_segments(DecayWalk &w, int walks, gdn_dtype dtype)
 {
     const int least = dtype == GDN_F32 ? 1 : 4;
@@ -55,12 +59,20 @@ void choose_segments(DecayWalk &w, int walks, gdn_dtype dtype)
     const long long units = (long long)w.B * w.Hv * walks * (dtype == GDN_F32 && !wide_walk(w, walks) ? 2 : 1);
     long long n = sm_count() / units;
     if (n > kMaxDecaySegments) n = kMaxDecaySegments;
-    if (n < 1) n = 1;
-    int per = (int)((nchunks + n - 1) / n);
+    w.nseg = 1;
+    w.seg_chunks = nchunks;
+    w.head_chunks = 0;
+    if (n < 2 || nchunks <= least) return;
+    // the shortest segments of which n and a head of `part` percent of one cover the sequence
+    const long long part = dtype == GDN_F32 ? 25 : 85;
+    int per = (int)((100LL * nchunks + 100 * n + part - 1) / (100 * n + part));
     if (per < least) per = least;
+    const int head = nchunks - n * per > 0 ? (int)(nchunks - n * per) : 0;
+    const int nseg = (nchunks - head + per - 1) / per;
+    if (nseg < 2) return;
+    w.nseg = nseg;
     w.seg_chunks = per;
-    w.nseg = (nchunks + per - 1) / per;
-    if (w.nseg < 1) w.nseg = 1;
+    w.head_chunks = head;
 }
 size_t segment_bytes(const DecayWalk &w)
 {

@@ -159,7 +159,8 @@ __device__ __forceinline__ void store_rows(__nv_bfloat16 *dst, uint32_t t_lane, 
     }
 }
 
-template <bool STATE_ONLY, int NZ, int NP>
+// FIRST: the first launch of a segmented walk.
+template <bool FIRST, int NZ, int NP>
 __global__ void __launch_bounds__(kDtThreads, 1)
 decay_tc_kernel(const __grid_constant__ TcWalks p)
 {
@@ -176,9 +177,10 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
     const DecayCtl ctl{bar, abort_flag};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x;
-    const WalkSpan sp = walk_span(w, blockIdx.y, STATE_ONLY);
+    const WalkSpan sp = walk_span(w, blockIdx.y, FIRST);
+    const bool state_only = FIRST && sp.state_only;
     const int n = sp.c1 - sp.c0;                             // chunks of this CTA
-    if (STATE_ONLY) let_next_launch_start();
+    if (FIRST) let_next_launch_start();
     const uint32_t sbase = smem_u32(sm);
     const size_t hstate = (size_t)kHeadDim * kHeadDim;
 
@@ -186,7 +188,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
     // whose end state may be wanted undecayed.  It is the walk's last (forwards) or first (backwards).
     const int special = w.rev ? 0 : sp.nchunks - 1;
     const int tail = sp.L - (sp.nchunks - 1) * C;
-    const int back = (w.fin_back && !STATE_ONLY) ? 1 : 0;
+    const int back = (w.fin_back && !FIRST) ? 1 : 0;
 
     // The first stages' tiles, in flight while the rest is set up (only this thread waits on D_EMPTY).
     auto load_stage = [&](int c) {
@@ -196,12 +198,12 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
         unsigned char *st = sm + s * kStageBytes;
         uint64_t *full = &bar[D_FULL + s];
         const int hx = h / (w.Hv / w.hx), hy = h / (w.Hv / w.hy), hz = h / (w.Hv / w.hz);
-        mbar_arrive_expect_tx(full, STATE_ONLY ? 4 * TILE : kStageBytes);
+        mbar_arrive_expect_tx(full, state_only ? 4 * TILE : kStageBytes);
         tma_load_4d(st + 2 * TILE, &tm_y, full, 0, hy, t0, sp.bt);
         tma_load_4d(st + 3 * TILE, &tm_y, full, 64, hy, t0, sp.bt);
         tma_load_4d(st + 4 * TILE, &tm_z, full, 0, hz, t0, sp.bt);
         tma_load_4d(st + 5 * TILE, &tm_z, full, 64, hz, t0, sp.bt);
-        if (!STATE_ONLY) {
+        if (!state_only) {
             tma_load_4d(st + 0 * TILE, &tm_x, full, 0, hx, t0, sp.bt);
             tma_load_4d(st + 1 * TILE, &tm_x, full, 64, hx, t0, sp.bt);
         }
@@ -209,12 +211,12 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
     if (tid == 0) {
         for (int i = 0; i < (int)D_NBAR; ++i)
             mbar_init(&bar[i], i == D_ZP || i == D_HREADY || i == D_CUT ? 8 : i == D_PREADY || i == D_PREADY + 1 || i == D_OFREE ? 4
-                               : ((i >= D_EMPTY && i < D_EMPTY + kStages) || i == D_DRAIN) && !STATE_ONLY ? 2 : 1);
+                               : ((i >= D_EMPTY && i < D_EMPTY + kStages) || i == D_DRAIN) && !state_only ? 2 : 1);
         *abort_flag = 0;
         fence_mbar_init();
 #pragma unroll 1
         for (int c = 0; c < min(n, kStages); ++c) load_stage(c);
-        if (!STATE_ONLY) prefetch_tensormap(&tm_o);
+        if (!state_only) prefetch_tensormap(&tm_o);
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, T_COLS);
@@ -244,7 +246,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
         if (ti < 18 && ti >= 2) {    // decay of segment ti - 2's start state up to this segment
             const int g = ti - 2, here = tokens_before(sp, w.rev, sp.c0);
             if (w.nseg > 1 && g <= sp.seg)
-                seg_decay[g] = (float)decay_pow(loglam, here - tokens_before(sp, w.rev, g * w.seg_chunks));
+                seg_decay[g] = (float)decay_pow(loglam, here - tokens_before(sp, w.rev, segment_start(w, g)));
         } else if (ti < 2) {         // lambda^L of full chunks and of the special one, in two floats
             const double p = decay_pow(loglam, ti ? tail - back : C);
             tab[TAB_L + 2 * ti] = (float)p;
@@ -302,7 +304,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
             }
             __syncwarp();
         }
-        if (!STATE_ONLY && warp == 2) {
+        if (!state_only && warp == 2) {
             // ==================================================== MMA issuer: G and O
             // Short loops: this code and the other roles' share the instruction cache.
             auto issue_g = [&](int c) -> bool {
@@ -373,7 +375,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
         uint64_t H[32];                                      // H^T[dz][64 part + 2 e], +1
 #pragma unroll
         for (int e = 0; e < 32; ++e) H[e] = 0;
-        const bool has_init = w.init && (STATE_ONLY ? sp.copy_init : w.nseg == 1);
+        const bool has_init = w.init && (FIRST ? !state_only : w.nseg == 1);
         if (has_init) {
             const float *src = w.init + ((size_t)sp.b * w.Hv + h) * hstate;
             if (w.init_trans) {
@@ -398,7 +400,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
 #pragma unroll
             for (int e = 0; e < 32; ++e) H[e] = mul2(pack2(f, f), H[e]);
         }
-        if (w.nseg > 1 && !STATE_ONLY) {
+        if (w.nseg > 1 && !FIRST) {
             wait_for_launch_before();
 #pragma unroll 1
             for (int g = 0; g <= sp.seg; ++g) {
@@ -486,7 +488,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
         if (n > 0 && (ok = make_z(0))) {
             store_z();
             announce_z();
-            if (!STATE_ONLY) write_h();
+            if (!state_only) write_h();
         }
         for (int c = 0; c < n && ok; ++c) {
             if (c + 1 < n && !(ok = make_z(c + 1))) break;   // while D of this chunk runs
@@ -506,7 +508,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
             }
             if (c + 1 < n) {
                 announce_z();
-                if (!STATE_ONLY) {
+                if (!state_only) {
                     if (!(ok = ctl.wait(D_XFULL, c & 1))) break;
                     tc_fence_after();
                     write_h();
@@ -514,7 +516,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
             }
         }
         float *dst = nullptr;
-        if (STATE_ONLY) dst = w.seg + (((size_t)sp.b * w.nseg + sp.seg) * w.Hv + h) * hstate;
+        if (FIRST) dst = w.seg + (((size_t)sp.b * w.nseg + sp.seg) * w.Hv + h) * hstate;
         else if (w.fin && sp.c1 == sp.nchunks) dst = w.fin + ((size_t)sp.b * w.Hv + h) * hstate;
         if (ok && dst) {
 #pragma unroll
@@ -545,7 +547,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
                 const int e = sgn * (g + 8 * half - 8 * d - 2 * t);
                 mask[d][half] = pack2(e >= 0 ? 1.f : 0.f, e - sgn >= 0 ? 1.f : 0.f);
             }
-        if (!STATE_ONLY) {
+        if (!state_only) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
 #pragma unroll
@@ -578,7 +580,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
             if (lane == 0) mbar_arrive(&bar[D_PREADY + (c & 1)]);                  // and G is read
         };
         if (tab[TAB_PW + 63] >= kScaleMin) {
-            for (int c = 0; c < n && !STATE_ONLY; ++c) {
+            for (int c = 0; c < n && !state_only; ++c) {
                 if (!wait_p(c)) break;
                 const float *ct = tab + TAB_C + (sp.c0 + c == special ? 64 : 0) + 2 * t;
                 const int bn = w.rev ? 4 : q4 + 1;
@@ -606,7 +608,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
                 announce_p(c);
             }
         } else {
-            for (int c = 0; c < n && !STATE_ONLY; ++c) {
+            for (int c = 0; c < n && !state_only; ++c) {
                 if (!wait_p(c)) break;
                 const float *ft = tab + TAB_F + (sp.c0 + c == special ? 64 : 0);
 #pragma unroll 1
@@ -638,7 +640,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
         const uint32_t o_at = sbase + DOFF_O + (q4 >> 1) * TILE +
                               sw128_chunk(8 * (lane >> 4) + (lane & 7), 4 * (q4 & 1) + ((lane >> 3) & 1));
         const size_t stride = (size_t)w.Hv * kHeadDim;
-        for (int c = 0; c < n && !STATE_ONLY; ++c) {
+        for (int c = 0; c < n && !state_only; ++c) {
             const int cw = sp.c0 + c;
             const float *ft = tab + TAB_F + (cw == special ? 64 : 0);
             int t0;
@@ -746,16 +748,16 @@ bool make_map_f32(CUtensorMap *map, const void *base, int B, int T, int H)
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool STATE_ONLY, int NZ, int NP>
+template <bool FIRST, int NZ, int NP>
 cudaError_t launch_tc(const TcWalks &p, cudaStream_t stream)
 {
-    cudaError_t err = cudaFuncSetAttribute(decay_tc_kernel<STATE_ONLY, NZ, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t err = cudaFuncSetAttribute(decay_tc_kernel<FIRST, NZ, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            (int)D_SMEM);
     if (err != cudaSuccess) return err;
     const DecayWalk &w = p.d.w[0];
     const dim3 grid((unsigned)w.Hv, (unsigned)(w.B * w.nseg), (unsigned)p.d.n);
-    if (!STATE_ONLY && w.nseg > 1) return launch_after(decay_tc_kernel<STATE_ONLY, NZ, NP>, grid, kDtThreads, (int)D_SMEM, stream, p);
-    decay_tc_kernel<STATE_ONLY, NZ, NP><<<grid, kDtThreads, D_SMEM, stream>>>(p);
+    if (!FIRST && w.nseg > 1) return launch_after(decay_tc_kernel<FIRST, NZ, NP>, grid, kDtThreads, (int)D_SMEM, stream, p);
+    decay_tc_kernel<FIRST, NZ, NP><<<grid, kDtThreads, D_SMEM, stream>>>(p);
     return cudaGetLastError();
 }
 

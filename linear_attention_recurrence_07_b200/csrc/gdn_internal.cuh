@@ -96,10 +96,11 @@ struct DecayWalk {
     int B, T, Hv;
     bool rev = false;
     const int *cu_seqlens = nullptr; // packed sequences (see ChunkArgs), forwards only
-    // Segments (dense only): nseg > 1 pieces of seg_chunks chunks.  A first launch writes
-    // seg [B, nseg, Hv, 128, 128]: entry 0 the start state, entry g the state that segment
-    // g - 1 adds on its own; the main launch starts segment g from the decayed sum of 0 .. g.
-    int nseg = 1, seg_chunks = 0;
+    // Segments (dense only): nseg > 1 pieces of seg_chunks chunks behind the first head_chunks.  A
+    // first launch walks those, and writes seg [B, nseg, Hv, 128, 128]: entry 0 the state behind
+    // them, entry g the state that segment g - 1 adds on its own; the second launch starts segment
+    // g from the decayed sum of 0 .. g.
+    int nseg = 1, seg_chunks = 0, head_chunks = 0;
     float *seg = nullptr;
 };
 // Up to three walks of the same B, T, Hv and segments, side by side in one launch (two with

@@ -69,6 +69,15 @@ def test_prefill_in_segments(dtype, Hqk, Hv):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("s0", [True, False])
+def test_prefill_in_segments_behind_a_head(dtype, s0):
+    """A quarter of the device's width in heads: the first launch walks the sequence's head too."""
+    d = inputs((1, 1800), 12, 36, dtype, 46, s0=s0)
+    check_forward(d, *forward(d), "head")
+    assert binding.device_status() == "GDN_OK"
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
 def test_prefill_without_states(dtype):
     d = inputs((3, 130), 1, 3, dtype, 50, s0=False)
     check_forward(d, *forward(d), "no S0")
@@ -240,6 +249,15 @@ def test_gradients_in_segments(dtype, Hqk, Hv):
     d = inputs((1, 1130), Hqk, Hv, dtype, 140 + Hv)
     dO, dSF = upstream(d, 141)
     check_backward(d, dO, dSF, backward(d, dO, dSF), f"heads {Hqk}/{Hv}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("state", [False, True])
+def test_gradients_in_segments_behind_a_head(dtype, state):
+    d = inputs((1, 1800), 6, 12, dtype, 146, s0=state)
+    dO, dSF = upstream(d, 147, state=state)
+    check_backward(d, dO, dSF, backward(d, dO, dSF), "head")
+    assert binding.device_status() == "GDN_OK"
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
