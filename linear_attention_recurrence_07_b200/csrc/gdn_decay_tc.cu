@@ -32,14 +32,14 @@
 //   warps 16-19 O epilogue (stmatrix, TMA store)
 //
 // Measured: 16 QK / 48 V heads, B=8, T=8192: 0.65-0.68 ms, 3.3 TB/s (half of the copy
-// bandwidth), 300 TF/s of the recurrence's own arithmetic; B=1, T=4096: 70 us (three
-// segments); gradients at 48 heads, T=4096: 124-131 us.  A chunk takes 2400 to 2700 cycles per
-// SM (the clock settles at 1.65 GHz under this load).  No single unit bounds it: the chain from D
-// through the state's registers to the next D (pieces of Z 1100, reading D 550, H 280 cycles of
-// its two warpgroups, and D itself), the tensor core 57-65% of the time (65 cycles per 128 x 128 x 16
-// MMA make 780 for D; H X 270, Z P 200, G 280), shared memory 70%.  Giving Z' warps of its own,
-// Z' or O a second buffer, or Z P a place before H X was no faster: what runs earlier takes the
-// tensor core from D.
+// bandwidth), 300 TF/s of the recurrence's own arithmetic; B=1, T=4096: 64 us (a head and
+// three segments); gradients at 48 heads, T=4096: 124-131 us.  A chunk takes 2400 to 2700
+// cycles per SM (the clock settles at 1.65 GHz under this load).  No single unit bounds it: the
+// chain from D through the state's registers to the next D (pieces of Z 1100, reading D 550, H
+// 280 cycles of its two warpgroups, and D itself), the tensor core 57-65% of the time (65 cycles
+// per 128 x 128 x 16 MMA make 780 for D; H X 270, Z P 200, G 280), shared memory 70%.  Giving Z'
+// warps of its own, Z' or O a second buffer, or Z P a place before H X was no faster: what runs
+// earlier takes the tensor core from D.
 // What counted on the way: no spills (setmaxnreg; 1.6 times), MMAs issued by an elected lane,
 // and the size of the loops: unrolled roles of 98 KB of code waited for instructions a quarter
 // of the time.
