@@ -456,6 +456,9 @@ gdn_status gdn_bwd_chunk(const void *q, const void *k, const void *v, const floa
  *      pieces (the 24 bits of an fp32), so S_final carries fp32 accuracy; where o
  *      reads it, the state is rounded to bf16, and so are the decayed scores
  *      (two pieces of 16 bits in all for T <= 64).
+ *      Scores (a row of q with one of k) and the sums of a row may reach 2^66: a chunk's
+ *      products pass through fp32 with up to 60 bits of the decay's powers.  For
+ *      decays below 0.65 a state is exact to 24 bits down to magnitudes of 2^-64.
  * With few heads for the device (B * Hv below the number of SMs) each sequence
  * is cut into a head and up to 16 segments, whose states a first launch computes
  * side by side with the head.  workspace: device scratch of gdn_decay_fwd_workspace(...) bytes for the
@@ -514,7 +517,7 @@ gdn_status gdn_decay_decode_step_slots(const void *q, const void *k, const void 
  * workspace: gdn_decay_bwd_workspace(...) bytes for the current device, rules as
  *      for gdn_decay_fwd.  It holds the segments' states and, where QK heads are
  *      shared, two fp32 rows per token and V head.
- * Sizes, dtypes and errors as gdn_decay_fwd.  No atomics: repeated calls return
+ * Sizes, dtypes, range and errors as gdn_decay_fwd.  No atomics: repeated calls return
  * the same bits.
  */
 size_t gdn_decay_bwd_workspace(int B, int T, int Hqk, int Hv, int dk, int dv, gdn_dtype dtype);

@@ -19,9 +19,14 @@
 // one chunk, whose first rows have few terms and no H, get 16 bits of P in two pieces (they
 // are bound by latency, and the pieces share the room of P's second buffer).  Z' has three
 // pieces, all 24 bits, where an end state is wanted, two where the state only feeds O; small
-// pieces are accumulated first, because the tensor core truncates.  lambda^{-p_j}
-// grows to lambda^{-63}: below lambda = 2^-(100/63) the scale is held at 2^100, which
-// replaces a factor lambda^p < 2^-100 on H's share of a row by 2^-100.
+// pieces are accumulated first, because the tensor core truncates.
+//
+// Range.  lambda^{-p_j} grows to lambda^{-63}: below lambda = 2^-(100/63) the scale is held at
+// 2^100, which replaces a factor lambda^p < 2^-100 on H's share of a row by 2^-100.  Heads whose
+// scales span more than 40 bits are centred: state, Z' and P carry 2^-s and the scale of O 2^s, s
+// half of the span and at most 40 (powers of two, in the tables and at the walk's ends only, so
+// the results' bits are the same).  Scores and sums stay finite to 2^67 (2^28 uncentred), those
+// that the causal mask multiplies by zero too, and a state keeps its 24 bits down to 2^-64.
 //
 // One CTA per (sequence or segment, V head), warp-specialised:
 //   warp 0      TMA producer: X, Y, Z tiles, four stages of 48 KB
@@ -65,7 +70,7 @@ constexpr uint32_t DOFF_P = kStages * kStageBytes;    // two buffers, chunk c us
 constexpr uint32_t DOFF_O = DOFF_P + 2 * TILE;
 constexpr uint32_t DOFF_TAB = DOFF_O + 2 * TILE;      // powers; per token: Z weights, O scales, P scales
 constexpr uint32_t TAB_PW = 0, TAB_W = 66, TAB_F = 66 + 128, TAB_C = 66 + 256, TAB_L = 66 + 3 * 128,
-                   TAB_FLOATS = TAB_L + 6;
+                   TAB_FLOATS = TAB_L + 6;     // TAB_L: lambda^L twice (two floats each), factors of start and end state
 constexpr uint32_t DOFF_BAR = DOFF_TAB + TAB_FLOATS * 4;
 enum : int {
     D_FULL = 0,                    // x4: tiles of a stage landed
@@ -99,6 +104,7 @@ constexpr uint32_t IDD_D = idesc_bf16(128, 128, false, true);
 constexpr int kRegsIssue = 40, kRegsState = 160, kRegsP = 56, kRegsOut = 56;
 constexpr double kScaleFloor = -69.31471805599453;    // log of 2^-100
 constexpr float kScaleMin = 7.8886091e-31f;           // 2^-100
+constexpr double kCentred = -27.725887222397812;      // log of 2^-40
 
 template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -225,10 +231,14 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
     if (warp == 2 || warp == 3 || warp >= 12) {
         // tables: [0] of each pair for full chunks, [1] for the special one
         const double loglam = decay_log(w.decay[h]);
-        const bool strong = 63.0 * loglam < kScaleFloor;     // lambda^63 below the scales' floor
+        const double span = 63.0 * loglam;                   // log of lambda^63
+        const bool strong = span < kScaleFloor;              // below the scales' floor
+        // 2^s, s half of the span
+        const int s = span < kCentred ? min(40, (int)(span * -0.72134752044448170)) : 0;
+        const double up = __hiloint2double((1023 + s) << 20, 0), down = __hiloint2double((1023 - s) << 20, 0);
         const int ti = warp < 4 ? tid - 64 : tid - 320;      // 0 .. 319
         for (int i = ti; i < 65 + 3 * 128; i += 320) {
-            double e;
+            double e, centre = 1.0;
             uint32_t at;
             if (i < 65) {
                 e = i;
@@ -240,8 +250,9 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
                 e = which < 2 ? max(L - p - bk, 0) : which < 4 ? p : -p;
                 at = TAB_W + (i - 65);
                 if (strong && which >= 2 && which < 4) e = fmin(e, kScaleFloor / loglam);
+                centre = which >= 2 && which < 4 ? up : down;
             }
-            tab[at] = (float)decay_pow(loglam, e);
+            tab[at] = (float)(centre * decay_pow(loglam, e));
         }
         if (ti < 18 && ti >= 2) {    // decay of segment ti - 2's start state up to this segment
             const int g = ti - 2, here = tokens_before(sp, w.rev, sp.c0);
@@ -251,6 +262,8 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
             const double p = decay_pow(loglam, ti ? tail - back : C);
             tab[TAB_L + 2 * ti] = (float)p;
             tab[TAB_L + 2 * ti + 1] = (float)(p - (double)(float)p);
+            // the walk's ends: segments' states stay centred, and with no tokens the state passes as it is
+            tab[TAB_L + 4 + ti] = sp.L == 0 ? 1.f : ti ? (FIRST ? 1.f : (float)up) : (float)((w.init_decays ? decay_pow(loglam, 1.0) : 1.0) * down);
         }
     }
     tc_fence_before();
@@ -395,8 +408,8 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
             }
         }
         const uint32_t tmem = all_set(), t_lane = tmem + ((uint32_t)(q4 * 32) << 16);
-        if (has_init && w.init_decays && sp.L > 0) {
-            const float f = tab[TAB_PW + 1];
+        if (has_init && tab[TAB_L + 4] != 1.f) {
+            const float f = tab[TAB_L + 4];
 #pragma unroll
             for (int e = 0; e < 32; ++e) H[e] = mul2(pack2(f, f), H[e]);
         }
@@ -514,6 +527,11 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
                     write_h();
                 }
             }
+        }
+        if (tab[TAB_L + 5] != 1.f) {
+            const float f = tab[TAB_L + 5];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) H[e] = mul2(pack2(f, f), H[e]);
         }
         float *dst = nullptr;
         if (FIRST) dst = w.seg + (((size_t)sp.b * w.nseg + sp.seg) * w.Hv + h) * hstate;

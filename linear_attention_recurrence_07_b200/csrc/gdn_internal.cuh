@@ -98,8 +98,8 @@ struct DecayWalk {
     const int *cu_seqlens = nullptr; // packed sequences (see ChunkArgs), forwards only
     // Segments (dense only): nseg > 1 pieces of seg_chunks chunks behind the first head_chunks.  A
     // first launch walks those, and writes seg [B, nseg, Hv, 128, 128]: entry 0 the state behind
-    // them, entry g the state that segment g - 1 adds on its own; the second launch starts segment
-    // g from the decayed sum of 0 .. g.
+    // them, entry g the state that segment g - 1 adds on its own (tensor cores: times the
+    // head's power of two); the second launch starts segment g from the decayed sum of 0 .. g.
     int nseg = 1, seg_chunks = 0, head_chunks = 0;
     float *seg = nullptr;
 };
