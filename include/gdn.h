@@ -455,7 +455,7 @@ gdn_status gdn_bwd_chunk(const void *q, const void *k, const void *v, const floa
  *      with an fp32 state: v's decayed copies enter its update in three bf16
  *      pieces (the 24 bits of an fp32), so S_final carries fp32 accuracy; where o
  *      reads it, the state is rounded to bf16, and so are the decayed scores
- *      (two pieces of 16 bits in all for T <= 64).
+ *      (two pieces of 16 bits in all for sequences of at most 64 tokens, packed or not).
  *      Scores (a row of q with one of k) and the sums of a row may reach 2^66: a chunk's
  *      products pass through fp32 with up to 60 bits of the decay's powers.  For
  *      decays below 0.65 a state is exact to 24 bits down to magnitudes of 2^-64.

@@ -48,6 +48,8 @@
 // What counted on the way: no spills (setmaxnreg; 1.6 times), MMAs issued by an elected lane,
 // and the size of the loops: unrolled roles of 98 KB of code waited for instructions a quarter
 // of the time.
+#include <type_traits>
+
 #include "tc_common.cuh"
 #include "decay_common.cuh"
 
@@ -165,7 +167,8 @@ __device__ __forceinline__ void store_rows(__nv_bfloat16 *dst, uint32_t t_lane, 
     }
 }
 
-// FIRST: the first launch of a segmented walk.
+// FIRST: the first launch of a segmented walk.  NZ, NP: pieces of Z' and of P; NP = 0: two for
+// sequences of one chunk, else one.
 template <bool FIRST, int NZ, int NP>
 __global__ void __launch_bounds__(kDtThreads, 1)
 decay_tc_kernel(const __grid_constant__ TcWalks p)
@@ -186,6 +189,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
     const WalkSpan sp = walk_span(w, blockIdx.y, FIRST);
     const bool state_only = FIRST && sp.state_only;
     const int n = sp.c1 - sp.c0;                             // chunks of this CTA
+    const bool fine = NP == 2 || (NP == 0 && sp.nchunks == 1);   // P in two pieces
     if (FIRST) let_next_launch_start();
     const uint32_t sbase = smem_u32(sm);
     const size_t hstate = (size_t)kHeadDim * kHeadDim;
@@ -363,9 +367,9 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t zd = smem_desc_sw128(sbase + s * kStageBytes + 4 * TILE, TILE, 1024);
-                    const uint64_t pd = smem_desc_sw128(sbase + DOFF_P + (NP == 1 ? (c & 1) * TILE : 0), 16, 1024);
+                    const uint64_t pd = smem_desc_sw128(sbase + DOFF_P + (c & 1) * TILE, 16, 1024);
 #pragma unroll 1
-                    for (int pc = NP - 1; pc >= 0; --pc)
+                    for (int pc = fine ? 1 : 0; pc >= 0; --pc)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             mma_bf16(tmem + T_O, zd + k * (2048 >> 4), pd + pc * (TILE >> 4) + k * 2, IDD_OI, true);
@@ -582,9 +586,9 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
             tc_fence_after();
             return true;
         };
-        auto store_p = [&](int c, int k, int half, uint64_t v) {
+        auto store_p = [&](auto two, int c, int k, int half, uint64_t v) {
             unsigned char *at = pt + half * 1024 + ((k ^ g) << 4);       // (i0 + 8 half) & 7 = g
-            if (NP == 2) {
+            if constexpr (decltype(two)::value) {            // c = 0: the pieces fill both buffers
                 *reinterpret_cast<uint32_t *>(at) = split_pair(v);
                 *reinterpret_cast<uint32_t *>(at + TILE) = round_pair(v);
             } else {
@@ -597,54 +601,59 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[D_PREADY + (c & 1)]);                  // and G is read
         };
-        if (tab[TAB_PW + 63] >= kScaleMin) {
-            for (int c = 0; c < n && !state_only; ++c) {
-                if (!wait_p(c)) break;
-                const float *ct = tab + TAB_C + (sp.c0 + c == special ? 64 : 0) + 2 * t;
-                const int bn = w.rev ? 4 : q4 + 1;
-                int b = w.rev ? q4 : 0;                      // 16 columns
-                uint32_t next[8];
-                tmem_ld16x256b_x2(t_lane + T_G + 64 * (c & 1) + 16 * b, next);
+        // code of its own for each kind, so that the short loop stays short
+        auto rows_of_p = [&](auto two) {
+            if (tab[TAB_PW + 63] >= kScaleMin) {
+                for (int c = 0; c < n && !state_only; ++c) {
+                    if (!wait_p(c)) break;
+                    const float *ct = tab + TAB_C + (sp.c0 + c == special ? 64 : 0) + 2 * t;
+                    const int bn = w.rev ? 4 : q4 + 1;
+                    int b = w.rev ? q4 : 0;                      // 16 columns
+                    uint32_t next[8];
+                    tmem_ld16x256b_x2(t_lane + T_G + 64 * (c & 1) + 16 * b, next);
 #pragma unroll 1
-                for (; b < bn; ++b) {
-                    uint32_t r[8];
-                    tmem_wait_ld();
+                    for (; b < bn; ++b) {
+                        uint32_t r[8];
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) r[x] = next[x];
-                    if (b + 1 < bn) tmem_ld16x256b_x2(t_lane + T_G + 64 * (c & 1) + 16 * (b + 1), next);
+                        for (int x = 0; x < 8; ++x) r[x] = next[x];
+                        if (b + 1 < bn) tmem_ld16x256b_x2(t_lane + T_G + 64 * (c & 1) + 16 * (b + 1), next);
 #pragma unroll
-                    for (int d = 0; d < 2; ++d) {
-                        const float2 sc = *reinterpret_cast<const float2 *>(ct + 16 * b + 8 * d);
+                        for (int d = 0; d < 2; ++d) {
+                            const float2 sc = *reinterpret_cast<const float2 *>(ct + 16 * b + 8 * d);
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            uint64_t v = mul2(pack2(sc.x, sc.y), pack2(__uint_as_float(r[4 * d + 2 * half]), __uint_as_float(r[4 * d + 2 * half + 1])));
-                            if (b == q4) v = mul2(v, mask[d][half]);
-                            store_p(c, 2 * b + d, half, v);
+                            for (int half = 0; half < 2; ++half) {
+                                uint64_t v = mul2(pack2(sc.x, sc.y), pack2(__uint_as_float(r[4 * d + 2 * half]), __uint_as_float(r[4 * d + 2 * half + 1])));
+                                if (b == q4) v = mul2(v, mask[d][half]);
+                                store_p(two, c, 2 * b + d, half, v);
+                            }
                         }
                     }
+                    announce_p(c);
                 }
-                announce_p(c);
-            }
-        } else {
-            for (int c = 0; c < n && !state_only; ++c) {
-                if (!wait_p(c)) break;
-                const float *ft = tab + TAB_F + (sp.c0 + c == special ? 64 : 0);
+            } else {
+                for (int c = 0; c < n && !state_only; ++c) {
+                    if (!wait_p(c)) break;
+                    const float *ft = tab + TAB_F + (sp.c0 + c == special ? 64 : 0);
 #pragma unroll 1
-                for (int k = 0; k < 8; ++k) {
-                    uint32_t r[4];
-                    tmem_ld16x256b_x1(t_lane + T_G + 64 * (c & 1) + 8 * k, r);
-                    tmem_wait_ld();
+                    for (int k = 0; k < 8; ++k) {
+                        uint32_t r[4];
+                        tmem_ld16x256b_x1(t_lane + T_G + 64 * (c & 1) + 8 * k, r);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int e = sgn * (i0 + 8 * half - 8 * k - 2 * t), e1 = e - sgn;
-                        const float f = 1.f / ft[i0 + 8 * half];
-                        store_p(c, k, half, pack2(e >= 0 ? f * tab[TAB_PW + e] * __uint_as_float(r[2 * half]) : 0.f,
-                                               e1 >= 0 ? f * tab[TAB_PW + e1] * __uint_as_float(r[2 * half + 1]) : 0.f));
+                        for (int half = 0; half < 2; ++half) {
+                            const int e = sgn * (i0 + 8 * half - 8 * k - 2 * t), e1 = e - sgn;
+                            const float f = 1.f / ft[i0 + 8 * half];
+                            store_p(two, c, k, half, pack2(e >= 0 ? f * tab[TAB_PW + e] * __uint_as_float(r[2 * half]) : 0.f,
+                                                   e1 >= 0 ? f * tab[TAB_PW + e1] * __uint_as_float(r[2 * half + 1]) : 0.f));
+                        }
                     }
+                    announce_p(c);
                 }
-                announce_p(c);
             }
-        }
+        };
+        if (NP != 1 && fine) rows_of_p(std::true_type{});
+        else rows_of_p(std::false_type{});
     } else {
         // ======================================================== O
         regs_dec<kRegsOut>();
@@ -809,6 +818,8 @@ cudaError_t launch_decay_walks_tc(const DecayWalks &d, cudaStream_t stream)
     cudaError_t err = cudaSuccess;
     if (w.nseg > 1) err = ends ? launch_tc<true, 3, 1>(p, stream) : launch_tc<true, 2, 1>(p, stream);
     if (err != cudaSuccess) return err;
+    // packed calls with more than a chunk of tokens hold sequences of both kinds
+    if (w.cu_seqlens && w.T > C) return ends ? launch_tc<false, 3, 0>(p, stream) : launch_tc<false, 2, 0>(p, stream);
     if (w.T <= C) return ends ? launch_tc<false, 3, 2>(p, stream) : launch_tc<false, 2, 2>(p, stream);
     return ends ? launch_tc<false, 3, 1>(p, stream) : launch_tc<false, 2, 1>(p, stream);
 }

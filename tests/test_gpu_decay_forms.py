@@ -1,5 +1,5 @@
 """Forms of the decay walk's calls: no end state with one chunk and with segments, packed calls of
-one chunk."""
+one chunk, short prompts packed against alone."""
 import numpy as np
 import pytest
 import torch
@@ -71,4 +71,17 @@ def test_packed_call_of_one_chunk(dtype, lengths, end):
             assert not end or torch.equal(SF[i].cpu(), d["S0"][i])
             continue
         check_forward(sequence(d, lengths, i), o[None, a:a + n], SF[i:i + 1] if end else None, f"sequence {i} of {n}")
+        a += n
+
+
+def test_a_short_prompt_packed_is_as_exact_as_alone():
+    """bf16: the scores of a sequence of one chunk have two pieces, whatever the call packs beside it."""
+    lengths = [64, 200, 1, 37, 63, 90, 5]
+    d = inputs((sum(lengths),), 2, 6, torch.bfloat16, 490, states=len(lengths))
+    o, SF = packed(d, lengths)
+    a = 0
+    for i, n in enumerate(lengths):
+        if n <= 64:
+            alone = forward(sequence(d, lengths, i))
+            assert torch.equal(o[None, a:a + n], alone[0]) and torch.equal(SF[i:i + 1], alone[1]), n
         a += n
