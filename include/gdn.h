@@ -438,8 +438,10 @@ gdn_status gdn_bwd_chunk(const void *q, const void *k, const void *v, const floa
  * Layouts, head map, ownership, streams and errors are those at the top of this
  * file; instead of alpha and beta there is
  *   decay     [Hv]     float, lambda_h itself (not its logarithm)
- * expected in (0, 1]; the kernels clamp log lambda below at -87.  The decay is a
- * constant of the layer: no gradient with respect to it is computed.
+ * expected in (0, 1]; the kernels clamp log lambda below at -87, so that 0 acts as
+ * exp(-87).  A negative or NaN decay makes the outputs, states and gradients of its
+ * head NaN.  The decay is a constant of the layer: no gradient with respect to it is
+ * computed.
  * A non-finite q, k or v makes the outputs of its whole chunk of 64 tokens (from
  * its sequence's start) undefined, and those after it; other sequences and heads
  * keep their values.

@@ -8,8 +8,13 @@ namespace gdn {
 namespace {
 
 // lambda^e for integer e >= 0, with log lambda >= -87; computed in 64 bits, because a
-// power is applied once per chunk and its relative error adds up over the chunks.
-__device__ __forceinline__ double decay_log(float lam) { return fmax(log((double)lam), -87.0); }
+// power is applied once per chunk and its relative error adds up over the chunks.  A negative or
+// NaN decay stays NaN.
+__device__ __forceinline__ double decay_log(float lam)
+{
+    const double l = log((double)lam);
+    return l < -87.0 ? -87.0 : l;
+}
 __device__ __forceinline__ double decay_pow(double loglam, double e) { return exp(e * loglam); }
 
 // The two launches of a segmented walk overlap: the first lets the second start as its CTAs

@@ -45,8 +45,7 @@ decay_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *_
     const size_t qk = ((size_t)b * Hqk + hq) * kHeadDim + tid;
     sk[tid] = to_f32(k[qk]);
     sq[tid] = to_f32(q[qk]);
-    // log lambda >= -87, as in the prefill
-    const float lam = fmaxf(decay[h], 1.6458114e-38f);
+    const float lam = clamped_decay(decay[h]);
     const size_t vo = (size_t)bh * kHeadDim + c0 + 4 * l8;
     const float v0 = to_f32(v[vo]), v1 = to_f32(v[vo + 1]), v2 = to_f32(v[vo + 2]), v3 = to_f32(v[vo + 3]);
     __syncthreads();

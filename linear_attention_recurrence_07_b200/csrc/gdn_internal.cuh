@@ -177,4 +177,9 @@ __device__ __forceinline__ float clamped_log(float alpha) {
     return fmaxf(logf(alpha), -87.0f);
 }
 
+// A head's decay with the same clamp; negative or NaN: NaN, which the head's results show.
+__device__ __forceinline__ float clamped_decay(float lam) {
+    return lam >= 0.f ? fmaxf(lam, 1.6458114e-38f) : __int_as_float(0x7fc00000);
+}
+
 }  // namespace gdn

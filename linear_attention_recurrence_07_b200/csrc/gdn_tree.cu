@@ -190,7 +190,8 @@ tree_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
             if (i < N) {
                 sm.jump[i] = p[x] < -1 || p[x] >= i ? -2 : p[x];
                 sm.mask[i] = 1ull << i;
-                sm.b[i] = (double)fmaxf(log2f(ga[x]), kLog2Clamp);
+                const float l = log2f(ga[x]);
+                sm.b[i] = (double)(DELTA ? fmaxf(l, kLog2Clamp) : l < kLog2Clamp ? kLog2Clamp : l);   // a bad decay stays NaN
                 sm.beta[i] = be[x];
             }
         }
@@ -520,7 +521,7 @@ commit_kernel(const T *__restrict__ k, const T *__restrict__ v, const float *__r
         for (int j = 0; j < kGroup; ++j) {
             const size_t node = (size_t)b * n + path[len - 1 - d0 - min(j, m - 1)];
             nk[j] = j < m ? to_f32(k[(node * Hqk + hq) * kHeadDim + tid]) : 0.f;
-            na[j] = j < m ? fmaxf(DELTA ? alpha[node * Hv + h] : decay[h], 1.6458114e-38f) : 1.f;
+            na[j] = j >= m ? 1.f : DELTA ? fmaxf(alpha[node * Hv + h], 1.6458114e-38f) : clamped_decay(decay[h]);
             nv[j] = nb[j] = 0.f;
             if (tid < kComCols) {
                 nv[j] = to_f32(v[(node * Hv + h) * kHeadDim + c0 + tid]);
