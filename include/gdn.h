@@ -530,6 +530,18 @@ gdn_status gdn_decay_bwd(const void *q, const void *k, const void *v, const floa
                          gdn_dtype dtype, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * gdn_set_decay_wait_limit -- how long any wait inside the tensor-core kernel of the
+ * CALLING THREAD's later gdn_decay_fwd, _varlen and _bwd calls (GDN_BF16) may take
+ * before it gives up, in microseconds; 0, the default, is two seconds.  (It is
+ * counted in tries of up to 20 us; below that a wait gives up at once.)  A wait that
+ * gives up ends its CTA, leaves the outputs undefined and is reported by
+ * gdn_device_status.  Negative: GDN_ERR_INVALID_ARG.  gdn_get_decay_wait_limit
+ * returns the calling thread's setting.
+ */
+gdn_status gdn_set_decay_wait_limit(long long microseconds);
+long long gdn_get_decay_wait_limit(void);
+
+/*
  * Verification of a TREE of drafted tokens over a pool of states, and the update
  * of the states along the accepted path.  gdn_decode_tokens checks a chain of
  * drafts; a tree checks several continuations in one pass, and reads each state

@@ -105,6 +105,10 @@ def library():
                 ("gdn_state_load", [vp] * 5 + [I] * 7 + [vp])):
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = I
+        lib.gdn_set_decay_wait_limit.argtypes = [ctypes.c_longlong]
+        lib.gdn_set_decay_wait_limit.restype = I
+        lib.gdn_get_decay_wait_limit.argtypes = []
+        lib.gdn_get_decay_wait_limit.restype = ctypes.c_longlong
         lib.gdn_device_status.argtypes = [vp]
         lib.gdn_device_status.restype = I
         lib.gdn_status_string.argtypes = [I]
@@ -637,6 +641,21 @@ def gdn_decay_bwd(q, k, v, decay, S0, dO, dS_final, dq, dk, dv, dS0, workspace=N
     _check(_call(dev, library().gdn_decay_bwd, *ptrs, B, T, Hqk, Hv, dkk, dvv, code, _ptr(workspace),
                  0 if workspace is None else workspace.numel(), _stream_handle(stream, dev)),
            "gdn_decay_bwd")
+
+
+@contextlib.contextmanager
+def decay_wait_limit(microseconds):
+    """Context manager: how long a wait inside this thread's bf16 decay prefill and
+    gradient kernels may take before it gives up (C entry point
+    ``gdn_set_decay_wait_limit``; 0 = the default of two seconds); the previous limit is
+    restored after the block."""
+    lib = library()
+    prev = lib.gdn_get_decay_wait_limit()
+    _check(lib.gdn_set_decay_wait_limit(int(microseconds)), "gdn_set_decay_wait_limit")
+    try:
+        yield
+    finally:
+        lib.gdn_set_decay_wait_limit(prev)
 
 
 def _tree_call(what, q, k, v, gates, parents, accepted, state_pool, slots, o, stream):

@@ -28,6 +28,11 @@ int sm_count()
     return sms;
 }
 
+// Microseconds that a wait inside a tensor-core walk may take (0: the default); see
+// gdn_set_decay_wait_limit.
+thread_local long long g_wait_limit = 0;
+constexpr long long kDefaultWait = 2000000;
+
 constexpr size_t kStateBytes = (size_t)gdn::kHeadDim * gdn::kHeadDim * sizeof(float);
 constexpr int kMaxDecaySegments = 16;
 
@@ -79,8 +84,10 @@ size_t segment_bytes(const DecayWalk &w)
     return w.nseg > 1 ? (size_t)w.B * w.nseg * w.Hv * kStateBytes : 0;
 }
 
-gdn_status run_walks(const gdn::DecayWalks &d, gdn_dtype dtype, cudaStream_t s)
+gdn_status run_walks(gdn::DecayWalks &d, gdn_dtype dtype, cudaStream_t s)
 {
+    const long long tries = (g_wait_limit > 0 ? g_wait_limit : kDefaultWait) / gdn::kWaitTryMicros;
+    d.wait_tries = (int)(tries < 0x7fffffff ? tries : 0x7fffffff);
     if (dtype == GDN_F32) return launch_status(gdn::launch_decay_walks_simt(d, s));
     if (!gdn::chunk_tc_available()) return GDN_ERR_UNSUPPORTED;
     return launch_status(gdn::launch_decay_walks_tc(d, s));
@@ -199,6 +206,15 @@ gdn_status check_cache(const void *pool, const int *slots, const void *codes, co
 }  // namespace
 
 extern "C" {
+
+gdn_status gdn_set_decay_wait_limit(long long microseconds)
+{
+    if (microseconds < 0) return GDN_ERR_INVALID_ARG;
+    g_wait_limit = microseconds;
+    return GDN_OK;
+}
+
+long long gdn_get_decay_wait_limit(void) { return g_wait_limit; }
 
 size_t gdn_decay_fwd_workspace(int B, int T, int Hv, int dk, int dv, gdn_dtype dtype)
 {

@@ -114,14 +114,16 @@ template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setm
 struct DecayCtl {
     uint64_t *bar;
     volatile int *abort_flag;
+    const DecayWalks &d;
     // One thread.  (Inlined and short: a call would not let ptxas give the roles their own
-    // register counts, and the loops of all roles share the instruction cache.)  A try
-    // suspends for up to 20 us, so the limit is about two seconds.
+    // register counts, and the loops of all roles share the instruction cache; a limit in clocks
+    // cost 4% of a long prefill.)  The second of two launches may count against its limit what the
+    // first has left, at most the walk of a segment.
     __device__ __forceinline__ bool wait_one(int i, uint32_t parity) const {
         bool got = mbar_try_wait(&bar[i], parity);
 #pragma unroll 1
-        for (int k = 100000; !got && k > 0; --k) {
-            got = mbar_try_wait_suspend(&bar[i], parity, 20000);
+        for (int k = d.wait_tries; !got && k > 0; --k) {
+            got = mbar_try_wait_suspend(&bar[i], parity, kWaitTryMicros * 1000);
             if (*abort_flag) k = 0;
         }
         if (!got) *abort_flag = 1;
@@ -183,7 +185,7 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + DOFF_MISC + 4);
     float *tab = reinterpret_cast<float *>(sm + DOFF_TAB);
     float *seg_decay = reinterpret_cast<float *>(sm + DOFF_O);       // read before any O
-    const DecayCtl ctl{bar, abort_flag};
+    const DecayCtl ctl{bar, abort_flag, p.d};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x;
     const WalkSpan sp = walk_span(w, blockIdx.y, FIRST);

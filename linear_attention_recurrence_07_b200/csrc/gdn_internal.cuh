@@ -110,7 +110,9 @@ struct DecayWalks {
     DecayWalk w[kMaxWalks];
     int n;
     bool wide;      // CUDA cores: one CTA per head instead of four
+    int wait_tries; // tensor cores: tries, of up to kWaitTryMicros each, before a wait gives up
 };
+constexpr int kWaitTryMicros = 20;
 cudaError_t launch_decay_walks_simt(const DecayWalks &d, cudaStream_t stream);
 cudaError_t launch_decay_walks_tc(const DecayWalks &d, cudaStream_t stream);   // bf16 operands
 cudaError_t decay_tc_take_error(unsigned *out);
