@@ -533,8 +533,8 @@ gdn_status gdn_decay_bwd(const void *q, const void *k, const void *v, const floa
  * gdn_set_decay_wait_limit -- how long any wait inside the tensor-core kernel of the
  * CALLING THREAD's later gdn_decay_fwd, _varlen and _bwd calls (GDN_BF16) may take
  * before it gives up, in microseconds; 0, the default, is two seconds.  (It is
- * counted in tries of up to 20 us; below that a wait gives up at once.)  A wait that
- * gives up ends its CTA, leaves the outputs undefined and is reported by
+ * counted in tries of up to 20 us, after a first one of the hardware's own length.)
+ * A wait that gives up ends its CTA, leaves the outputs undefined and is reported by
  * gdn_device_status.  Negative: GDN_ERR_INVALID_ARG.  gdn_get_decay_wait_limit
  * returns the calling thread's setting.
  */

@@ -292,10 +292,11 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
                 if (!ctl.wait_one(D_EMPTY + c % kStages, ((c / kStages) - 1) & 1)) break;
                 load_stage(c);
             }
-            // On an abort, copies still in flight land before the CTA's memory goes away.
-            if (*abort_flag)
-                for (int i = max(0, c - kStages); i < c; ++i)
-                    mbar_wait(&bar[D_FULL + i % kStages], (i / kStages) & 1, 1ll << 28);
+            // Copies in flight land before the CTA's memory goes away.  (Another role may give up after
+            // the last copy is issued, so this does not ask whether one has.)
+#pragma unroll 1
+            for (int i = max(0, c - kStages); i < c; ++i)
+                mbar_wait(&bar[D_FULL + i % kStages], (i / kStages) & 1, 1ll << 28);
         }
         if (warp == 1) {
             // ==================================================== MMA issuer: D
