@@ -260,16 +260,18 @@ decay_tc_kernel(const __grid_constant__ TcWalks p)
             }
             tab[at] = (float)(centre * decay_pow(loglam, e));
         }
-        if (ti < 18 && ti >= 2) {    // decay of segment ti - 2's start state up to this segment
-            const int g = ti - 2, here = tokens_before(sp, w.rev, sp.c0);
+        // threads with one entry of the tables
+        if (ti >= 288 && ti < 304) { // decay of a segment's start state up to this segment
+            const int g = ti - 288, here = tokens_before(sp, w.rev, sp.c0);
             if (w.nseg > 1 && g <= sp.seg)
                 seg_decay[g] = (float)decay_pow(loglam, here - tokens_before(sp, w.rev, segment_start(w, g)));
-        } else if (ti < 2) {         // lambda^L of full chunks and of the special one, in two floats
-            const double p = decay_pow(loglam, ti ? tail - back : C);
-            tab[TAB_L + 2 * ti] = (float)p;
-            tab[TAB_L + 2 * ti + 1] = (float)(p - (double)(float)p);
+        } else if (ti >= 304 && ti < 306) {    // lambda^L of full chunks and of the special one, in two floats
+            const int last = ti - 304;
+            const double p = decay_pow(loglam, last ? tail - back : C);
+            tab[TAB_L + 2 * last] = (float)p;
+            tab[TAB_L + 2 * last + 1] = (float)(p - (double)(float)p);
             // the walk's ends: segments' states stay centred, and with no tokens the state passes as it is
-            tab[TAB_L + 4 + ti] = sp.L == 0 ? 1.f : ti ? (FIRST ? 1.f : (float)up) : (float)((w.init_decays ? decay_pow(loglam, 1.0) : 1.0) * down);
+            tab[TAB_L + 4 + last] = sp.L == 0 ? 1.f : last ? (FIRST ? 1.f : (float)up) : (float)((w.init_decays ? decay_pow(loglam, 1.0) : 1.0) * down);
         }
     }
     tc_fence_before();
