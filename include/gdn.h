@@ -437,7 +437,8 @@ gdn_status gdn_bwd_chunk(const void *q, const void *k, const void *v, const floa
  *
  * Layouts, head map, ownership, streams and errors are those at the top of this
  * file; instead of alpha and beta there is
- *   decay     [Hv]     float, lambda_h itself (not its logarithm)
+ *   decay     [Hv]     float, lambda_h itself (not its logarithm), 16-byte
+ *                      aligned too: rows of a [layers, Hv] table need Hv % 4 == 0
  * expected in (0, 1]; the kernels clamp log lambda below at -87, so that 0 acts as
  * exp(-87).  A negative or NaN decay makes the outputs, states and gradients of its
  * head NaN.  The decay is a constant of the layer: no gradient with respect to it is
@@ -455,7 +456,8 @@ gdn_status gdn_bwd_chunk(const void *q, const void *k, const void *v, const floa
  * Out: o [B, T, Hv, dv]; S_final [B, Hv, dk, dv] or NULL (may be S0).
  * dtype: GDN_F32 computes in fp32 on CUDA cores; GDN_BF16 on the tensor cores
  *      with an fp32 state: v's decayed copies enter its update in three bf16
- *      pieces (the 24 bits of an fp32), so S_final carries fp32 accuracy; where o
+ *      pieces (the 24 bits of an fp32), so S_final carries fp32 accuracy (in two
+ *      pieces, 16 bits, where the call wants no end state); where o
  *      reads it, the state is rounded to bf16, and so are the decayed scores
  *      (two pieces of 16 bits in all for sequences of at most 64 tokens, packed or not).
  *      Scores (a row of q with one of k) and the sums of a row may reach 2^66: a chunk's

@@ -17,9 +17,10 @@
 // sums.  Narrow: 32 columns, two CTAs per SM; the score tile is computed four times, but
 // short prompts of few heads still spread over the device.
 //
-// Bound by fp32 arithmetic: 1.8 M multiply-adds per chunk and head (wide), 14,400 cycles of
-// an SM; measured 17 us, of which shared-memory operands and the phases' barriers take the
-// rest.  48 heads, T=512: 120 us; gradients of B=2, T=206: 202 us (narrow: 369).
+// Bound by fp32 arithmetic: 2.9 M multiply-adds per chunk and head (wide: scores 0.5, H's share
+// 1.05, P z 0.3, the state's update 1.05), 22,800 cycles of an SM or 12 us; measured 24 us (144
+// heads, one CTA on each SM), of which shared-memory operands and the phases' barriers take the
+// rest.  48 heads, T=512: 119 us; gradients of B=2, T=206: 207 us (narrow: 369).
 #include "decay_common.cuh"
 
 namespace gdn {

@@ -36,9 +36,9 @@
 //   warps 12-15 G -> P (shared memory)
 //   warps 16-19 O epilogue (stmatrix, TMA store)
 //
-// Measured: 16 QK / 48 V heads, B=8, T=8192: 0.65-0.68 ms, 3.3 TB/s (half of the copy
+// Measured: 16 QK / 48 V heads, B=8, T=8192: 0.67-0.69 ms, 3.3 TB/s (half of the copy
 // bandwidth), 300 TF/s of the recurrence's own arithmetic; B=1, T=4096: 64 us (a head and
-// three segments); gradients at 48 heads, T=4096: 124-131 us.  A chunk takes 2400 to 2700
+// three segments); gradients at 48 heads, T=4096: 129-132 us.  A chunk takes 2400 to 2700
 // cycles per SM (the clock settles at 1.65 GHz under this load).  No single unit bounds it: the
 // chain from D through the state's registers to the next D (pieces of Z 1100, reading D 550, H
 // 280 cycles of its two warpgroups, and D itself), the tensor core 57-65% of the time (65 cycles

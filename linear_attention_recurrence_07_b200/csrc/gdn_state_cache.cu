@@ -7,7 +7,7 @@
 // Pure HBM stream: 640 bytes and a scale per row against a few instructions per
 // value.  The quotients are per row, correctly rounded, and the codes one product
 // and one rounding per value, so that codes are reproducible bit for bit.
-// Storing 64 sequences of 48 heads: 42 us, 6.0 TB/s; loading 24: 18 us, 5.2 TB/s.
+// Storing 64 sequences of 48 heads: 43 us, 5.9 TB/s; loading 24: 18 us, 5.2 TB/s.
 #include <cuda_fp8.h>
 
 #include "gdn_internal.cuh"
@@ -17,7 +17,8 @@ namespace {
 
 constexpr int kCacheThreads = 256;
 // Rows in flight per warp (a CTA takes eight times as many).  64 sequences of 48 heads, 2 / 4 / 8
-// rows: store 41 / 36 / 34 us, load 40 / 40 / 41 us; 24 of them: store 15 / 13 / 13, load 15 / 14 / 15.
+// rows, inputs not in L2: store 46 / 42 / 42 us, load 42 / 42 / 43 us; 24 of them: store 20 / 19 / 19,
+// load 19 / 19 / 19.
 constexpr int kStoreRows = 8, kLoadRows = 4;
 constexpr float kTinyRow = 1e-30f;
 
