@@ -207,7 +207,8 @@ gdn_status gdn_chunk_fwd_pipelined(const void *q, const void *k, const void *v,
 
 /*
  * gdn_device_status -- waits for `stream`, then reports and clears the device
- * error words of the tensor-core prefill kernels.  Returns GDN_ERR_TIMEOUT if a
+ * error words of the tensor-core prefill kernels and of the decay rule's tensor-core
+ * kernel (prefill and gradients).  Returns GDN_ERR_TIMEOUT if a
  * bounded wait inside any of them gave up since the last call (on any stream:
  * the words are per library, not per call), GDN_ERR_CUDA if the stream reports
  * an error, else GDN_OK.  The kernels never trap or hang: a wait that gives up

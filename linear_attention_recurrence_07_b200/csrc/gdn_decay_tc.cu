@@ -41,7 +41,7 @@
 // three segments); gradients at 48 heads, T=4096: 129-132 us.  A chunk takes 2400 to 2700
 // cycles per SM (the clock settles at 1.65 GHz under this load).  No single unit bounds it: the
 // chain from D through the state's registers to the next D (pieces of Z 1100, reading D 550, H
-// 280 cycles of its two warpgroups, and D itself), the tensor core 57-65% of the time (65 cycles
+// 280 cycles of its two warpgroups, and D itself), the tensor core 55-65% of the time (65 cycles
 // per 128 x 128 x 16 MMA make 780 for D; H X 270, Z P 200, G 280), shared memory 70%.  Giving Z'
 // warps of its own, Z' or O a second buffer, or Z P a place before H X was no faster: what runs
 // earlier takes the tensor core from D.
