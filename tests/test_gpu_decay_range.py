@@ -16,7 +16,7 @@ def scaled(d, **exps):
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
 @pytest.mark.parametrize("T", [64, 150, 1130])
-@pytest.mark.parametrize("eq,ek,ev", [(14, 14, 2), (16, 16, 0), (0, 0, 30), (20, 20, 24), (-14, -14, 0), (-16, 20, -20), (-24, -24, 4)])
+@pytest.mark.parametrize("eq,ek,ev", [(14, 14, 2), (16, 16, 0), (0, 0, 30), (20, 20, 24), (-14, -14, 0), (-16, 20, -20), (-24, -24, 4), (24, -36, -26)])
 def test_prefill(dtype, T, eq, ek, ev):
     d = scaled(inputs((1, T), 1, 8, dtype, 400 + T), q=eq, k=ek, v=ev, S0=ek + ev)
     d["decay"] = STRONG
